@@ -66,6 +66,40 @@ class LinkCeilings(ctypes.Structure):
                 ("h2d_copy_gbps", ctypes.c_double)]
 
 
+class RmsNormArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("act_dtype", ctypes.c_int32),
+                ("add_dtype", ctypes.c_int32), ("eps", ctypes.c_float), ("x", ctypes.c_void_p),
+                ("ld_x", ctypes.c_int64), ("add", ctypes.c_void_p), ("ld_add", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("x_out", ctypes.c_void_p), ("ld_x_out", ctypes.c_int64),
+                ("out", ctypes.c_void_p), ("ld_out", ctypes.c_int64), ("q_out", ctypes.c_void_p),
+                ("ld_q", ctypes.c_int64), ("s_out", ctypes.c_void_p)]
+
+
+class QuantizeArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("act_dtype", ctypes.c_int32), ("x", ctypes.c_void_p),
+                ("ld_x", ctypes.c_int64), ("q_out", ctypes.c_void_p), ("ld_q", ctypes.c_int64),
+                ("s_out", ctypes.c_void_p)]
+
+
+class Int8MatmulArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("q_x", ctypes.c_void_p), ("ld_x", ctypes.c_int64), ("s_x", ctypes.c_void_p),
+                ("q_w", ctypes.c_void_p), ("ld_w", ctypes.c_int64), ("s_w", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("y_in", ctypes.c_void_p), ("ld_y", ctypes.c_int64),
+                ("res", ctypes.c_void_p), ("ld_res", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("ld_out", ctypes.c_int64)]
+
+
+class Int8FfnArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("I", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("q_x", ctypes.c_void_p), ("ld_x", ctypes.c_int64), ("s_x", ctypes.c_void_p),
+                ("q_gu", ctypes.c_void_p), ("ld_gu", ctypes.c_int64), ("s_gu", ctypes.c_void_p),
+                ("q_dn", ctypes.c_void_p), ("ld_dn", ctypes.c_int64), ("s_dn", ctypes.c_void_p),
+                ("y_in", ctypes.c_void_p), ("ld_y", ctypes.c_int64), ("res", ctypes.c_void_p),
+                ("ld_res", ctypes.c_int64), ("out", ctypes.c_void_p), ("ld_out", ctypes.c_int64),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
 KERNELS = ["router", "route", "gateup", "down", "combine", "gemm_gateup", "gemm_down", "stage"]
 
 
@@ -119,6 +153,11 @@ def load_library(path: str = LIB_PATH, with_torch: bool = True):
     lib.moe_plan_residency.argtypes = [vp, i32, vp]
     lib.moe_plan_profile.argtypes = [vp, i32]
     lib.moe_plan_kernel_times.argtypes = [vp, ctypes.POINTER(KernelTimes)]
+    lib.moe_rms_norm.argtypes = [ctypes.POINTER(RmsNormArgs), vp]
+    lib.moe_quantize_rows.argtypes = [ctypes.POINTER(QuantizeArgs), vp]
+    lib.moe_int8_matmul.argtypes = [ctypes.POINTER(Int8MatmulArgs), vp]
+    lib.moe_int8_ffn_workspace.argtypes = [i32, i32, i32, ctypes.POINTER(ctypes.c_size_t)]
+    lib.moe_int8_ffn.argtypes = [ctypes.POINTER(Int8FfnArgs), vp]
     lib.moe_plan_destroy.argtypes = [vp]
     lib.moe_plan_destroy.restype = None
     lib.moe_status_str.argtypes = [st]
@@ -129,7 +168,8 @@ def load_library(path: str = LIB_PATH, with_torch: bool = True):
                "moe_cache_update", "moe_plan_stats", "moe_plan_reset_stats", "moe_plan_residency",
                "moe_plan_profile", "moe_plan_kernel_times", "moe_plan_get_info", "moe_measure_link_ceilings",
                "moe_debug_fail_alloc", "moe_debug_live_allocs", "moe_plan_set_host_compute",
-               "moe_prefetch", "moe_plan_prefetch_slots"):
+               "moe_prefetch", "moe_plan_prefetch_slots", "moe_rms_norm", "moe_quantize_rows", "moe_int8_matmul",
+               "moe_int8_ffn_workspace", "moe_int8_ffn"):
         getattr(lib, fn).restype = st
     _lib = lib
     return lib
@@ -202,6 +242,158 @@ def _layer_weights(router_w, router_b, experts):
     rb = None if router_b is None else np.ascontiguousarray(router_b, dtype=np.float32)
     ex = np.ascontiguousarray(experts, dtype=np.uint8)
     return LayerWeights(_ptr(rw), _ptr(rb), _ptr(ex)), (rw, rb, ex)
+
+
+# ---- dense operators beside the routed layer
+#
+# Tensors are on one GPU, matrices two-dimensional with consecutive elements in a row
+# (any row stride), vectors packed. The work runs on `stream` (default: torch's current
+# stream of that GPU); the GPU need not be the current one.
+
+
+def _refuse(fn, msg):
+    raise MoeError(MOE_E_INVALID, fn, msg)
+
+
+class _Operands:
+    """The tensors of one call: checks each against what the operator takes, collects the
+    device they share."""
+
+    def __init__(self, fn):
+        self.fn, self.device = fn, None
+
+    def _tensor(self, name, t, dtypes):
+        if t.dtype not in dtypes:
+            _refuse(self.fn, "%s has dtype %s" % (name, t.dtype))
+        d = t.get_device()
+        if d < 0:
+            _refuse(self.fn, "%s is not on a GPU" % name)
+        if self.device is None:
+            self.device = d
+        elif d != self.device:
+            _refuse(self.fn, "%s is on another GPU than the other tensors" % name)
+
+    def mat(self, name, t, rows, cols, *dtypes):
+        """(address, row stride) of a matrix, (None, 0) for None."""
+        if t is None:
+            return None, 0
+        self._tensor(name, t, dtypes)
+        if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+            _refuse(self.fn, "%s has shape %s, not (%d, %d)" % (name, tuple(t.shape), rows, cols))
+        if t.stride(1) != 1 and cols > 1:
+            _refuse(self.fn, "%s: the elements of a row are not consecutive" % name)
+        # a single row's stride says nothing (and may be less than its length)
+        return t.data_ptr(), t.stride(0) if rows > 1 else cols
+
+    def vec(self, name, t, n, *dtypes):
+        """Address of a packed vector, None for None."""
+        if t is None:
+            return None
+        self._tensor(name, t, dtypes)
+        if t.dim() != 1 or t.shape[0] != n:
+            _refuse(self.fn, "%s has shape %s, not (%d,)" % (name, tuple(t.shape), n))
+        if t.stride(0) != 1 and n > 1:
+            _refuse(self.fn, "%s is not packed" % name)
+        return t.data_ptr()
+
+    def call(self, args, stream):
+        import torch
+        fn = getattr(load_library(), self.fn)
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        if self.device == torch.cuda.current_device():
+            _check(fn(ctypes.byref(args), _stream(stream)), self.fn)
+        else:
+            with torch.cuda.device(self.device):
+                _check(fn(ctypes.byref(args), _stream(stream)), self.fn)
+
+
+def _act_of(fn, name, t):
+    """moe_act_dtype of a tensor, and its torch dtype."""
+    import torch
+    if t.dtype == torch.bfloat16:
+        return ACT_BF16
+    if t.dtype == torch.float32:
+        return ACT_F32
+    _refuse(fn, "%s has dtype %s, not bfloat16 or float32" % (name, t.dtype))
+
+
+def _shape2(fn, name, t):
+    if t.dim() != 2:
+        _refuse(fn, "%s has %d dimensions, not 2" % (name, t.dim()))
+    return t.shape
+
+
+def rms_norm(x, weight, eps=1e-6, add=None, x_out=None, out=None, q_out=None, s_out=None, stream=None):
+    """Root-mean-square norm of s = x + add (add: x's dtype, or float32 such as forward()'s y):
+    x_out = s rounded to x's dtype, out = the norm in x's dtype, q_out int8 [T, H] and s_out
+    float32 [T] = its codes and scales; any of the outputs may be None (moe_rms_norm)."""
+    import torch
+    fn = "moe_rms_norm"
+    T, H = _shape2(fn, "x", x)
+    act, ad = _act_of(fn, "x", x), ACT_F32 if add is None else _act_of(fn, "add", add)
+    o = _Operands(fn)
+    dt = x.dtype
+    a = RmsNormArgs(T, H, act, ad, eps, *o.mat("x", x, T, H, dt), *o.mat("add", add, T, H, dt, torch.float32),
+                    o.vec("weight", weight, H, dt), *o.mat("x_out", x_out, T, H, dt), *o.mat("out", out, T, H, dt),
+                    *o.mat("q_out", q_out, T, H, torch.int8), o.vec("s_out", s_out, T, torch.float32))
+    o.call(a, stream)
+
+
+def quantize_rows(x, q_out, s_out, stream=None):
+    """int8 codes q_out [T, H] and float32 scales s_out [T] of the rows of x [T, H]
+    (moe_quantize_rows): activations, or a weight matrix, whose rows are its channels."""
+    import torch
+    fn = "moe_quantize_rows"
+    T, H = _shape2(fn, "x", x)
+    o = _Operands(fn)
+    a = QuantizeArgs(T, H, _act_of(fn, "x", x), *o.mat("x", x, T, H, x.dtype),
+                     *o.mat("q_out", q_out, T, H, torch.int8), o.vec("s_out", s_out, T, torch.float32))
+    o.call(a, stream)
+
+
+def int8_matmul(q_x, s_x, q_w, s_w, out, bias=None, y_in=None, res=None, stream=None):
+    """out [T, N] = act(s_x s_w (q_x @ q_w.T) + bias + y_in + res), q_x int8 [T, K], q_w int8
+    [N, K]; bias float32 [N], y_in float32 [T, N], res in out's dtype; out may be y_in or
+    res (moe_int8_matmul)."""
+    import torch
+    fn = "moe_int8_matmul"
+    (T, K), N = _shape2(fn, "q_x", q_x), _shape2(fn, "q_w", q_w)[0]
+    o = _Operands(fn)
+    f32, i8 = torch.float32, torch.int8
+    a = Int8MatmulArgs(T, N, K, _act_of(fn, "out", out), *o.mat("q_x", q_x, T, K, i8), o.vec("s_x", s_x, T, f32),
+                       *o.mat("q_w", q_w, N, K, i8), o.vec("s_w", s_w, N, f32), o.vec("bias", bias, N, f32),
+                       *o.mat("y_in", y_in, T, N, f32), *o.mat("res", res, T, N, out.dtype),
+                       *o.mat("out", out, T, N, out.dtype))
+    o.call(a, stream)
+    return out
+
+
+def int8_ffn_workspace(T, H, I) -> int:
+    """Bytes of workspace that int8_ffn needs for T tokens (moe_int8_ffn_workspace)."""
+    lib = load_library()
+    n = ctypes.c_size_t()
+    _check(lib.moe_int8_ffn_workspace(T, H, I, ctypes.byref(n)), "moe_int8_ffn_workspace")
+    return int(n.value)
+
+
+def int8_ffn(q_x, s_x, q_gu, s_gu, q_dn, s_dn, out, workspace, y_in=None, res=None, stream=None):
+    """Gated feed-forward block on 8-bit codes: q_x int8 [T, H], q_gu int8 [2I, H] (gate rows,
+    then up rows), q_dn int8 [H, I]; out [T, H] = act(block + y_in + res). workspace: a uint8
+    tensor of int8_ffn_workspace(T, H, I) bytes, one for each call in flight (moe_int8_ffn)."""
+    import torch
+    fn = "moe_int8_ffn"
+    (T, H), I = _shape2(fn, "q_x", q_x), _shape2(fn, "q_dn", q_dn)[1]
+    o = _Operands(fn)
+    f32, i8 = torch.float32, torch.int8
+    a = Int8FfnArgs(T, H, I, _act_of(fn, "out", out), *o.mat("q_x", q_x, T, H, i8), o.vec("s_x", s_x, T, f32),
+                    *o.mat("q_gu", q_gu, 2 * I, H, i8), o.vec("s_gu", s_gu, 2 * I, f32),
+                    *o.mat("q_dn", q_dn, H, I, i8), o.vec("s_dn", s_dn, H, f32),
+                    *o.mat("y_in", y_in, T, H, f32), *o.mat("res", res, T, H, out.dtype),
+                    *o.mat("out", out, T, H, out.dtype),
+                    o.vec("workspace", workspace, workspace.numel(), torch.uint8), workspace.numel())
+    o.call(a, stream)
+    return out
 
 
 class Plan:

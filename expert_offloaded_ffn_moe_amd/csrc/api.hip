@@ -26,6 +26,7 @@
 #include <type_traits>
 #include <vector>
 
+#include "dense.h"
 #include "host_ffn.h"
 #include "host_logic.h"
 #include "kernels.h"
@@ -127,6 +128,14 @@ struct Workspace {
 };
 
 }  // namespace
+
+moe_status moe::report_error(moe_status s, const char* msg) noexcept {
+  try {
+    g_last_error = msg;
+  } catch (...) {  // no memory for the message: the status alone is returned
+  }
+  return s;
+}
 
 struct moe_plan {
   moe_config cfg{};

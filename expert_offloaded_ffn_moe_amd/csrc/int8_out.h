@@ -1,0 +1,55 @@
+// The epilogue that the 8-bit matrix products share, and their lane layouts.
+//
+// A product's sum over K is exact in int32 (K <= 131056 codes of -128..127), so it
+// does not depend on how K is split over lanes, waves or tiles. The scales, the bias
+// and what is added multiply and add in fp32; the output is rounded once.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "dense.h"
+
+namespace moe {
+
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(1))) const i32x4 gi32x4;
+
+// act(v) as stored: fp32, or bf16 to nearest even with a NaN kept one
+template <bool BF16>
+struct OutElem;
+template <>
+struct OutElem<false> {
+  typedef float T;
+  static __device__ __forceinline__ float load(float v) { return v; }
+  static __device__ __forceinline__ float rounded(float v) { return v; }
+};
+template <>
+struct OutElem<true> {
+  typedef uint16_t T;
+  static __device__ __forceinline__ float load(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+  static __device__ __forceinline__ uint16_t rounded(float f) {
+    const uint32_t u = __float_as_uint(f);
+    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (uint16_t)((u >> 16) | 0x40u);
+    return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
+  }
+};
+
+// out[t][n] of the product whose sum is `acc`
+template <bool BF16>
+__device__ __forceinline__ void int8_store(const Int8Out& o, int t, int n, float sx, float sw, int acc) {
+  typedef typename OutElem<BF16>::T E;
+  float v = (float)acc * sx * sw;
+  if (o.bias) v += o.bias[n];
+  if (o.y) v += o.y[t * o.ld_y + n];
+  if (o.res) v += OutElem<BF16>::load(static_cast<const E*>(o.res)[t * o.ld_res + n]);
+  static_cast<E*>(o.out)[t * o.ld_out + n] = OutElem<BF16>::rounded(v);
+}
+
+// silu(g) u, each from its exact sum; exp(-g) past fp32's range gives the limit 0
+__device__ __forceinline__ float gated_value(int g_acc, int u_acc, float sx, float sg, float su) {
+  const float g = (float)g_acc * sx * sg, u = (float)u_acc * sx * su;
+  return g / (1.f + __expf(-g)) * u;
+}
+
+}  // namespace moe

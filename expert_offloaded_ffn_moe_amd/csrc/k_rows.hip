@@ -1,0 +1,350 @@
+// Row kernels: root-mean-square norm with the residual's addition, and the 8-bit
+// codes of a row.
+//
+//   s_j = act(x_j + r_j),  p_j = s_j g_j,  n_j = p_j / sqrt(mean(s^2) + eps)
+//   code_j = round half even(127 p_j / max|p|),  scale = max|p| / (127 sqrt(mean(s^2) + eps))
+//
+// The row's root mean square divides every n_j alike, so the codes are those of p and
+// do not depend on its rounding. With bf16 activations p (8 x 8 bits of mantissa) and
+// 127 p (23 bits) are exact in fp32, and the quotient is rounded correctly by Markstein's
+// two-step correction of a product with a correctly rounded reciprocal (IBM J. Res.
+// Dev. 34, 1990): a code differs from the definition's only where the quotient's own fp32
+// rounding reaches a half, which it cannot (the quotient is either k + 1/2 or at least
+// 2^-17 from it at |code| >= 64, less below in step with the spacing of fp32). With fp32
+// activations the same steps run in fp64. mean(s^2) is summed in fp64: squares of large
+// activations would leave fp32's range.
+//
+// One pass: a row is held in registers between the sums and the outputs, so each input
+// is read once and each output written once. The bound is the bytes, and for a few rows
+// the latency of a load, two reductions and a store.
+#include <hip/hip_runtime.h>
+
+#include "dense.h"
+#include "wave.h"
+
+namespace moe {
+namespace {
+
+constexpr int kChunk = 8;  // elements of a row that a thread takes at a time
+
+// Rows may start at any element: 16-byte accesses at the element's alignment, which
+// gfx950 performs as one access.
+struct __attribute__((packed, aligned(2))) Bf16x8 {
+  uint32_t v[4];
+};
+struct __attribute__((packed, aligned(4))) F32x4 {
+  float v[4];
+};
+struct __attribute__((packed, aligned(1))) I8x8 {
+  uint32_t v[2];
+};
+
+__device__ __forceinline__ float bf16_value(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+
+// round to nearest even; a NaN stays one
+__device__ __forceinline__ uint16_t to_bf16(float f) {
+  const uint32_t u = __float_as_uint(f);
+  if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (uint16_t)((u >> 16) | 0x40u);
+  return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
+}
+
+__device__ __forceinline__ void load8(const uint16_t* p, int n, float* v) {
+  if (n >= kChunk) {
+    const Bf16x8 w = *reinterpret_cast<const Bf16x8*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w.v[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w.v[i] & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) v[i] = i < n ? bf16_value(p[i]) : 0.f;
+  }
+}
+
+__device__ __forceinline__ void load8(const float* p, int n, float* v) {
+  if (n >= kChunk) {
+    const F32x4 a = reinterpret_cast<const F32x4*>(p)[0], b = reinterpret_cast<const F32x4*>(p)[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = a.v[i];
+      v[4 + i] = b.v[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) v[i] = i < n ? p[i] : 0.f;
+  }
+}
+
+__device__ __forceinline__ void store8(uint16_t* p, int n, const float* v) {
+  if (n >= kChunk) {
+    Bf16x8 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w.v[i] = (uint32_t)to_bf16(v[2 * i]) | (uint32_t)to_bf16(v[2 * i + 1]) << 16;
+    *reinterpret_cast<Bf16x8*>(p) = w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i)
+      if (i < n) p[i] = to_bf16(v[i]);
+  }
+}
+
+__device__ __forceinline__ void store8(float* p, int n, const float* v) {
+  if (n >= kChunk) {
+    F32x4 a, b;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a.v[i] = v[i];
+      b.v[i] = v[4 + i];
+    }
+    reinterpret_cast<F32x4*>(p)[0] = a;
+    reinterpret_cast<F32x4*>(p)[1] = b;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i)
+      if (i < n) p[i] = v[i];
+  }
+}
+
+template <typename ACT>
+struct Act;
+template <>
+struct Act<uint16_t> {
+  typedef float P;  // the type of p, its largest size and the quotient
+  static __device__ __forceinline__ float rounded(float f) { return bf16_value(to_bf16(f)); }
+};
+template <>
+struct Act<float> {
+  typedef double P;
+  static __device__ __forceinline__ float rounded(float f) { return f; }
+};
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dppd(double v) {  // a lane left out of ROWS keeps 0
+  const uint64_t u = __double_as_longlong(v);
+  const uint32_t lo = dpp<CTRL, ROWS>(0, (int)(uint32_t)u), hi = dpp<CTRL, ROWS>(0, (int)(uint32_t)(u >> 32));
+  return __longlong_as_double((int64_t)((uint64_t)hi << 32 | lo));
+}
+
+__device__ __forceinline__ double lane63(double v) {
+  const uint64_t u = __double_as_longlong(v);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, 63);
+  const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
+  return __longlong_as_double((int64_t)((uint64_t)hi << 32 | lo));
+}
+
+__device__ __forceinline__ double wave_sum(double v) {
+  v += dppd<kDppXor1, 0xF>(v);
+  v += dppd<kDppXor2, 0xF>(v);
+  v += dppd<kDppHalfMirror, 0xF>(v);
+  v += dppd<kDppMirror, 0xF>(v);
+  v += dppd<kDppBcast15, 0xA>(v);
+  v += dppd<kDppBcast31, 0xC>(v);
+  return lane63(v);
+}
+
+// largest of non-negative values (a lane left out contributes 0)
+__device__ __forceinline__ double wave_max_pos(double v) {
+  v = fmax(v, dppd<kDppXor1, 0xF>(v));
+  v = fmax(v, dppd<kDppXor2, 0xF>(v));
+  v = fmax(v, dppd<kDppHalfMirror, 0xF>(v));
+  v = fmax(v, dppd<kDppMirror, 0xF>(v));
+  v = fmax(v, dppd<kDppBcast15, 0xA>(v));
+  v = fmax(v, dppd<kDppBcast31, 0xC>(v));
+  return lane63(v);
+}
+
+__device__ __forceinline__ uint32_t wave_max_u(uint32_t v) {
+  v = max(v, (uint32_t)dpp<kDppXor1, 0xF>(0, (int)v));
+  v = max(v, (uint32_t)dpp<kDppXor2, 0xF>(0, (int)v));
+  v = max(v, (uint32_t)dpp<kDppHalfMirror, 0xF>(0, (int)v));
+  v = max(v, (uint32_t)dpp<kDppMirror, 0xF>(0, (int)v));
+  v = max(v, (uint32_t)dpp<kDppBcast15, 0xA>(0, (int)v));
+  v = max(v, (uint32_t)dpp<kDppBcast31, 0xC>(0, (int)v));
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float f) { return __float_as_uint(f) & 0x7FFFFFFFu; }
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// Codes under the row's largest size: a = 127 p 2^(1-e) and b = max|p| 2^(1-e) in [2, 4), so
+// that nothing over- or underflows; q = a y, corrected once, is a / b rounded correctly.
+// Adding 1.5 2^23 (2^52) rounds to a whole number, half to even, and leaves its two's
+// complement in the low bits.
+struct Quotient32 {
+  float c, b, y;
+  __device__ __forceinline__ explicit Quotient32(float top) {
+    const float f = power_of_two(128 - (int)(__float_as_uint(top) >> 23));
+    c = 127.f * f;
+    b = top * f;
+    y = 1.f / b;
+  }
+  __device__ __forceinline__ uint32_t code(float p) const {
+    const float a = p * c;
+    const float q = a * y;
+    return __float_as_uint(fmaf(fmaf(-b, q, a), y, q) + 12582912.f) & 0xFFu;
+  }
+};
+struct Quotient64 {
+  double b, y;
+  __device__ __forceinline__ explicit Quotient64(double top) : b(top), y(1.0 / top) {}
+  __device__ __forceinline__ uint32_t code(double p) const {
+    const double a = 127.0 * p;
+    const double q = a * y;
+    return (uint32_t)__double_as_longlong(fma(fma(-b, q, a), y, q) + 6755399441055744.0) & 0xFFu;
+  }
+};
+template <typename P>
+struct QuotientOf;
+template <>
+struct QuotientOf<float> {
+  typedef Quotient32 T;
+};
+template <>
+struct QuotientOf<double> {
+  typedef Quotient64 T;
+};
+
+// TPR threads of a workgroup of BLOCK take one row, NC chunks of 8 elements each
+// (chunk c of thread t: elements 8 (t + c TPR) ..). ADD: 0 none, 1 act, 2 fp32.
+template <typename ACT, bool NORM, int ADD, int TPR, int BLOCK, int NC>
+__global__ __launch_bounds__(BLOCK) void k_rows(RowArgs a) {
+  typedef typename Act<ACT>::P P;
+  constexpr int kRows = BLOCK / TPR, kWaves = TPR / 64;
+  const int row = blockIdx.x * kRows + (int)threadIdx.x / TPR;
+  if (kRows > 1 && row >= a.T) return;  // a row is one wave then: nothing waits for it
+  const int t = threadIdx.x % TPR;
+  const ACT* x = static_cast<const ACT*>(a.x) + row * a.ld_x;
+
+  float v[NC][kChunk], g[NC][kChunk], r[NC][kChunk];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int j = kChunk * (t + c * TPR), n = a.H - j;
+    load8(x + j, n, v[c]);
+    if (ADD == 1) load8(static_cast<const ACT*>(a.add) + row * a.ld_add + j, n, r[c]);
+    if (ADD == 2) load8(static_cast<const float*>(a.add) + row * a.ld_add + j, n, r[c]);
+    if (NORM) load8(static_cast<const ACT*>(a.weight) + j, n, g[c]);
+  }
+  double sum = 0.0;
+  uint32_t top_bits = 0;  // of |p| as fp32: a NaN's are the largest
+  P top = 0;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int j = kChunk * (t + c * TPR), n = a.H - j;
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) {
+      if (ADD) v[c][i] = Act<ACT>::rounded(v[c][i] + r[c][i]);
+      if (NORM) sum = fma((double)v[c][i], (double)v[c][i], sum);
+      const P p = NORM ? (P)v[c][i] * (P)g[c][i] : (P)v[c][i];
+      top_bits = max(top_bits, abs_bits((float)p));
+      if (sizeof(P) == 8) top = fmax((double)top, fabs((double)p));
+    }
+    if (ADD && a.x_out && n > 0) store8(static_cast<ACT*>(a.x_out) + row * a.ld_x_out + j, n, v[c]);
+  }
+  if (NORM) sum = wave_sum(sum);
+  top_bits = wave_max_u(top_bits);
+  if (sizeof(P) == 8) top = wave_max_pos(top);
+  if (kWaves > 1) {
+    __shared__ double part_sum[kWaves];
+    __shared__ uint32_t part_bits[kWaves];
+    __shared__ P part_top[kWaves];
+    const int w = t / 64;
+    if (t % 64 == 0) {
+      part_sum[w] = sum;
+      part_bits[w] = top_bits;
+      part_top[w] = top;
+    }
+    __syncthreads();
+    sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+      if (NORM) sum += part_sum[i];
+      top_bits = max(top_bits, part_bits[i]);
+      if (sizeof(P) == 8) top = fmax((double)top, (double)part_top[i]);
+    }
+  }
+  if (sizeof(P) == 4) top = __uint_as_float(top_bits);
+  const double rstd = NORM ? 1.0 / sqrt(sum / a.H + (double)a.eps) : 1.0;
+  if (NORM && a.out) {
+    const float rs = (float)rstd;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int j = kChunk * (t + c * TPR), n = a.H - j;
+      float o[kChunk];
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i)
+        o[i] = sizeof(P) == 8 ? (float)((double)v[c][i] * (double)g[c][i] * rstd) : v[c][i] * g[c][i] * rs;
+      if (n > 0) store8(static_cast<ACT*>(a.out) + row * a.ld_out + j, n, o);
+    }
+  }
+  if (!a.q) return;
+  // A NaN or an infinity in the row: scale NaN and codes 0, so that every product
+  // with the row is NaN. A row of (next to) nothing: scale and codes 0.
+  const bool bad = top_bits >= 0x7F800000u || (NORM && !(rstd > 0.0));
+  const bool none = top_bits < (27u << 23);  // under 2^-100
+  if (t == 0) a.s[row] = bad ? __uint_as_float(0x7FC00000u) : none ? 0.f : (float)((double)top * rstd / 127.0);
+  const typename QuotientOf<P>::T quot(bad || none ? (P)1 : top);
+  const uint32_t keep = bad || none ? 0u : ~0u;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int j = kChunk * (t + c * TPR), n = a.H - j;
+    uint32_t code[kChunk];
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) code[i] = quot.code(NORM ? (P)v[c][i] * (P)g[c][i] : (P)v[c][i]) & keep;
+    int8_t* q = a.q + row * a.ld_q + j;
+    if (n >= kChunk) {
+      I8x8 w;
+      w.v[0] = code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24;
+      w.v[1] = code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24;
+      *reinterpret_cast<I8x8*>(q) = w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i)
+        if (i < n) q[i] = (int8_t)code[i];
+    }
+  }
+}
+
+template <typename ACT, bool NORM, int ADD>
+void launch(const RowArgs& a, hipStream_t s) {
+#define ROWS(TPR, BLOCK, NC)                                                                              \
+  hipLaunchKernelGGL((k_rows<ACT, NORM, ADD, TPR, BLOCK, NC>), dim3((a.T - 1) / (BLOCK / TPR) + 1), dim3(BLOCK), \
+                     0, s, a)
+  if (a.H <= 512)
+    ROWS(64, 256, 1);
+  else if (a.H <= 2048)
+    ROWS(256, 256, 1);
+  else if (a.H <= 8192)
+    ROWS(1024, 1024, 1);
+  else
+    ROWS(1024, 1024, 2);
+#undef ROWS
+}
+
+template <typename ACT>
+void launch_norm(const RowArgs& a, hipStream_t s) {
+  if (!a.add)
+    launch<ACT, true, 0>(a, s);
+  else if (a.add_f32 && sizeof(ACT) == 2)
+    launch<ACT, true, 2>(a, s);
+  else
+    launch<ACT, true, 1>(a, s);
+}
+
+}  // namespace
+
+void launch_rms_norm(const RowArgs& a, hipStream_t s) {
+  if (a.act_bf16)
+    launch_norm<uint16_t>(a, s);
+  else
+    launch_norm<float>(a, s);
+}
+
+void launch_quantize_rows(const RowArgs& a, hipStream_t s) {
+  if (a.act_bf16)
+    launch<uint16_t, false, 0>(a, s);
+  else
+    launch<float, false, 0>(a, s);
+}
+
+}  // namespace moe

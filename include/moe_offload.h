@@ -398,6 +398,134 @@ moe_status moe_plan_kernel_times(moe_plan* plan, moe_kernel_times* out);
 moe_status moe_measure_link_ceilings(size_t hbm_bytes, size_t host_bytes, int32_t iters, moe_stream stream,
                                      moe_link_ceilings* out);
 
+/* ---- Dense operators beside the routed layer --------------------------------
+ *
+ * What stands before and beside moe_layer_forward in a transformer's layer: the norm
+ * that feeds the router, and the dense products (attention's projections, an expert
+ * shared by every token) on 8-bit codes. They need no plan: every buffer is the
+ * caller's, nothing is allocated, and nothing is kept between calls, so calls on
+ * different streams or threads may overlap as long as their buffers are apart, and all
+ * may be captured into a HIP graph.
+ *
+ * Codes of a row v: scale = max|v| / 127 (fp32), code = round half even(127 v / max|v|),
+ * in -127..127; the value is code * scale. A row with a NaN or an infinity (a product of
+ * the norm beyond fp32's range counts as one) has scale NaN and codes 0, so that every
+ * product with it is NaN; one whose largest size is under 2^-100 has scale and codes 0.
+ *
+ * Conventions, besides those above:
+ *  - A matrix has rows of consecutive elements and a row stride ld_* in elements; 0
+ *    stands for packed rows. Elements between the rows and behind the last one are
+ *    neither read nor written. Matrices and vectors are aligned to their element;
+ *    codes that a product reads (q_x, q_w, q_gu, q_dn) to 16 bytes, rows too.
+ *  - Work is enqueued on the device of `stream` (the null stream: the current device).
+ *  - T == 0 is a no-op: no pointer is looked at then.
+ *  - An output may not overlap an input or another output, but for the cases named.
+ *  - Errors: MOE_E_INVALID (arguments), MOE_E_HIP (launch failure). */
+
+/* Root-mean-square norm with the residual's addition:
+ *   s = act(x + add) (fp32 sum, rounded once; x itself without add)
+ *   n[t][j] = s[t][j] * weight[j] / sqrt(mean_j(s[t][j]^2) + eps)
+ * and any of the outputs x_out = s, out = act(n), and the codes of n with their scales.
+ * mean(s^2) is summed in fp64; the codes are those of s * weight exactly for bf16
+ * activations, in fp64 for fp32 ones (the row's root mean square cancels in them).
+ * `add` is in the activation's type or fp32, so that moe_layer_forward's y is added as it
+ * stands. x_out, out may each be x or add themselves (same address, stride and type). */
+typedef struct {
+  int32_t T;              /* rows, 0..2^20 */
+  int32_t H;              /* 1..16384 */
+  int32_t act_dtype;      /* moe_act_dtype of x, weight, x_out and out */
+  int32_t add_dtype;      /* moe_act_dtype of add: act_dtype or MOE_ACT_F32 */
+  float eps;              /* > 0 */
+  const void* x;          /* device [T][H] */
+  int64_t ld_x;
+  const void* add;        /* device [T][H], or NULL */
+  int64_t ld_add;
+  const void* weight;     /* device [H] */
+  void* x_out;            /* device [T][H], or NULL (needs add) */
+  int64_t ld_x_out;
+  void* out;              /* device [T][H], or NULL */
+  int64_t ld_out;
+  int8_t* q_out;          /* device [T][H] codes, or NULL */
+  int64_t ld_q;
+  float* s_out;           /* device [T] scales; given exactly if q_out is */
+} moe_rms_norm_args;
+moe_status moe_rms_norm(const moe_rms_norm_args* args, moe_stream stream);
+
+/* Codes and scales of the rows of x: activations that no norm writes, or a weight
+ * matrix [N][K], whose rows are its channels. */
+typedef struct {
+  int32_t T;              /* rows, 0..2^20 */
+  int32_t H;              /* 1..16384 */
+  int32_t act_dtype;      /* moe_act_dtype of x */
+  const void* x;          /* device [T][H] */
+  int64_t ld_x;
+  int8_t* q_out;          /* device [T][H] */
+  int64_t ld_q;
+  float* s_out;           /* device [T] */
+} moe_quantize_args;
+moe_status moe_quantize_rows(const moe_quantize_args* args, moe_stream stream);
+
+/* Product of 8-bit codes with a scale for each token and each channel:
+ *   out[t][n] = act( s_x[t] s_w[n] sum_k q_x[t][k] q_w[n][k] + bias[n] + y_in[t][n] + res[t][n] )
+ * The sum is exact in int32 (codes -128..127), the rest fp32, rounded once. y_in is
+ * what an operator such as moe_layer_forward left in fp32, res the residual stream in
+ * out's type. out may be res or y_in themselves (same address, stride and type). */
+typedef struct {
+  int32_t T;              /* tokens, 0..2^20 */
+  int32_t N;              /* channels, 1..2^24 */
+  int32_t K;              /* multiple of 16, 16..131056 */
+  int32_t out_dtype;      /* moe_act_dtype of out and res */
+  const int8_t* q_x;      /* device [T][K] */
+  int64_t ld_x;
+  const float* s_x;       /* device [T] */
+  const int8_t* q_w;      /* device [N][K] */
+  int64_t ld_w;
+  const float* s_w;       /* device [N] */
+  const float* bias;      /* device [N], or NULL */
+  const float* y_in;      /* device [T][N], or NULL */
+  int64_t ld_y;
+  const void* res;        /* device [T][N], or NULL */
+  int64_t ld_res;
+  void* out;              /* device [T][N] */
+  int64_t ld_out;
+} moe_int8_matmul_args;
+moe_status moe_int8_matmul(const moe_int8_matmul_args* args, moe_stream stream);
+
+/* Gated feed-forward block on 8-bit codes, the dense counterpart of one expert (the
+ * expert that a layer shares among all tokens):
+ *   h = silu(Wg x) * (Wu x) in fp32, from exact sums; h' = codes of each token's h
+ *   out[t][n] = act( (Wd h')[t][n] + y_in[t][n] + res[t][n] )
+ * with x = q_x * s_x and each weight its code times its channel's scale. q_gu holds the
+ * I gate rows, then the I up rows. A code of h may differ by one step from that of
+ * exactly computed h where 127 h / max|h| lies next to a half. The workspace holds
+ * what moe_int8_ffn_workspace says, 256-byte aligned; its contents need not be kept,
+ * and calls that overlap in time need one each. out may be res or y_in themselves. */
+typedef struct {
+  int32_t T;              /* tokens, 0..2^20 */
+  int32_t H;              /* multiple of 16, 16..131056 */
+  int32_t I;              /* multiple of 16, 16..16384 */
+  int32_t out_dtype;      /* moe_act_dtype of out and res */
+  const int8_t* q_x;      /* device [T][H] */
+  int64_t ld_x;
+  const float* s_x;       /* device [T] */
+  const int8_t* q_gu;     /* device [2I][H] */
+  int64_t ld_gu;
+  const float* s_gu;      /* device [2I] */
+  const int8_t* q_dn;     /* device [H][I] */
+  int64_t ld_dn;
+  const float* s_dn;      /* device [H] */
+  const float* y_in;      /* device [T][H], or NULL */
+  int64_t ld_y;
+  const void* res;        /* device [T][H], or NULL */
+  int64_t ld_res;
+  void* out;              /* device [T][H] */
+  int64_t ld_out;
+  void* workspace;        /* device */
+  size_t workspace_bytes;
+} moe_int8_ffn_args;
+moe_status moe_int8_ffn_workspace(int32_t T, int32_t H, int32_t I, size_t* bytes);
+moe_status moe_int8_ffn(const moe_int8_ffn_args* args, moe_stream stream);
+
 /* Free everything the plan owns (synchronises the device first). NULL is a no-op. */
 void moe_plan_destroy(moe_plan* plan);
 
