@@ -251,77 +251,80 @@ def _layer_weights(router_w, router_b, experts):
 # stream of that GPU); the GPU need not be the current one.
 
 
+# A call of a few tokens takes less time on the GPU than a handful of Python calls, so the
+# checks below read each tensor's properties once, and in the order that costs least.
+
+
 def _refuse(fn, msg):
     raise MoeError(MOE_E_INVALID, fn, msg)
 
 
-class _Operands:
-    """The tensors of one call: checks each against what the operator takes, collects the
-    device they share."""
+def _refuse_tensor(fn, name, t, shape, dtype, dev):
+    if t.dtype is not dtype:
+        _refuse(fn, "%s has dtype %s, not %s" % (name, t.dtype, dtype))
+    if t.get_device() < 0:
+        _refuse(fn, "%s is not on a GPU" % name)
+    if t.get_device() != dev:
+        _refuse(fn, "%s is on another GPU than the other tensors" % name)
+    if t.shape != shape:
+        _refuse(fn, "%s has shape %s, not %s" % (name, tuple(t.shape), shape))
+    _refuse(fn, "%s: the elements of a row are not consecutive" % name)
 
-    def __init__(self, fn):
-        self.fn, self.device = fn, None
 
-    def _tensor(self, name, t, dtypes):
-        if t.dtype not in dtypes:
-            _refuse(self.fn, "%s has dtype %s" % (name, t.dtype))
-        d = t.get_device()
-        if d < 0:
-            _refuse(self.fn, "%s is not on a GPU" % name)
-        if self.device is None:
-            self.device = d
-        elif d != self.device:
-            _refuse(self.fn, "%s is on another GPU than the other tensors" % name)
+def _mat(fn, name, t, rows, cols, dtype, dev):
+    """(address, row stride) of a matrix, (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t.dtype is dtype and t.get_device() == dev and t.shape == (rows, cols):
+        ld, step = t.stride()
+        if step == 1 or cols == 1:
+            # a single row's stride says nothing (and may be less than its length)
+            return t.data_ptr(), ld if rows > 1 else cols
+    _refuse_tensor(fn, name, t, (rows, cols), dtype, dev)
 
-    def mat(self, name, t, rows, cols, *dtypes):
-        """(address, row stride) of a matrix, (None, 0) for None."""
-        if t is None:
-            return None, 0
-        self._tensor(name, t, dtypes)
-        if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
-            _refuse(self.fn, "%s has shape %s, not (%d, %d)" % (name, tuple(t.shape), rows, cols))
-        if t.stride(1) != 1 and cols > 1:
-            _refuse(self.fn, "%s: the elements of a row are not consecutive" % name)
-        # a single row's stride says nothing (and may be less than its length)
-        return t.data_ptr(), t.stride(0) if rows > 1 else cols
 
-    def vec(self, name, t, n, *dtypes):
-        """Address of a packed vector, None for None."""
-        if t is None:
-            return None
-        self._tensor(name, t, dtypes)
-        if t.dim() != 1 or t.shape[0] != n:
-            _refuse(self.fn, "%s has shape %s, not (%d,)" % (name, tuple(t.shape), n))
-        if t.stride(0) != 1 and n > 1:
-            _refuse(self.fn, "%s is not packed" % name)
+def _vec(fn, name, t, n, dtype, dev):
+    """Address of a packed vector, None for None."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.get_device() == dev and t.shape == (n,) and (n <= 1 or t.stride(0) == 1):
         return t.data_ptr()
-
-    def call(self, args, stream):
-        import torch
-        fn = getattr(load_library(), self.fn)
-        if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        if self.device == torch.cuda.current_device():
-            _check(fn(ctypes.byref(args), _stream(stream)), self.fn)
-        else:
-            with torch.cuda.device(self.device):
-                _check(fn(ctypes.byref(args), _stream(stream)), self.fn)
+    _refuse_tensor(fn, name, t, (n,), dtype, dev)
 
 
 def _act_of(fn, name, t):
-    """moe_act_dtype of a tensor, and its torch dtype."""
+    """moe_act_dtype of a tensor."""
     import torch
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return ACT_BF16
-    if t.dtype == torch.float32:
+    if t.dtype is torch.float32:
         return ACT_F32
     _refuse(fn, "%s has dtype %s, not bfloat16 or float32" % (name, t.dtype))
 
 
 def _shape2(fn, name, t):
-    if t.dim() != 2:
-        _refuse(fn, "%s has %d dimensions, not 2" % (name, t.dim()))
-    return t.shape
+    s = t.shape
+    if len(s) != 2:
+        _refuse(fn, "%s has %d dimensions, not 2" % (name, len(s)))
+    return s
+
+
+def _run(fn, name, args, dev, stream):
+    """Enqueue on `stream`, by default torch's current stream of GPU `dev`."""
+    import torch
+    if dev < 0:
+        _refuse(name, "the tensors are not on a GPU")
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        s = _stream(stream)
+    if dev == torch._C._cuda_getDevice():
+        status = fn(ctypes.byref(args), s)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(ctypes.byref(args), s)
+    if status != MOE_OK:
+        _check(status, name)
 
 
 def rms_norm(x, weight, eps=1e-6, add=None, x_out=None, out=None, q_out=None, s_out=None, stream=None):
@@ -329,27 +332,30 @@ def rms_norm(x, weight, eps=1e-6, add=None, x_out=None, out=None, q_out=None, s_
     x_out = s rounded to x's dtype, out = the norm in x's dtype, q_out int8 [T, H] and s_out
     float32 [T] = its codes and scales; any of the outputs may be None (moe_rms_norm)."""
     import torch
-    fn = "moe_rms_norm"
+    lib, fn = _lib or load_library(), "moe_rms_norm"
     T, H = _shape2(fn, "x", x)
-    act, ad = _act_of(fn, "x", x), ACT_F32 if add is None else _act_of(fn, "add", add)
-    o = _Operands(fn)
-    dt = x.dtype
-    a = RmsNormArgs(T, H, act, ad, eps, *o.mat("x", x, T, H, dt), *o.mat("add", add, T, H, dt, torch.float32),
-                    o.vec("weight", weight, H, dt), *o.mat("x_out", x_out, T, H, dt), *o.mat("out", out, T, H, dt),
-                    *o.mat("q_out", q_out, T, H, torch.int8), o.vec("s_out", s_out, T, torch.float32))
-    o.call(a, stream)
+    dt, dev = x.dtype, x.get_device()
+    act = _act_of(fn, "x", x)
+    adt = dt if add is None else add.dtype
+    if adt is not dt and adt is not torch.float32:
+        _refuse(fn, "add has dtype %s, not %s or float32" % (adt, dt))
+    a = RmsNormArgs(T, H, act, act if adt is dt else ACT_F32, eps, *_mat(fn, "x", x, T, H, dt, dev),
+                    *_mat(fn, "add", add, T, H, adt, dev), _vec(fn, "weight", weight, H, dt, dev),
+                    *_mat(fn, "x_out", x_out, T, H, dt, dev), *_mat(fn, "out", out, T, H, dt, dev),
+                    *_mat(fn, "q_out", q_out, T, H, torch.int8, dev), _vec(fn, "s_out", s_out, T, torch.float32, dev))
+    _run(lib.moe_rms_norm, fn, a, dev, stream)
 
 
 def quantize_rows(x, q_out, s_out, stream=None):
     """int8 codes q_out [T, H] and float32 scales s_out [T] of the rows of x [T, H]
     (moe_quantize_rows): activations, or a weight matrix, whose rows are its channels."""
     import torch
-    fn = "moe_quantize_rows"
+    lib, fn = _lib or load_library(), "moe_quantize_rows"
     T, H = _shape2(fn, "x", x)
-    o = _Operands(fn)
-    a = QuantizeArgs(T, H, _act_of(fn, "x", x), *o.mat("x", x, T, H, x.dtype),
-                     *o.mat("q_out", q_out, T, H, torch.int8), o.vec("s_out", s_out, T, torch.float32))
-    o.call(a, stream)
+    dev = x.get_device()
+    a = QuantizeArgs(T, H, _act_of(fn, "x", x), *_mat(fn, "x", x, T, H, x.dtype, dev),
+                     *_mat(fn, "q_out", q_out, T, H, torch.int8, dev), _vec(fn, "s_out", s_out, T, torch.float32, dev))
+    _run(lib.moe_quantize_rows, fn, a, dev, stream)
 
 
 def int8_matmul(q_x, s_x, q_w, s_w, out, bias=None, y_in=None, res=None, stream=None):
@@ -357,15 +363,16 @@ def int8_matmul(q_x, s_x, q_w, s_w, out, bias=None, y_in=None, res=None, stream=
     [N, K]; bias float32 [N], y_in float32 [T, N], res in out's dtype; out may be y_in or
     res (moe_int8_matmul)."""
     import torch
-    fn = "moe_int8_matmul"
-    (T, K), N = _shape2(fn, "q_x", q_x), _shape2(fn, "q_w", q_w)[0]
-    o = _Operands(fn)
-    f32, i8 = torch.float32, torch.int8
-    a = Int8MatmulArgs(T, N, K, _act_of(fn, "out", out), *o.mat("q_x", q_x, T, K, i8), o.vec("s_x", s_x, T, f32),
-                       *o.mat("q_w", q_w, N, K, i8), o.vec("s_w", s_w, N, f32), o.vec("bias", bias, N, f32),
-                       *o.mat("y_in", y_in, T, N, f32), *o.mat("res", res, T, N, out.dtype),
-                       *o.mat("out", out, T, N, out.dtype))
-    o.call(a, stream)
+    lib, fn = _lib or load_library(), "moe_int8_matmul"
+    T, K = _shape2(fn, "q_x", q_x)
+    N = _shape2(fn, "q_w", q_w)[0]
+    f32, i8, dt, dev = torch.float32, torch.int8, out.dtype, q_x.get_device()
+    a = Int8MatmulArgs(T, N, K, _act_of(fn, "out", out), *_mat(fn, "q_x", q_x, T, K, i8, dev),
+                       _vec(fn, "s_x", s_x, T, f32, dev), *_mat(fn, "q_w", q_w, N, K, i8, dev),
+                       _vec(fn, "s_w", s_w, N, f32, dev), _vec(fn, "bias", bias, N, f32, dev),
+                       *_mat(fn, "y_in", y_in, T, N, f32, dev), *_mat(fn, "res", res, T, N, dt, dev),
+                       *_mat(fn, "out", out, T, N, dt, dev))
+    _run(lib.moe_int8_matmul, fn, a, dev, stream)
     return out
 
 
@@ -382,17 +389,17 @@ def int8_ffn(q_x, s_x, q_gu, s_gu, q_dn, s_dn, out, workspace, y_in=None, res=No
     then up rows), q_dn int8 [H, I]; out [T, H] = act(block + y_in + res). workspace: a uint8
     tensor of int8_ffn_workspace(T, H, I) bytes, one for each call in flight (moe_int8_ffn)."""
     import torch
-    fn = "moe_int8_ffn"
-    (T, H), I = _shape2(fn, "q_x", q_x), _shape2(fn, "q_dn", q_dn)[1]
-    o = _Operands(fn)
-    f32, i8 = torch.float32, torch.int8
-    a = Int8FfnArgs(T, H, I, _act_of(fn, "out", out), *o.mat("q_x", q_x, T, H, i8), o.vec("s_x", s_x, T, f32),
-                    *o.mat("q_gu", q_gu, 2 * I, H, i8), o.vec("s_gu", s_gu, 2 * I, f32),
-                    *o.mat("q_dn", q_dn, H, I, i8), o.vec("s_dn", s_dn, H, f32),
-                    *o.mat("y_in", y_in, T, H, f32), *o.mat("res", res, T, H, out.dtype),
-                    *o.mat("out", out, T, H, out.dtype),
-                    o.vec("workspace", workspace, workspace.numel(), torch.uint8), workspace.numel())
-    o.call(a, stream)
+    lib, fn = _lib or load_library(), "moe_int8_ffn"
+    T, H = _shape2(fn, "q_x", q_x)
+    I = _shape2(fn, "q_dn", q_dn)[1]
+    f32, i8, dt, dev, n = torch.float32, torch.int8, out.dtype, q_x.get_device(), workspace.numel()
+    a = Int8FfnArgs(T, H, I, _act_of(fn, "out", out), *_mat(fn, "q_x", q_x, T, H, i8, dev),
+                    _vec(fn, "s_x", s_x, T, f32, dev), *_mat(fn, "q_gu", q_gu, 2 * I, H, i8, dev),
+                    _vec(fn, "s_gu", s_gu, 2 * I, f32, dev), *_mat(fn, "q_dn", q_dn, H, I, i8, dev),
+                    _vec(fn, "s_dn", s_dn, H, f32, dev), *_mat(fn, "y_in", y_in, T, H, f32, dev),
+                    *_mat(fn, "res", res, T, H, dt, dev), *_mat(fn, "out", out, T, H, dt, dev),
+                    _vec(fn, "workspace", workspace, n, torch.uint8, dev), n)
+    _run(lib.moe_int8_ffn, fn, a, dev, stream)
     return out
 
 

@@ -56,5 +56,8 @@ struct Int8Args {
 void launch_int8_matmul(const Int8Args& a, bool out_bf16, hipStream_t s);
 // out = h [T][N] fp32 = silu(gate) * up
 void launch_int8_gated(const Int8Args& a, hipStream_t s);
+// the same two for many rows
+void launch_int8_gemm(const Int8Args& a, bool out_bf16, hipStream_t s);
+void launch_int8_gated_gemm(const Int8Args& a, hipStream_t s);
 
 }  // namespace moe

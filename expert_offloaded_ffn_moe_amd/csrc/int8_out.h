@@ -46,6 +46,63 @@ __device__ __forceinline__ void int8_store(const Int8Out& o, int t, int n, float
   static_cast<E*>(o.out)[t * o.ld_out + n] = OutElem<BF16>::rounded(v);
 }
 
+// Four neighbouring elements of a row, at any element's alignment (gfx950 performs such
+// accesses whole).
+struct __attribute__((packed, aligned(4))) F32x4u {
+  float v[4];
+};
+struct __attribute__((packed, aligned(2))) Bf16x4u {
+  uint32_t v[2];
+};
+__device__ __forceinline__ void load4(const float* p, int n, float* v) {
+  if (n >= 4) {
+    const F32x4u w = *reinterpret_cast<const F32x4u*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = w.v[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = i < n ? p[i] : 0.f;
+  }
+}
+__device__ __forceinline__ void load4(const uint16_t* p, int n, float* v) {
+  if (n >= 4) {
+    const Bf16x4u w = *reinterpret_cast<const Bf16x4u*>(p);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      v[2 * i] = __uint_as_float(w.v[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w.v[i] & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = i < n ? OutElem<true>::load(p[i]) : 0.f;
+  }
+}
+__device__ __forceinline__ void store4(float* p, int n, const float* v) {
+  if (n >= 4) {
+    F32x4u w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w.v[i] = v[i];
+    *reinterpret_cast<F32x4u*>(p) = w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) p[i] = v[i];
+  }
+}
+__device__ __forceinline__ void store4(uint16_t* p, int n, const float* v) {
+  if (n >= 4) {
+    Bf16x4u w;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      w.v[i] = (uint32_t)OutElem<true>::rounded(v[2 * i]) | (uint32_t)OutElem<true>::rounded(v[2 * i + 1]) << 16;
+    *reinterpret_cast<Bf16x4u*>(p) = w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) p[i] = OutElem<true>::rounded(v[i]);
+  }
+}
+
 // silu(g) u, each from its exact sum; exp(-g) past fp32's range gives the limit 0
 __device__ __forceinline__ float gated_value(int g_acc, int u_acc, float sx, float sg, float su) {
   const float g = (float)g_acc * sx * sg, u = (float)u_acc * sx * su;

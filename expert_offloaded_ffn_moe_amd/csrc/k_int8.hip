@@ -18,6 +18,7 @@
 namespace moe {
 namespace {
 
+constexpr int kSkinnyRows = 16;  // tokens up to which these kernels run
 constexpr int kSkinnyWaves = 8;  // waves of a workgroup, splitting K
 constexpr int kStep = 4;         // 64-byte K steps of a wave's load block
 
@@ -100,12 +101,16 @@ void skinny(const Int8Args& a, hipStream_t s) {
 }  // namespace
 
 void launch_int8_matmul(const Int8Args& a, bool out_bf16, hipStream_t s) {
+  if (a.T > kSkinnyRows) return launch_int8_gemm(a, out_bf16, s);
   if (out_bf16)
     skinny<false, true>(a, s);
   else
     skinny<false, false>(a, s);
 }
 
-void launch_int8_gated(const Int8Args& a, hipStream_t s) { skinny<true, false>(a, s); }
+void launch_int8_gated(const Int8Args& a, hipStream_t s) {
+  if (a.T > kSkinnyRows) return launch_int8_gated_gemm(a, s);
+  skinny<true, false>(a, s);
+}
 
 }  // namespace moe

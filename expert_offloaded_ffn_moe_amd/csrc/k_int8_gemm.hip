@@ -1,0 +1,325 @@
+// 8-bit matrix product for many rows, and its gated form: tiles of tokens x channels on
+// v_mfma_i32_32x32x32_i8.
+//
+// Lane layout of the 32x32x32 MFMA: lane l supplies 16 bytes of row l % 32 of each
+// operand at K offset 16 (l / 32), and receives the sums of column l % 32 and rows
+// 8 (v / 4) + 4 (l / 32) + v % 4 (v = 0..15). Tokens are the row operand and channels the
+// column operand, so that 32 lanes store neighbouring channels.
+//
+// A tile of BM tokens x BN channels runs over K in steps of BK bytes (64 or 128) through a
+// ring of LDS buffers, filled by loads that go from memory to LDS directly (16 bytes a lane,
+// 1024 / BK rows an instruction). In LDS the 16-byte pieces of row r stand at places
+// piece ^ swizzle(r): an instruction writes its lanes' bytes in lane order, so each lane
+// fetches the piece that belongs at its place, and sixteen lanes that read one piece of
+// sixteen rows then use every bank once. Pieces past K come from a line of zeros.
+//
+// A step is two halves. The operands of one are read from LDS while the products of the
+// other run; the barrier that frees the oldest buffer and opens the next stands between the
+// two, so that it, too, is covered by products.
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "int8_out.h"
+
+namespace moe {
+namespace {
+
+typedef __attribute__((address_space(3))) void lvoid;
+
+// place of row r's piece p: p ^ swizzle(r); sixteen rows' places of one piece, 256 bytes of
+// LDS apart or less, are in different banks
+template <int BK>
+__device__ __forceinline__ int swizzle(int r) {
+  return BK == 64 ? r >> 2 & 3 : r >> 1 & 7;
+}
+
+// what pieces past K are read from
+__device__ const i32x4 zero_piece = {0, 0, 0, 0};
+
+// Workgroups are dealt to the 8 XCDs round-robin; each XCD gets one contiguous range of
+// the tiles, so that the tiles of its L2 share rows and channels.
+__device__ __forceinline__ int xcd_order(int b, int nb) {
+  constexpr int kXcd = 8;
+  const int per = nb / kXcd, rem = nb % kXcd, x = b % kXcd, i = b / kXcd;
+  return x < rem ? x * (per + 1) + i : rem * (per + 1) + (x - rem) * per + i;
+}
+
+template <int N>
+__device__ __forceinline__ void wait_loads_but() {  // all but the newest N loads are in, and every LDS read
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+
+// 16 bytes from each lane's address to LDS at `to` + 16 lane. Written as one block, so that
+// the compiler, which cannot tell the ring's buffers apart, adds no wait for it before the
+// LDS reads of the others: wait_loads_but counts these loads instead. It has no output
+// register. (A write of M0 is followed by one wait state before its use.)
+__device__ __forceinline__ void load_to_lds(const int8_t* from, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory", "m0");
+}
+
+// PASSES rows, ROWS apart, of four channels each, from their sums in LDS. WHOLE: every row
+// and channel is one of the matrix's, and what the rows need is loaded for all of them
+// before it is used.
+template <bool GATED, bool BF16, int PASSES, int ROWS, int LDROW, bool WHOLE>
+__device__ __forceinline__ void store_rows(const Int8Args& a, int t0, int n, const float* sx, const int* from,
+                                           const float* sw, const float* su, const float* bias) {
+  typedef typename OutElem<BF16>::T E;
+  constexpr int kAt = PASSES < 4 ? PASSES : 4;  // rows at once
+  const int left = WHOLE ? 4 : a.N - n;
+  if (!WHOLE && left <= 0) return;
+#pragma unroll
+  for (int p0 = 0; p0 < PASSES; p0 += kAt) {
+    float v[kAt][4], more[kAt][4];
+#pragma unroll
+    for (int p = 0; p < kAt; ++p) {
+      const int r = (p0 + p) * ROWS;
+      const i32x4 s = *reinterpret_cast<const i32x4*>(from + r * LDROW);
+      if (GATED) {
+        const i32x4 u = *reinterpret_cast<const i32x4*>(from + r * LDROW + 16);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[p][e] = gated_value(s[e], u[e], sx[r], sw[e], su[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[p][e] = (float)s[e] * sx[r] * sw[e] + bias[e];
+      }
+    }
+    if (!GATED && a.o.y) {
+#pragma unroll
+      for (int p = 0; p < kAt; ++p)
+        if (WHOLE || t0 + (p0 + p) * ROWS < a.T) load4(a.o.y + (t0 + (p0 + p) * ROWS) * a.o.ld_y + n, left, more[p]);
+#pragma unroll
+      for (int p = 0; p < kAt; ++p)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[p][e] += more[p][e];
+    }
+    if (!GATED && a.o.res) {
+#pragma unroll
+      for (int p = 0; p < kAt; ++p)
+        if (WHOLE || t0 + (p0 + p) * ROWS < a.T)
+          load4(static_cast<const E*>(a.o.res) + (t0 + (p0 + p) * ROWS) * a.o.ld_res + n, left, more[p]);
+#pragma unroll
+      for (int p = 0; p < kAt; ++p)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[p][e] += more[p][e];
+    }
+#pragma unroll
+    for (int p = 0; p < kAt; ++p)
+      if (WHOLE || t0 + (p0 + p) * ROWS < a.T)
+        store4(static_cast<E*>(a.o.out) + (t0 + (p0 + p) * ROWS) * a.o.ld_out + n, left, v[p]);
+  }
+}
+
+// WM x WN waves, each TM x TN blocks of 32 x 32; RING buffers. GATED: of every 32 channels
+// of the tile the first 16 are gate rows and the others the same rows of up, and h is
+// stored in fp32.
+template <int WM, int WN, int TM, int TN, int BK, int RING, bool GATED, bool BF16>
+__global__ __launch_bounds__(64 * WM* WN) void k_int8_gemm(Int8Args a, int mtiles) {
+  constexpr int kWaves = WM * WN, BM = 32 * TM * WM, BN = 32 * TN * WN;
+  constexpr int kPieces = BK / 16, kRowsPer = 64 / kPieces;  // pieces of a row; rows of a load instruction
+  constexpr int kLoadsA = BM / kRowsPer / kWaves, kLoadsB = BN / kRowsPer / kWaves;  // instructions of a wave per step
+  static_assert(kLoadsA * kRowsPer * kWaves == BM && kLoadsB * kRowsPer * kWaves == BN, "rows divide among the waves");
+  constexpr int kLoads = kLoadsA + kLoadsB;
+  __shared__ __attribute__((aligned(1024))) uint8_t sh[RING][(BM + BN) * BK];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tile = xcd_order(blockIdx.x, gridDim.x);
+  const int m0 = tile % mtiles * BM, n0 = tile / mtiles * (GATED ? BN / 2 : BN);
+
+  __shared__ float rows_sx[BM];
+  for (int i = threadIdx.x; i < BM; i += 64 * kWaves) rows_sx[i] = a.o.sx[min(m0 + i, a.T - 1)];
+  // this lane's channels in the epilogue: columns c .. c + 3 of the wave's (gated: gate
+  // columns; up's are 16 on), their scales and bias
+  constexpr int kCols = 32 * TN, kRow = kCols + 8;
+  constexpr int kLanes = kCols / 4 / (GATED ? 2 : 1), kRows = 64 / kLanes;  // lanes of a row, rows a pass
+  const int wm = wave / WN, wn = wave % WN, half = lane >> 5, l32 = lane & 31;
+  const int lc = lane % kLanes * 4, c = GATED ? lc / 16 * 32 + lc % 16 : lc;
+  const int n = n0 + wn * (GATED ? kCols / 2 : kCols) + lc;
+  float sw[4], su[4] = {0.f, 0.f, 0.f, 0.f}, bias[4] = {0.f, 0.f, 0.f, 0.f};
+  load4(a.o.sw + n, a.N - n, sw);
+  if (GATED) load4(a.o.sw + a.N + n, a.N - n, su);
+  if (!GATED && a.o.bias) load4(a.o.bias + n, a.N - n, bias);
+
+  // this lane's piece of each row that it fetches; rows past the last are read as the last,
+  // and not stored
+  const int lrow = lane / kPieces;
+  const int8_t* p[kLoads];
+  int at[kLoads];  // its offset in K
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const bool in_a = i < kLoadsA;
+    const int r = (in_a ? wave * kLoadsA + i : wave * kLoadsB + i - kLoadsA) * kRowsPer + lrow;
+    int64_t row = in_a ? min(m0 + r, a.T - 1) : min(n0 + r, a.N - 1);
+    if (GATED && !in_a) row = (int64_t)min(n0 + r / 32 * 16 + r % 16, a.N - 1) + (r & 16 ? a.N : 0);
+    at[i] = (lane % kPieces ^ swizzle<BK>(r)) * 16;
+    p[i] = (in_a ? a.x + row * a.ld_x : a.w + row * a.ld_w) + at[i];
+  }
+  const int8_t* zeros = reinterpret_cast<const int8_t*>(&zero_piece);
+  const uint32_t ring = (uint32_t)(uintptr_t)(lvoid*)&sh[0][0];
+  int kat = 0;  // K offset of the next step to load
+  // the part'th of `parts` parts of the next step's pieces into buffer `buf` (past the last
+  // step: zeros)
+  auto stage = [&](int buf, int part, int parts) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      if (i < kLoads * part / parts || i >= kLoads * (part + 1) / parts) continue;
+      const int to = i < kLoadsA ? (wave * kLoadsA + i) * 1024 : BM * BK + (wave * kLoadsB + i - kLoadsA) * 1024;
+      load_to_lds(kat + at[i] < a.K ? p[i] : zeros, ring + buf * (BM + BN) * BK + to);
+      p[i] += BK;
+    }
+    if (part == parts - 1) kat += BK;
+  };
+
+  i32x16 acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = i32x16{};
+  constexpr int kHalf = BK / 64;  // MFMA steps of a half
+  struct Operands {
+    i32x4 a[kHalf][TM], b[kHalf][TN];
+  };
+  // the part'th of `parts` parts of a half's operands
+  auto fetch = [&](Operands& f, int buf, int h, int part, int parts) {
+    constexpr int kAll = kHalf * (TN + TM);
+#pragma unroll
+    for (int x = 0; x < kAll; ++x) {
+      if (x < kAll * part / parts || x >= kAll * (part + 1) / parts) continue;
+      const int s = x / (TN + TM), i = x % (TN + TM);
+      const int off = l32 * BK + (((2 * (h * kHalf + s) + half) ^ swizzle<BK>(l32)) << 4);
+      if (i < TN)
+        f.b[s][i] = *reinterpret_cast<const i32x4*>(&sh[buf][BM * BK + (wn * TN + i) * 32 * BK + off]);
+      else
+        f.a[s][i - TN] = *reinterpret_cast<const i32x4*>(&sh[buf][(wm * TM + i - TN) * 32 * BK + off]);
+    }
+  };
+  auto products = [&](const Operands& f, int x) {
+    const int s = x / TM, i = x % TM;
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+      acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.a[s][i], f.b[s][j], acc[i][j], 0, 0, 0);
+  };
+  // A half has kSlots slots of TN products; the operands of the next are asked for in the
+  // first of them, so that they are in when its products start, and loads follow.
+  constexpr int kSlots = TM * kHalf, kReadSlots = kSlots >= 4 ? 2 : 1, kLoadSlot0 = kSlots > kReadSlots ? kReadSlots : 0;
+  const int steps = (a.K + BK - 1) / BK;
+#pragma unroll
+  for (int r = 0; r < RING; ++r) stage(r, 0, 1);
+  wait_loads_but<(RING - 1) * kLoads>();
+  __builtin_amdgcn_s_barrier();
+  Operands f0, f1;
+  fetch(f0, 0, 0, 0, 1);
+  int buf = 0;
+  for (int k = 0; k < steps; ++k) {
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
+      products(f0, i);
+      __builtin_amdgcn_sched_barrier(0);
+      if (i < kReadSlots) fetch(f1, buf, 1, i, kReadSlots);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    const int done = buf;  // every wave has all of it in registers at the barrier
+    buf = buf + 1 == RING ? 0 : buf + 1;
+    wait_loads_but<(RING - 2) * kLoads>();  // the next buffer is in, this one's operands too
+    __builtin_amdgcn_s_barrier();
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
+      products(f1, i);
+      __builtin_amdgcn_sched_barrier(0);
+      if (i < kReadSlots) fetch(f0, buf, 0, i, kReadSlots);
+      if (i >= kLoadSlot0) stage(done, i - kLoadSlot0, kSlots - kLoadSlot0);
+    }
+  }
+
+  // Each wave turns its sums in LDS, a block of 32 rows at a time (rows 32 bytes longer, so
+  // that the two rows of a write use different banks), and reads four neighbouring
+  // channels of a row a lane: whole lines are read and written from there on.
+  wait_loads_but<0>();
+  __syncthreads();
+  static_assert(sizeof(sh) >= kWaves * 32 * kRow * 4, "the waves' blocks fit the buffers");
+  int* turn = reinterpret_cast<int*>(&sh[0][0]) + wave * 32 * kRow;
+  const bool whole = n0 + (GATED ? BN / 2 : BN) <= a.N;  // every channel of the tile is one
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) turn[(8 * (v / 4) + 4 * half + v % 4) * kRow + 32 * j + l32] = acc[i][j][v];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const int r0 = (wm * TM + i) * 32 + lane / kLanes;  // this lane's first row in the tile
+    const int* from = turn + lane / kLanes * kRow + c;
+    constexpr int kPasses = 32 / kRows;
+    if (whole && m0 + (wm * TM + i + 1) * 32 <= a.T)
+      store_rows<GATED, BF16, kPasses, kRows, kRow, true>(a, m0 + r0, n, rows_sx + r0, from, sw, su, bias);
+    else
+      store_rows<GATED, BF16, kPasses, kRows, kRow, false>(a, m0 + r0, n, rows_sx + r0, from, sw, su, bias);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+}
+
+}  // namespace
+
+// The tiles, and what 128 bytes of K cost a CU in each (us, one tile on a CU, and two where
+// they fit), measured on products of 64 to 2048 tokens with 2048 to 7168 channels and K. A
+// large tile reads the fewest bytes per product, but too few of them leave CUs idle: the tile
+// whose rounds over the 256 CUs cost least is taken. Against the next best tile that gives,
+// at K = 7168: 2048 x 7168 105 us (128 x 256: 114), 2048 x 4096 62 (128 x 128: 66), 1024 x
+// 7168 58 (128 x 128: 63), 256 x 7168 23 (64 x 64: 25), 128 x 7168 17.5 (64 x 128: 22).
+struct Tile {
+  int tokens, channels;
+  float one, two;  // two: of both tiles of a CU together, 0 where only one fits
+};
+constexpr Tile kTiles[] = {{256, 256, 1.85f, 0.f}, {128, 256, 1.04f, 0.f}, {128, 128, 0.55f, 0.f}, {64, 128, 0.41f, 0.70f}, {64, 64, 0.31f, 0.41f}};
+
+static int choose_tile(int64_t T, int64_t channels) {
+  constexpr int kCus = 256;
+  int best = 0;
+  float least = 0.f;
+  for (int i = 0; i < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++i) {
+    const Tile& c = kTiles[i];
+    const int64_t n = ((T - 1) / c.tokens + 1) * ((channels - 1) / c.channels + 1);
+    float cost;
+    if (c.two == 0.f) {
+      cost = (float)((n - 1) / kCus + 1) * c.one;
+    } else {
+      const int64_t rest = n % (2 * kCus);
+      cost = (float)(n / (2 * kCus)) * c.two + (rest == 0 ? 0.f : rest <= kCus ? c.one : c.two);
+    }
+    if (i == 0 || cost < least) {
+      best = i;
+      least = cost;
+    }
+  }
+  return best;
+}
+
+template <bool GATED, bool BF16, int WM, int WN, int TM, int TN, int BK, int RING>
+static void gemm_tile(const Int8Args& a, hipStream_t s) {
+  const int mt = (a.T - 1) / (32 * TM * WM) + 1, nt = (a.N - 1) / (32 * TN * WN / (GATED ? 2 : 1)) + 1;
+  hipLaunchKernelGGL((k_int8_gemm<WM, WN, TM, TN, BK, RING, GATED, BF16>), dim3(mt * nt), dim3(64 * WM * WN), 0, s, a, mt);
+}
+
+template <bool GATED, bool BF16>
+static void gemm(const Int8Args& a, hipStream_t s) {
+  switch (choose_tile(a.T, GATED ? 2 * (int64_t)a.N : a.N)) {
+    case 0: return gemm_tile<GATED, BF16, 2, 4, 4, 2, 64, 4>(a, s);
+    case 1: return gemm_tile<GATED, BF16, 2, 4, 2, 2, 128, 3>(a, s);
+    case 2: return gemm_tile<GATED, BF16, 2, 4, 2, 1, 128, 4>(a, s);
+    case 3: return gemm_tile<GATED, BF16, 2, 4, 1, 1, 128, 3>(a, s);
+    default: return gemm_tile<GATED, BF16, 2, 2, 1, 1, 128, 4>(a, s);
+  }
+}
+
+void launch_int8_gemm(const Int8Args& a, bool out_bf16, hipStream_t s) {
+  if (out_bf16)
+    gemm<false, true>(a, s);
+  else
+    gemm<false, false>(a, s);
+}
+
+void launch_int8_gated_gemm(const Int8Args& a, hipStream_t s) { gemm<true, false>(a, s); }
+
+}  // namespace moe
