@@ -19,6 +19,9 @@
 // the latency of a load, two reductions and a store.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+#include <type_traits>
+
 #include "dense.h"
 #include "wave.h"
 
@@ -48,33 +51,52 @@ __device__ __forceinline__ uint16_t to_bf16(float f) {
   return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
 }
 
-__device__ __forceinline__ void load8(const uint16_t* p, int n, float* v) {
-  if (n >= kChunk) {
-    const Bf16x8 w = *reinterpret_cast<const Bf16x8*>(p);
+// Eight elements as loaded, and their values.
+template <typename E>
+struct Raw;
+template <>
+struct Raw<uint16_t> {
+  Bf16x8 w;
+  __device__ __forceinline__ void load(const uint16_t* p, int n) {
+    if (n >= kChunk) {
+      w = *reinterpret_cast<const Bf16x8*>(p);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w.v[i] = (2 * i < n ? (uint32_t)p[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)p[2 * i + 1] << 16 : 0u);
+    }
+  }
+  __device__ __forceinline__ void values(float* v) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       v[2 * i] = __uint_as_float(w.v[i] << 16);
       v[2 * i + 1] = __uint_as_float(w.v[i] & 0xFFFF0000u);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i) v[i] = i < n ? bf16_value(p[i]) : 0.f;
   }
-}
-
-__device__ __forceinline__ void load8(const float* p, int n, float* v) {
-  if (n >= kChunk) {
-    const F32x4 a = reinterpret_cast<const F32x4*>(p)[0], b = reinterpret_cast<const F32x4*>(p)[1];
+};
+template <>
+struct Raw<float> {
+  F32x4 a, b;
+  __device__ __forceinline__ void load(const float* p, int n) {
+    if (n >= kChunk) {
+      a = reinterpret_cast<const F32x4*>(p)[0];
+      b = reinterpret_cast<const F32x4*>(p)[1];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a.v[i] = i < n ? p[i] : 0.f;
+        b.v[i] = 4 + i < n ? p[4 + i] : 0.f;
+      }
+    }
+  }
+  __device__ __forceinline__ void values(float* v) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       v[i] = a.v[i];
       v[4 + i] = b.v[i];
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i) v[i] = i < n ? p[i] : 0.f;
   }
-}
+};
 
 __device__ __forceinline__ void store8(uint16_t* p, int n, const float* v) {
   if (n >= kChunk) {
@@ -205,119 +227,166 @@ struct QuotientOf<double> {
   typedef Quotient64 T;
 };
 
+// 1 / sqrt(m) to about 2^-44: the fp32 estimate and one Newton step in fp64 (m in fp32's range)
+__device__ __forceinline__ double rsqrt64(double m) {
+  if (!(m > 1e-36 && m < 1e36)) return 1.0 / sqrt(m);
+  const double r = (double)__frsqrt_rn((float)m);
+  return r * fma(-0.5 * m * r, r, 1.5);
+}
+
 // TPR threads of a workgroup of BLOCK take one row, NC chunks of 8 elements each
-// (chunk c of thread t: elements 8 (t + c TPR) ..). ADD: 0 none, 1 act, 2 fp32.
+// (chunk c of thread t: elements 8 (t + c TPR) ..), then the row `gridDim.x` rows of
+// workgroups on, whose loads are under way before the first is reduced. ADD: 0 none, 1 act,
+// 2 fp32.
 template <typename ACT, bool NORM, int ADD, int TPR, int BLOCK, int NC>
 __global__ __launch_bounds__(BLOCK) void k_rows(RowArgs a) {
   typedef typename Act<ACT>::P P;
+  typedef typename std::conditional<ADD == 1, ACT, float>::type AddT;
   constexpr int kRows = BLOCK / TPR, kWaves = TPR / 64;
-  const int row = blockIdx.x * kRows + (int)threadIdx.x / TPR;
-  if (kRows > 1 && row >= a.T) return;  // a row is one wave then: nothing waits for it
   const int t = threadIdx.x % TPR;
-  const ACT* x = static_cast<const ACT*>(a.x) + row * a.ld_x;
+  const int step = gridDim.x * kRows;
+  int row = blockIdx.x * kRows + (int)threadIdx.x / TPR;
+  if (kRows > 1 && row >= a.T) return;  // a row is one wave then: nothing waits for it
 
-  float v[NC][kChunk], g[NC][kChunk], r[NC][kChunk];
-#pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    const int j = kChunk * (t + c * TPR), n = a.H - j;
-    load8(x + j, n, v[c]);
-    if (ADD == 1) load8(static_cast<const ACT*>(a.add) + row * a.ld_add + j, n, r[c]);
-    if (ADD == 2) load8(static_cast<const float*>(a.add) + row * a.ld_add + j, n, r[c]);
-    if (NORM) load8(static_cast<const ACT*>(a.weight) + j, n, g[c]);
-  }
-  double sum = 0.0;
-  uint32_t top_bits = 0;  // of |p| as fp32: a NaN's are the largest
-  P top = 0;
-#pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    const int j = kChunk * (t + c * TPR), n = a.H - j;
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i) {
-      if (ADD) v[c][i] = Act<ACT>::rounded(v[c][i] + r[c][i]);
-      if (NORM) sum = fma((double)v[c][i], (double)v[c][i], sum);
-      const P p = NORM ? (P)v[c][i] * (P)g[c][i] : (P)v[c][i];
-      top_bits = max(top_bits, abs_bits((float)p));
-      if (sizeof(P) == 8) top = fmax((double)top, fabs((double)p));
-    }
-    if (ADD && a.x_out && n > 0) store8(static_cast<ACT*>(a.x_out) + row * a.ld_x_out + j, n, v[c]);
-  }
-  if (NORM) sum = wave_sum(sum);
-  top_bits = wave_max_u(top_bits);
-  if (sizeof(P) == 8) top = wave_max_pos(top);
-  if (kWaves > 1) {
-    __shared__ double part_sum[kWaves];
-    __shared__ uint32_t part_bits[kWaves];
-    __shared__ P part_top[kWaves];
-    const int w = t / 64;
-    if (t % 64 == 0) {
-      part_sum[w] = sum;
-      part_bits[w] = top_bits;
-      part_top[w] = top;
-    }
-    __syncthreads();
-    sum = 0.0;
-#pragma unroll
-    for (int i = 0; i < kWaves; ++i) {
-      if (NORM) sum += part_sum[i];
-      top_bits = max(top_bits, part_bits[i]);
-      if (sizeof(P) == 8) top = fmax((double)top, (double)part_top[i]);
-    }
-  }
-  if (sizeof(P) == 4) top = __uint_as_float(top_bits);
-  const double rstd = NORM ? 1.0 / sqrt(sum / a.H + (double)a.eps) : 1.0;
-  if (NORM && a.out) {
-    const float rs = (float)rstd;
+  Raw<ACT> x[NC], g[NC];
+  Raw<AddT> r[NC];
+  auto load = [&](int at) {
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int j = kChunk * (t + c * TPR), n = a.H - j;
-      float o[kChunk];
-#pragma unroll
-      for (int i = 0; i < kChunk; ++i)
-        o[i] = sizeof(P) == 8 ? (float)((double)v[c][i] * (double)g[c][i] * rstd) : v[c][i] * g[c][i] * rs;
-      if (n > 0) store8(static_cast<ACT*>(a.out) + row * a.ld_out + j, n, o);
+      x[c].load(static_cast<const ACT*>(a.x) + at * a.ld_x + j, n);
+      if (ADD) r[c].load(static_cast<const AddT*>(a.add) + at * a.ld_add + j, n);
     }
+  };
+  load(row);
+  if (NORM) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) g[c].load(static_cast<const ACT*>(a.weight) + kChunk * (t + c * TPR), a.H - kChunk * (t + c * TPR));
   }
-  if (!a.q) return;
-  // A NaN or an infinity in the row: scale NaN and codes 0, so that every product
-  // with the row is NaN. A row of (next to) nothing: scale and codes 0.
-  const bool bad = top_bits >= 0x7F800000u || (NORM && !(rstd > 0.0));
-  const bool none = top_bits < (27u << 23);  // under 2^-100
-  if (t == 0) a.s[row] = bad ? __uint_as_float(0x7FC00000u) : none ? 0.f : (float)((double)top * rstd / 127.0);
-  const typename QuotientOf<P>::T quot(bad || none ? (P)1 : top);
-  const uint32_t keep = bad || none ? 0u : ~0u;
+  const double inv_h = 1.0 / a.H;
+  for (int turn = 0; row < a.T; row += step, turn ^= 1) {
+    float v[NC][kChunk], w[NC][kChunk];
 #pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    const int j = kChunk * (t + c * TPR), n = a.H - j;
-    uint32_t code[kChunk];
+    for (int c = 0; c < NC; ++c) {
+      x[c].values(v[c]);
+      if (ADD) {
+        float rv[kChunk];
+        r[c].values(rv);
 #pragma unroll
-    for (int i = 0; i < kChunk; ++i) code[i] = quot.code(NORM ? (P)v[c][i] * (P)g[c][i] : (P)v[c][i]) & keep;
-    int8_t* q = a.q + row * a.ld_q + j;
-    if (n >= kChunk) {
-      I8x8 w;
-      w.v[0] = code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24;
-      w.v[1] = code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24;
-      *reinterpret_cast<I8x8*>(q) = w;
-    } else {
+        for (int i = 0; i < kChunk; ++i) v[c][i] = Act<ACT>::rounded(v[c][i] + rv[i]);
+      }
+    }
+    if (row + step < a.T) load(row + step);
+    double sum = 0.0;
+    uint32_t top_bits = 0;  // of |p| as fp32: a NaN's are the largest
+    P top = 0;
 #pragma unroll
-      for (int i = 0; i < kChunk; ++i)
-        if (i < n) q[i] = (int8_t)code[i];
+    for (int c = 0; c < NC; ++c) {
+      const int j = kChunk * (t + c * TPR), n = a.H - j;
+      if (NORM) g[c].values(w[c]);
+      if (NORM) {
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) sum = fma((double)v[c][i], (double)v[c][i], sum);
+      }
+      if (ADD && a.x_out && n > 0) store8(static_cast<ACT*>(a.x_out) + row * a.ld_x_out + j, n, v[c]);
+      if (!NORM || a.q) {
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) {
+          const P p = NORM ? (P)v[c][i] * (P)w[c][i] : (P)v[c][i];
+          top_bits = max(top_bits, abs_bits((float)p));
+          if (NORM && sizeof(P) == 8) top = fmax((double)top, fabs((double)p));
+        }
+      }
+    }
+    if (NORM) sum = wave_sum(sum);
+    if (!NORM || a.q) {
+      top_bits = wave_max_u(top_bits);
+      if (NORM && sizeof(P) == 8) top = wave_max_pos(top);
+    }
+    if (kWaves > 1) {
+      // two sets, so that a wave that is a row ahead writes another than the others read
+      __shared__ double part_sum[2][kWaves];
+      __shared__ uint32_t part_bits[2][kWaves];
+      __shared__ P part_top[2][kWaves];
+      if (t % 64 == 0) {
+        part_sum[turn][t / 64] = sum;
+        part_bits[turn][t / 64] = top_bits;
+        part_top[turn][t / 64] = top;
+      }
+      __syncthreads();
+      sum = 0.0;
+#pragma unroll
+      for (int i = 0; i < kWaves; ++i) {
+        if (NORM) sum += part_sum[turn][i];
+        top_bits = max(top_bits, part_bits[turn][i]);
+        if (NORM && sizeof(P) == 8) top = fmax((double)top, (double)part_top[turn][i]);
+      }
+    }
+    if (!NORM || sizeof(P) == 4) top = __uint_as_float(top_bits);
+    const double rstd = NORM ? rsqrt64(fma(sum, inv_h, (double)a.eps)) : 1.0;
+    if (NORM && a.out) {
+      const float rs = (float)rstd;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int j = kChunk * (t + c * TPR), n = a.H - j;
+        float o[kChunk];
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i)
+          o[i] = sizeof(P) == 8 ? (float)((double)v[c][i] * (double)w[c][i] * rstd) : v[c][i] * w[c][i] * rs;
+        if (n > 0) store8(static_cast<ACT*>(a.out) + row * a.ld_out + j, n, o);
+      }
+    }
+    if (NORM && !a.q) continue;
+    // A NaN or an infinity in the row: scale NaN and codes 0, so that every product
+    // with the row is NaN. A row of (next to) nothing: scale and codes 0.
+    const bool bad = top_bits >= 0x7F800000u || (NORM && !(rstd > 0.0));
+    const bool none = top_bits < (27u << 23);  // under 2^-100
+    if (t == 0)
+      a.s[row] = bad ? __uint_as_float(0x7FC00000u) : none ? 0.f : (float)((double)top * rstd * (1.0 / 127.0));
+    const typename QuotientOf<P>::T quot(bad || none ? (P)1 : top);
+    const uint32_t keep = bad || none ? 0u : ~0u;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int j = kChunk * (t + c * TPR), n = a.H - j;
+      uint32_t code[kChunk];
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i) code[i] = quot.code(NORM ? (P)v[c][i] * (P)w[c][i] : (P)v[c][i]) & keep;
+      int8_t* q = a.q + row * a.ld_q + j;
+      if (n >= kChunk) {
+        I8x8 o;
+        o.v[0] = code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24;
+        o.v[1] = code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24;
+        *reinterpret_cast<I8x8*>(q) = o;
+      } else {
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i)
+          if (i < n) q[i] = (int8_t)code[i];
+      }
     }
   }
 }
 
+// Rows of up to 512 elements take a wave, of 2048 four waves and of 8192 eight (two chunks a
+// thread; 1024 threads of one chunk: 36.6 us against 35.8 for the norm of 2048 x 7168 bf16
+// rows with an fp32 addition and all outputs, 256 of four 43). The norm's workgroups are half
+// of what fits the 256 CUs and go on to further rows, their loads a row ahead (twice as many:
+// 37.5 us; one row each: 43 before rows were loaded ahead); the codes alone, with fewer
+// registers, take one row each (2048 x 7168 rows: 8.9 us, 10.6 as the norm does).
 template <typename ACT, bool NORM, int ADD>
 void launch(const RowArgs& a, hipStream_t s) {
 #define ROWS(TPR, BLOCK, NC)                                                                              \
-  hipLaunchKernelGGL((k_rows<ACT, NORM, ADD, TPR, BLOCK, NC>), dim3((a.T - 1) / (BLOCK / TPR) + 1), dim3(BLOCK), \
-                     0, s, a)
+  {                                                                                                       \
+    const int all = (a.T - 1) / (BLOCK / TPR) + 1, grid = NORM ? std::min(all, 128 * 2048 / BLOCK) : all; \
+    hipLaunchKernelGGL((k_rows<ACT, NORM, ADD, TPR, BLOCK, NC>), dim3(grid), dim3(BLOCK), 0, s, a);       \
+  }
   if (a.H <= 512)
-    ROWS(64, 256, 1);
+    ROWS(64, 256, 1)
   else if (a.H <= 2048)
-    ROWS(256, 256, 1);
+    ROWS(256, 256, 1)
   else if (a.H <= 8192)
-    ROWS(1024, 1024, 1);
+    ROWS(512, 512, 2)
   else
-    ROWS(1024, 1024, 2);
+    ROWS(1024, 1024, 2)
 #undef ROWS
 }
 

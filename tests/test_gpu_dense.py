@@ -201,6 +201,7 @@ MATMUL = [
     (255, 256, 112, "f32", 0), (640, 2300, 640, "bf16", 0),
     # enough tiles for each of the larger ones, ragged at both ends
     (2050, 6500, 144, "f32", 0), (2047, 7168, 1168, "bf16", 0), (1000, 6700, 272, "bf16", 16), (1023, 6401, 48, "f32", 0),
+    (3, 6200, 208, "f32", 0), (16, 7165, 96, "bf16", 0), (29, 6163, 1040, "f32", 16), (32, 100, 64, "bf16", 0),
     (520, 6401, 400, "f32", 0), (250, 7001, 784, "bf16", 0), (127, 7165, 320, "f32", 0),
 ]
 
@@ -300,6 +301,7 @@ FFN = [
     (16, 2048, 768, "f32", 0), (17, 400, 240, "bf16", 16), (61, 1040, 496, "f32", 0), (65, 256, 128, "bf16", 0),
     (130, 528, 80, "f32", 0), (300, 2048, 768, "bf16", 0), (1025, 512, 272, "f32", 32), (3, 64, 16384, "f32", 0),
     (257, 1024, 1040, "f32", 0), (96, 2064, 304, "bf16", 0),
+    (5, 96, 3280, "f32", 0), (19, 80, 3104, "bf16", 16), (31, 256, 96, "f32", 0),
     (2050, 96, 3264, "f32", 0), (1001, 272, 3360, "bf16", 0), (515, 144, 3280, "f32", 16), (251, 80, 3504, "bf16", 0),
 ]
 
