@@ -56,7 +56,12 @@ struct Int8Args {
 void launch_int8_matmul(const Int8Args& a, bool out_bf16, hipStream_t s);
 // out = h [T][N] fp32 = silu(gate) * up
 void launch_int8_gated(const Int8Args& a, hipStream_t s);
-// the same two for many rows
+// The gated block's second half for a few tokens: the codes of h [T][K] fp32 and their
+// product in one kernel (a.x and a.o.sx are not read); the same bits as launch_quantize_rows and
+// launch_int8_matmul. Only where int8_down_fits.
+bool int8_down_fits(int T, int K);
+void launch_int8_down(const Int8Args& a, const float* h, bool out_bf16, hipStream_t s);
+// the first two for many rows
 void launch_int8_gemm(const Int8Args& a, bool out_bf16, hipStream_t s);
 void launch_int8_gated_gemm(const Int8Args& a, hipStream_t s);
 

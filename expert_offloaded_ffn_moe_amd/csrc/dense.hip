@@ -279,6 +279,12 @@ moe_status moe_int8_ffn(const moe_int8_ffn_args* a, moe_stream stream) {
   const OnStreamDevice on(st);
   Int8Args g{a->q_x, a->q_gu, x.ld, gu.ld, T, I, H, {a->s_x, a->s_gu, nullptr, nullptr, nullptr, h, 0, 0, I}};
   launch_int8_gated(g, st);
+  Int8Args d{q, a->q_dn, I, dn.ld, T, H, I,
+             {s, a->s_dn, nullptr, a->y_in, a->res, a->out, e.y.ld, e.res.ld, e.out.ld}};
+  if (int8_down_fits(T, I)) {
+    launch_int8_down(d, h, a->out_dtype == MOE_ACT_BF16, st);
+    return launched("the gated block");
+  }
   RowArgs r{};
   r.x = h;
   r.q = q;
@@ -287,8 +293,6 @@ moe_status moe_int8_ffn(const moe_int8_ffn_args* a, moe_stream stream) {
   r.T = T;
   r.H = I;
   launch_quantize_rows(r, st);
-  const Int8Args d{q, a->q_dn, I, dn.ld, T, H, I,
-                   {s, a->s_dn, nullptr, a->y_in, a->res, a->out, e.y.ld, e.res.ld, e.out.ld}};
   launch_int8_matmul(d, a->out_dtype == MOE_ACT_BF16, st);
   return launched("the gated block");
 }

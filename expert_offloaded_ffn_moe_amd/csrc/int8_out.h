@@ -35,12 +35,18 @@ struct OutElem<true> {
   }
 };
 
+// The product's value before the output's rounding: each step rounded on its own, so that
+// every kernel gives a token the same bits, whatever other tokens a call has.
+__device__ __forceinline__ float int8_scaled(int acc, float sx, float sw, float bias) {
+#pragma clang fp contract(off)
+  return (float)acc * sx * sw + bias;
+}
+
 // out[t][n] of the product whose sum is `acc`
 template <bool BF16>
 __device__ __forceinline__ void int8_store(const Int8Out& o, int t, int n, float sx, float sw, int acc) {
   typedef typename OutElem<BF16>::T E;
-  float v = (float)acc * sx * sw;
-  if (o.bias) v += o.bias[n];
+  float v = int8_scaled(acc, sx, sw, o.bias ? o.bias[n] : 0.f);
   if (o.y) v += o.y[t * o.ld_y + n];
   if (o.res) v += OutElem<BF16>::load(static_cast<const E*>(o.res)[t * o.ld_res + n]);
   static_cast<E*>(o.out)[t * o.ld_out + n] = OutElem<BF16>::rounded(v);

@@ -16,7 +16,9 @@
 // 3%, four: 13.0.
 #include <hip/hip_runtime.h>
 
+#include "codes.h"
 #include "int8_out.h"
+#include "wave.h"
 
 namespace moe {
 namespace {
@@ -104,6 +106,115 @@ __global__ __launch_bounds__(64 * kWaves) void k_int8_skinny(Int8Args a) {
   }
 }
 
+// The second half of the gated block for up to 16 tokens: as k_int8_skinny, with the
+// activations' codes formed in LDS from h first, while the first weights are on their way.
+// Each workgroup reads and codes all of h, which costs less than a launch of its own for as
+// long as h is small. A row of h is shared by kWaves / T waves at least, in registers of
+// kHeld elements a lane.
+constexpr int kHeld = 32;
+constexpr int kDownTokens = 16, kDownElements = 16384;
+
+__host__ __device__ constexpr int waves_per_row(int T) { return T == 1 ? 8 : T == 2 ? 4 : T <= 4 ? 2 : 1; }
+
+template <int CT, bool BF16>
+__global__ __launch_bounds__(64 * kWaves) void k_int8_down(Int8Args a, const float* h) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t codes[];  // [T][K + 16]: rows on different banks
+  __shared__ i32x4 part[kWaves][CT][64];
+  __shared__ float scale[kDownTokens];
+  __shared__ uint32_t tops[kWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int i = lane & 15, q = lane >> 4;
+  const int n0 = blockIdx.x * 16 * CT, ld = a.K + 16;
+  gi32x4* w[CT];
+#pragma unroll
+  for (int c = 0; c < CT; ++c) w[c] = (gi32x4*)(a.w + min(n0 + 16 * c + i, a.N - 1) * a.ld_w);
+  const int pieces = a.K / 16, blocks = (pieces + 4 * kStep - 1) / (4 * kStep);
+  i32x4 wv[CT][kStep];
+  auto load = [&](int b) {
+#pragma unroll
+    for (int s = 0; s < kStep; ++s)
+#pragma unroll
+      for (int c = 0; c < CT; ++c) wv[c][s] = w[c][min(b * 4 * kStep + 4 * s + q, pieces - 1)];
+  };
+  load(min(wave, blocks - 1));
+
+  const int wpr = waves_per_row(a.T), part_of_row = (wave % wpr) * 64 + lane;
+  for (int r0 = 0; r0 < a.T; r0 += kWaves / wpr) {
+    const int row = r0 + wave / wpr;
+    const bool mine = row < a.T;
+    float v[kHeld];
+    uint32_t top = 0;
+    if (mine) {
+#pragma unroll
+      for (int k = 0; k < kHeld / 4; ++k) {
+        const int j = 4 * (part_of_row + k * 64 * wpr);
+        const float4 f = j < a.K ? *reinterpret_cast<const float4*>(h + (int64_t)row * a.K + j) : float4{0.f, 0.f, 0.f, 0.f};
+        v[4 * k] = f.x;
+        v[4 * k + 1] = f.y;
+        v[4 * k + 2] = f.z;
+        v[4 * k + 3] = f.w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = max(top, abs_bits(v[4 * k + e]));
+      }
+    }
+    top = wave_max_u(top);
+    if (wpr > 1) {  // one round of rows then
+      if (lane == 0) tops[wave] = top;
+      __syncthreads();
+      for (int k = 0; k < wpr; ++k) top = max(top, tops[wave / wpr * wpr + k]);
+    }
+    if (!mine) continue;
+    const float size = __uint_as_float(top);
+    const bool none = top >= kNotFinite || top < kNoCodes;
+    if (lane == 0) scale[row] = code_scale(top, (double)size);  // every wave of the row the same
+    const Quotient64 quot(none ? 1.0 : (double)size);
+    const uint32_t keep = none ? 0u : ~0u;
+#pragma unroll
+    for (int k = 0; k < kHeld / 4; ++k) {
+      const int j = 4 * (part_of_row + k * 64 * wpr);
+      if (j >= a.K) break;
+      uint32_t c = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c |= quot.code((double)v[4 * k + e]) << (8 * e);
+      *reinterpret_cast<uint32_t*>(codes + row * ld + j) = c & keep;
+    }
+  }
+  __syncthreads();
+
+  const i32x4* x = reinterpret_cast<const i32x4*>(codes + min(i, a.T - 1) * ld);
+  i32x4 acc[CT];
+#pragma unroll
+  for (int c = 0; c < CT; ++c) acc[c] = i32x4{0, 0, 0, 0};
+  for (int b = wave; b < blocks; b += kWaves) {
+    i32x4 now[CT][kStep];
+#pragma unroll
+    for (int c = 0; c < CT; ++c)
+#pragma unroll
+      for (int s = 0; s < kStep; ++s) now[c][s] = wv[c][s];
+    if (b + kWaves < blocks) load(b + kWaves);
+#pragma unroll
+    for (int s = 0; s < kStep; ++s) {
+      const int p = b * 4 * kStep + 4 * s + q;
+      i32x4 xv = x[min(p, pieces - 1)];
+      if (p >= pieces) xv = i32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int c = 0; c < CT; ++c) acc[c] = mfma16(now[c][s], xv, acc[c]);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < CT; ++c) part[wave][c][lane] = acc[c];
+  __syncthreads();
+  for (int o = threadIdx.x; o < CT * 16 * 16; o += 64 * kWaves) {
+    const int r = o % 16, c = o / 16 % CT, t = o / (16 * CT), n = n0 + c * 16 + r;
+    if (t >= a.T || n >= a.N) continue;
+    const int* p = reinterpret_cast<const int*>(&part[0][c][16 * (r / 4) + t]) + r % 4;
+    int sum = 0;
+#pragma unroll
+    for (int v = 0; v < kWaves; ++v) sum += p[v * CT * 64 * 4];
+    int8_store<BF16>(a.o, t, n, scale[t], a.o.sw[n], sum);
+  }
+}
+
 // Two blocks a workgroup share each load of the activations, if that leaves three quarters of
 // the 256 CUs a workgroup: 16 tokens on 7168 x 7168 14.2 us (one block: 16.9), on 4096 x 2048
 // 5.2 us (4.0).
@@ -135,6 +246,29 @@ void launch_int8_matmul(const Int8Args& a, bool out_bf16, hipStream_t s) {
     skinny<false, true>(a, s);
   else
     skinny<false, false>(a, s);
+}
+
+bool int8_down_fits(int T, int K) {
+  return T <= kDownTokens && (int64_t)T * K <= kDownElements && K <= 64 * kHeld * waves_per_row(T);
+}
+
+void launch_int8_down(const Int8Args& a, const float* h, bool out_bf16, hipStream_t s) {
+  const int blocks = (a.N - 1) / 16 + 1;
+  const size_t lds = (size_t)a.T * (a.K + 16);
+#define DOWN(CT, BF16) \
+  hipLaunchKernelGGL((k_int8_down<CT, BF16>), dim3((blocks - 1) / CT + 1), dim3(64 * kWaves), lds, s, a, h)
+  if (blocks >= 2 * 192) {
+    if (out_bf16)
+      DOWN(2, true);
+    else
+      DOWN(2, false);
+  } else {
+    if (out_bf16)
+      DOWN(1, true);
+    else
+      DOWN(1, false);
+  }
+#undef DOWN
 }
 
 void launch_int8_gated(const Int8Args& a, hipStream_t s) {

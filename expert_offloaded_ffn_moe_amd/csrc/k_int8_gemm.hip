@@ -81,7 +81,7 @@ __device__ __forceinline__ void store_rows(const Int8Args& a, int t0, int n, con
         for (int e = 0; e < 4; ++e) v[p][e] = gated_value(s[e], u[e], sx[r], sw[e], su[e]);
       } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[p][e] = (float)s[e] * sx[r] * sw[e] + bias[e];
+        for (int e = 0; e < 4; ++e) v[p][e] = int8_scaled(s[e], sx[r], sw[e], bias[e]);
       }
     }
     if (!GATED && a.o.y) {

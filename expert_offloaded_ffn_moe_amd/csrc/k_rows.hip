@@ -22,6 +22,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "codes.h"
 #include "dense.h"
 #include "wave.h"
 
@@ -176,46 +177,7 @@ __device__ __forceinline__ double wave_max_pos(double v) {
   return lane63(v);
 }
 
-__device__ __forceinline__ uint32_t wave_max_u(uint32_t v) {
-  v = max(v, (uint32_t)dpp<kDppXor1, 0xF>(0, (int)v));
-  v = max(v, (uint32_t)dpp<kDppXor2, 0xF>(0, (int)v));
-  v = max(v, (uint32_t)dpp<kDppHalfMirror, 0xF>(0, (int)v));
-  v = max(v, (uint32_t)dpp<kDppMirror, 0xF>(0, (int)v));
-  v = max(v, (uint32_t)dpp<kDppBcast15, 0xA>(0, (int)v));
-  v = max(v, (uint32_t)dpp<kDppBcast31, 0xC>(0, (int)v));
-  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
-}
-
 __device__ __forceinline__ uint32_t abs_bits(float f) { return __float_as_uint(f) & 0x7FFFFFFFu; }
-__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
-
-// Codes under the row's largest size: a = 127 p 2^(1-e) and b = max|p| 2^(1-e) in [2, 4), so
-// that nothing over- or underflows; q = a y, corrected once, is a / b rounded correctly.
-// Adding 1.5 2^23 (2^52) rounds to a whole number, half to even, and leaves its two's
-// complement in the low bits.
-struct Quotient32 {
-  float c, b, y;
-  __device__ __forceinline__ explicit Quotient32(float top) {
-    const float f = power_of_two(128 - (int)(__float_as_uint(top) >> 23));
-    c = 127.f * f;
-    b = top * f;
-    y = 1.f / b;
-  }
-  __device__ __forceinline__ uint32_t code(float p) const {
-    const float a = p * c;
-    const float q = a * y;
-    return __float_as_uint(fmaf(fmaf(-b, q, a), y, q) + 12582912.f) & 0xFFu;
-  }
-};
-struct Quotient64 {
-  double b, y;
-  __device__ __forceinline__ explicit Quotient64(double top) : b(top), y(1.0 / top) {}
-  __device__ __forceinline__ uint32_t code(double p) const {
-    const double a = 127.0 * p;
-    const double q = a * y;
-    return (uint32_t)__double_as_longlong(fma(fma(-b, q, a), y, q) + 6755399441055744.0) & 0xFFu;
-  }
-};
 template <typename P>
 struct QuotientOf;
 template <>
@@ -339,12 +301,11 @@ __global__ __launch_bounds__(BLOCK) void k_rows(RowArgs a) {
     if (NORM && !a.q) continue;
     // A NaN or an infinity in the row: scale NaN and codes 0, so that every product
     // with the row is NaN. A row of (next to) nothing: scale and codes 0.
-    const bool bad = top_bits >= 0x7F800000u || (NORM && !(rstd > 0.0));
-    const bool none = top_bits < (27u << 23);  // under 2^-100
-    if (t == 0)
-      a.s[row] = bad ? __uint_as_float(0x7FC00000u) : none ? 0.f : (float)((double)top * rstd * (1.0 / 127.0));
-    const typename QuotientOf<P>::T quot(bad || none ? (P)1 : top);
-    const uint32_t keep = bad || none ? 0u : ~0u;
+    if (NORM && !(rstd > 0.0)) top_bits = kNotFinite;
+    const bool none = top_bits >= kNotFinite || top_bits < kNoCodes;
+    if (t == 0) a.s[row] = code_scale(top_bits, (double)top * rstd);
+    const typename QuotientOf<P>::T quot(none ? (P)1 : top);
+    const uint32_t keep = none ? 0u : ~0u;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int j = kChunk * (t + c * TPR), n = a.H - j;

@@ -62,6 +62,17 @@ __device__ __forceinline__ float wave_max(float v) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
+// Maximum over the wave of unsigned values, broadcast (rows left out contribute 0).
+__device__ __forceinline__ uint32_t wave_max_u(uint32_t v) {
+  v = max(v, (uint32_t)dpp<kDppXor1, 0xF>(0, (int)v));
+  v = max(v, (uint32_t)dpp<kDppXor2, 0xF>(0, (int)v));
+  v = max(v, (uint32_t)dpp<kDppHalfMirror, 0xF>(0, (int)v));
+  v = max(v, (uint32_t)dpp<kDppMirror, 0xF>(0, (int)v));
+  v = max(v, (uint32_t)dpp<kDppBcast15, 0xA>(0, (int)v));
+  v = max(v, (uint32_t)dpp<kDppBcast31, 0xC>(0, (int)v));
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
 // One step of the arg-max: take (ov, oid) when it comes first in the order
 // (value descending, id ascending).
 __device__ __forceinline__ void better(float& v, int& id, float ov, int oid) {

@@ -301,6 +301,9 @@ FFN = [
     (16, 2048, 768, "f32", 0), (17, 400, 240, "bf16", 16), (61, 1040, 496, "f32", 0), (65, 256, 128, "bf16", 0),
     (130, 528, 80, "f32", 0), (300, 2048, 768, "bf16", 0), (1025, 512, 272, "f32", 32), (3, 64, 16384, "f32", 0),
     (257, 1024, 1040, "f32", 0), (96, 2064, 304, "bf16", 0),
+    # the second product on codes formed beside it, at the ends of that
+    (1, 64, 16384, "f32", 0), (2, 48, 8192, "f32", 0), (4, 80, 4096, "bf16", 0), (3, 96, 4112, "f32", 0), (16, 256, 1024, "f32", 16),
+    (16, 6160, 16, "bf16", 0), (7, 128, 2048, "f32", 0), (9, 6145 + 15, 96, "f32", 0), (16, 128, 1040, "f32", 0),
     (5, 96, 3280, "f32", 0), (19, 80, 3104, "bf16", 16), (31, 256, 96, "f32", 0),
     (2050, 96, 3264, "f32", 0), (1001, 272, 3360, "bf16", 0), (515, 144, 3280, "f32", 16), (251, 80, 3504, "bf16", 0),
 ]
@@ -353,6 +356,31 @@ def test_int8_ffn_zero_and_nan_tokens(moe):
         nan = out.isnan()
         assert nan[4].all() and int(nan.sum()) == H
         assert torch.equal(out[2], res[2]) and torch.equal(out[5], res[5])
+
+
+@pytest.mark.parametrize("H,I", [(512, 272), (2048, 768)])
+def test_a_token_alone_or_among_others(moe, H, I):
+    """A token's output does not depend on the call's other tokens: bit for bit the same in
+    batches that take different kernels and tiles."""
+    T = 700
+    qx, sx, qgu, sgu, qdn, sdn = _ffn_case(T, H, I, 0, 5)
+    g = _gen(6)
+    y, res, bias = _rn(g, T, H), _rn(g, T, H).bfloat16(), _rn(g, 2 * I)
+
+    def ffn(a, b):
+        out = torch.empty(b - a, H, device="cuda", dtype=torch.bfloat16)
+        ws = torch.empty(moe.int8_ffn_workspace(b - a, H, I), dtype=torch.uint8, device="cuda")
+        return moe.int8_ffn(qx.m[a:b], sx[a:b], qgu.m, sgu, qdn.m, sdn, out, ws, y_in=y[a:b], res=res[a:b])
+
+    def matmul(a, b):
+        out = torch.empty(b - a, 2 * I, device="cuda")
+        return moe.int8_matmul(qx.m[a:b], sx[a:b], qgu.m, sgu, out, bias=bias)
+
+    for f in (ffn, matmul):
+        whole = f(0, T)
+        for n in (1, 2, 5, 16, 24, 33, 100, 260):
+            for a in (0, 333, T - n):
+                assert torch.equal(f(a, a + n), whole[a:a + n]), n
 
 
 def test_binding_refuses_on_the_gpu(moe):
