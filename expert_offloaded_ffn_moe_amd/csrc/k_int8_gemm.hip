@@ -1,10 +1,11 @@
 // 8-bit matrix product for many rows, and its gated form: tiles of tokens x channels on
-// v_mfma_i32_32x32x32_i8.
+// v_mfma_i32_16x16x64_i8.
 //
-// Lane layout of the 32x32x32 MFMA: lane l supplies 16 bytes of row l % 32 of each
-// operand at K offset 16 (l / 32), and receives the sums of column l % 32 and rows
-// 8 (v / 4) + 4 (l / 32) + v % 4 (v = 0..15). Tokens are the row operand and channels the
-// column operand, so that 32 lanes store neighbouring channels.
+// Lane layout of the 16x16x64 MFMA: lane l supplies 16 bytes of row l % 16 of each operand at
+// K offset 16 (l / 16), and receives the sums of column l % 16 and rows 4 (l / 16) .. + 3.
+// Tokens are the row operand and channels the column operand. (On random codes the matrix
+// pipes are held by power: 256 CUs of this instruction alone run at 2.1 GHz and 4.2 POPS, of
+// 32x32x32 at 1.75 GHz and 3.7.)
 //
 // A tile of BM tokens x BN channels runs over K in steps of BK bytes (64 or 128) through a
 // ring of LDS buffers, filled by loads that go from memory to LDS directly (16 bytes a lane,
@@ -13,9 +14,10 @@
 // fetches the piece that belongs at its place, and sixteen lanes that read one piece of
 // sixteen rows then use every bank once. Pieces past K come from a line of zeros.
 //
-// A step is two halves. The operands of one are read from LDS while the products of the
-// other run; the barrier that frees the oldest buffer and opens the next stands between the
-// two, so that it, too, is covered by products.
+// A step is two halves: of 64 bytes of K each where a step has 128, else of half of the rows
+// each. The operands of one are read from LDS while the products of the other run; the
+// barrier that frees the oldest buffer and opens the next stands between the two, so that
+// it, too, is covered by products.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -110,9 +112,8 @@ __device__ __forceinline__ void store_rows(const Int8Args& a, int t0, int n, con
   }
 }
 
-// WM x WN waves, each TM x TN blocks of 32 x 32; RING buffers. GATED: of every 32 channels
-// of the tile the first 16 are gate rows and the others the same rows of up, and h is
-// stored in fp32.
+// WM x WN waves, each 32 TM x 32 TN; RING buffers. GATED: of every 32 channels of the tile
+// the first 16 are gate rows and the others the same rows of up, and h is stored in fp32.
 template <int WM, int WN, int TM, int TN, int BK, int RING, bool GATED, bool BF16>
 __global__ __launch_bounds__(64 * WM* WN) void k_int8_gemm(Int8Args a, int mtiles) {
   constexpr int kWaves = WM * WN, BM = 32 * TM * WM, BN = 32 * TN * WN;
@@ -129,9 +130,9 @@ __global__ __launch_bounds__(64 * WM* WN) void k_int8_gemm(Int8Args a, int mtile
   for (int i = threadIdx.x; i < BM; i += 64 * kWaves) rows_sx[i] = a.o.sx[min(m0 + i, a.T - 1)];
   // this lane's channels in the epilogue: columns c .. c + 3 of the wave's (gated: gate
   // columns; up's are 16 on), their scales and bias
-  constexpr int kCols = 32 * TN, kRow = kCols + 8;
+  constexpr int kCols = 32 * TN, kRow = kCols + 4;
   constexpr int kLanes = kCols / 4 / (GATED ? 2 : 1), kRows = 64 / kLanes;  // lanes of a row, rows a pass
-  const int wm = wave / WN, wn = wave % WN, half = lane >> 5, l32 = lane & 31;
+  const int wm = wave / WN, wn = wave % WN, l16 = lane & 15, quarter = lane >> 4;
   const int lc = lane % kLanes * 4, c = GATED ? lc / 16 * 32 + lc % 16 : lc;
   const int n = n0 + wn * (GATED ? kCols / 2 : kCols) + lc;
   float sw[4], su[4] = {0.f, 0.f, 0.f, 0.f}, bias[4] = {0.f, 0.f, 0.f, 0.f};
@@ -159,63 +160,76 @@ __global__ __launch_bounds__(64 * WM* WN) void k_int8_gemm(Int8Args a, int mtile
   // the part'th of `parts` parts of the next step's pieces into buffer `buf` (past the last
   // step: zeros)
   auto stage = [&](int buf, int part, int parts) {
+    if (part == 0) {
+      if (kat + BK > a.K) {  // the last of K is in it, or nothing
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+          if (kat + at[i] >= a.K) p[i] = zeros;
+      }
+      kat += BK;
+    }
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       if (i < kLoads * part / parts || i >= kLoads * (part + 1) / parts) continue;
       const int to = i < kLoadsA ? (wave * kLoadsA + i) * 1024 : BM * BK + (wave * kLoadsB + i - kLoadsA) * 1024;
-      load_to_lds(kat + at[i] < a.K ? p[i] : zeros, ring + buf * (BM + BN) * BK + to);
+      load_to_lds(p[i], ring + buf * (BM + BN) * BK + to);
       p[i] += BK;
     }
-    if (part == parts - 1) kat += BK;
   };
 
-  i32x16 acc[TM][TN];
+  // blocks of 16 rows and columns of the wave, and the row blocks of a half
+  constexpr int kMB = 2 * TM, kNB = 2 * TN, kHalfMB = BK == 128 ? kMB : kMB / 2;
+  i32x4 acc[kMB][kNB];
 #pragma unroll
-  for (int i = 0; i < TM; ++i)
+  for (int i = 0; i < kMB; ++i)
 #pragma unroll
-    for (int j = 0; j < TN; ++j) acc[i][j] = i32x16{};
-  constexpr int kHalf = BK / 64;  // MFMA steps of a half
-  struct Operands {
-    i32x4 a[kHalf][TM], b[kHalf][TN];
+    for (int j = 0; j < kNB; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+  struct Rows {
+    i32x4 v[kHalfMB];
   };
-  // the part'th of `parts` parts of a half's operands
-  auto fetch = [&](Operands& f, int buf, int h, int part, int parts) {
-    constexpr int kAll = kHalf * (TN + TM);
-#pragma unroll
-    for (int x = 0; x < kAll; ++x) {
-      if (x < kAll * part / parts || x >= kAll * (part + 1) / parts) continue;
-      const int s = x / (TN + TM), i = x % (TN + TM);
-      const int off = l32 * BK + (((2 * (h * kHalf + s) + half) ^ swizzle<BK>(l32)) << 4);
-      if (i < TN)
-        f.b[s][i] = *reinterpret_cast<const i32x4*>(&sh[buf][BM * BK + (wn * TN + i) * 32 * BK + off]);
-      else
-        f.a[s][i - TN] = *reinterpret_cast<const i32x4*>(&sh[buf][(wm * TM + i - TN) * 32 * BK + off]);
-    }
+  struct Cols {
+    i32x4 v[kNB];
   };
-  auto products = [&](const Operands& f, int x) {
-    const int s = x / TM, i = x % TM;
+  // the part'th of `parts` parts of a half's rows, and of its columns
+  auto fetch_rows = [&](Rows& f, int buf, int h, int part, int parts) {
+    const int r0 = wm * 32 * TM + (BK == 128 ? 0 : h * kHalfMB * 16);
+    const int off = l16 * BK + (((BK == 128 ? 4 * h : 0) + quarter ^ swizzle<BK>(l16)) << 4);
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
-      acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.a[s][i], f.b[s][j], acc[i][j], 0, 0, 0);
+    for (int i = 0; i < kHalfMB; ++i)
+      if (i >= kHalfMB * part / parts && i < kHalfMB * (part + 1) / parts)
+        f.v[i] = *reinterpret_cast<const i32x4*>(&sh[buf][(r0 + 16 * i) * BK + off]);
   };
-  // A half has kSlots slots of TN products; the operands of the next are asked for in the
+  auto fetch_cols = [&](Cols& f, int buf, int h, int part, int parts) {
+    const int off = l16 * BK + (((BK == 128 ? 4 * h : 0) + quarter ^ swizzle<BK>(l16)) << 4);
+#pragma unroll
+    for (int j = 0; j < kNB; ++j)
+      if (j >= kNB * part / parts && j < kNB * (part + 1) / parts)
+        f.v[j] = *reinterpret_cast<const i32x4*>(&sh[buf][(BM + wn * 32 * TN + 16 * j) * BK + off]);
+  };
+  auto products = [&](const Rows& r, const Cols& c, int h, int i) {
+    const int at_row = BK == 128 ? i : h * kHalfMB + i;
+#pragma unroll
+    for (int j = 0; j < kNB; ++j) acc[at_row][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(r.v[i], c.v[j], acc[at_row][j], 0, 0, 0);
+  };
+  // A half has kHalfMB slots of kNB products; the operands of the next are asked for in the
   // first of them, so that they are in when its products start, and loads follow.
-  constexpr int kSlots = TM * kHalf, kReadSlots = kSlots >= 4 ? 2 : 1, kLoadSlot0 = kSlots > kReadSlots ? kReadSlots : 0;
-  const int steps = (a.K + BK - 1) / BK;
-#pragma unroll
-  for (int r = 0; r < RING; ++r) stage(r, 0, 1);
-  wait_loads_but<(RING - 1) * kLoads>();
-  __builtin_amdgcn_s_barrier();
-  Operands f0, f1;
-  fetch(f0, 0, 0, 0, 1);
+  constexpr int kReadSlots = kHalfMB / 2;
+  Rows r0, r1;
+  Cols c0, c1;
   int buf = 0;
-  for (int k = 0; k < steps; ++k) {
+  // One step: rows r0 and columns `now` are in registers at its start, those of the next
+  // step's first half at its end (columns in `next`, which with BK = 128 holds the second
+  // half's in between).
+  auto step = [&](Cols& now, Cols& next) {
 #pragma unroll
-    for (int i = 0; i < kSlots; ++i) {
+    for (int i = 0; i < kHalfMB; ++i) {
       __builtin_amdgcn_sched_barrier(0);
-      products(f0, i);
+      products(r0, now, 0, i);
       __builtin_amdgcn_sched_barrier(0);
-      if (i < kReadSlots) fetch(f1, buf, 1, i, kReadSlots);
+      if (i < kReadSlots) {
+        if (BK == 128) fetch_cols(next, buf, 1, i, kReadSlots);
+        fetch_rows(r1, buf, 1, i, kReadSlots);
+      }
     }
     __builtin_amdgcn_sched_barrier(0);
     const int done = buf;  // every wave has all of it in registers at the barrier
@@ -223,17 +237,34 @@ __global__ __launch_bounds__(64 * WM* WN) void k_int8_gemm(Int8Args a, int mtile
     wait_loads_but<(RING - 2) * kLoads>();  // the next buffer is in, this one's operands too
     __builtin_amdgcn_s_barrier();
 #pragma unroll
-    for (int i = 0; i < kSlots; ++i) {
+    for (int i = 0; i < kHalfMB; ++i) {
       __builtin_amdgcn_sched_barrier(0);
-      products(f1, i);
+      products(r1, BK == 128 ? next : now, 1, i);
       __builtin_amdgcn_sched_barrier(0);
-      if (i < kReadSlots) fetch(f0, buf, 0, i, kReadSlots);
-      if (i >= kLoadSlot0) stage(done, i - kLoadSlot0, kSlots - kLoadSlot0);
+      if (i < kReadSlots) {
+        fetch_cols(BK == 128 ? now : next, buf, 0, i, kReadSlots);
+        fetch_rows(r0, buf, 0, i, kReadSlots);
+      }
+      if (i >= kReadSlots) stage(done, i - kReadSlots, kHalfMB - kReadSlots);
+    }
+  };
+#pragma unroll
+  for (int r = 0; r < RING; ++r) stage(r, 0, 1);
+  wait_loads_but<(RING - 1) * kLoads>();
+  __builtin_amdgcn_s_barrier();
+  fetch_rows(r0, 0, 0, 0, 1);
+  fetch_cols(c0, 0, 0, 0, 1);
+  if (BK == 128) {
+    for (int k = 0; k < a.K; k += BK) step(c0, c1);
+  } else {  // two steps a turn, so that each set of columns has its registers; the second may be zeros
+    for (int k = 0; k < a.K; k += 2 * BK) {
+      step(c0, c1);
+      step(c1, c0);
     }
   }
 
-  // Each wave turns its sums in LDS, a block of 32 rows at a time (rows 32 bytes longer, so
-  // that the two rows of a write use different banks), and reads four neighbouring
+  // Each wave turns its sums in LDS, a block of 32 rows at a time (rows 16 bytes longer, so
+  // that the four rows of a write use different banks), and reads four neighbouring
   // channels of a row a lane: whole lines are read and written from there on.
   wait_loads_but<0>();
   __syncthreads();
@@ -244,9 +275,11 @@ __global__ __launch_bounds__(64 * WM* WN) void k_int8_gemm(Int8Args a, int mtile
   for (int i = 0; i < TM; ++i) {
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
+    for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int v = 0; v < 16; ++v) turn[(8 * (v / 4) + 4 * half + v % 4) * kRow + 32 * j + l32] = acc[i][j][v];
+      for (int j = 0; j < kNB; ++j)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) turn[(16 * b + 4 * quarter + v) * kRow + 16 * j + l16] = acc[2 * i + b][j][v];
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     const int r0 = (wm * TM + i) * 32 + lane / kLanes;  // this lane's first row in the tile
