@@ -23,8 +23,8 @@
 namespace moe {
 namespace {
 
-// Tokens up to which these kernels run. 32 tokens on 4096 x 2048: 5.1 us, in tiles 7.5; on
-// 7168 x 7168: 18.6, in tiles 17.4; 64 tokens: 33.6, in tiles 17.3.
+// Tokens up to which these kernels run. 32 tokens on 4096 x 2048: 5.1 us, in tiles 6.5; on
+// 7168 x 7168: 18.6, in tiles 14.0 (16 tokens 14.2); 64 tokens on these: 7.1 and 28.
 constexpr int kSkinnyRows = 32;
 constexpr int kWaves = 8;  // of a workgroup, splitting K
 constexpr int kStep = 2;   // 64-byte K steps of a wave's load block

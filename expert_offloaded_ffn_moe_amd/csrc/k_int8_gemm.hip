@@ -62,8 +62,8 @@ __device__ __forceinline__ void load_to_lds(const int8_t* from, uint32_t to) {
 
 // PASSES rows, ROWS apart, of four channels each, from their sums in LDS. WHOLE: every row
 // and channel is one of the matrix's, and what the rows need is loaded for all of them
-// before it is used.
-template <bool GATED, bool BF16, int PASSES, int ROWS, int LDROW, bool WHOLE>
+// before it is used. A sum is in PARTS parts, PART ints apart.
+template <bool GATED, bool BF16, int PASSES, int ROWS, int LDROW, int PARTS, int PART, bool WHOLE>
 __device__ __forceinline__ void store_rows(const Int8Args& a, int t0, int n, const float* sx, const int* from,
                                            const float* sw, const float* su, const float* bias) {
   typedef typename OutElem<BF16>::T E;
@@ -76,9 +76,11 @@ __device__ __forceinline__ void store_rows(const Int8Args& a, int t0, int n, con
 #pragma unroll
     for (int p = 0; p < kAt; ++p) {
       const int r = (p0 + p) * ROWS;
-      const i32x4 s = *reinterpret_cast<const i32x4*>(from + r * LDROW);
+      i32x4 s = *reinterpret_cast<const i32x4*>(from + r * LDROW);
+      for (int k = 1; k < PARTS; ++k) s += *reinterpret_cast<const i32x4*>(from + k * PART + r * LDROW);
       if (GATED) {
-        const i32x4 u = *reinterpret_cast<const i32x4*>(from + r * LDROW + 16);
+        i32x4 u = *reinterpret_cast<const i32x4*>(from + r * LDROW + 16);
+        for (int k = 1; k < PARTS; ++k) u += *reinterpret_cast<const i32x4*>(from + k * PART + r * LDROW + 16);
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[p][e] = gated_value(s[e], u[e], sx[r], sw[e], su[e]);
       } else {
@@ -112,22 +114,25 @@ __device__ __forceinline__ void store_rows(const Int8Args& a, int t0, int n, con
   }
 }
 
-// WM x WN waves, each 32 TM x 32 TN; RING buffers. GATED: of every 32 channels of the tile
+// WM x WN waves, each 32 TM x 32 TN; RING buffers. KG such groups of waves take the steps of
+// K in turn, each with buffers of its own, and add their sums at the end. GATED: of every 32 channels of the tile
 // the first 16 are gate rows and the others the same rows of up, and h is stored in fp32.
-template <int WM, int WN, int TM, int TN, int BK, int RING, bool GATED, bool BF16>
-__global__ __launch_bounds__(64 * WM* WN) void k_int8_gemm(Int8Args a, int mtiles) {
+template <int WM, int WN, int TM, int TN, int BK, int RING, int KG, bool GATED, bool BF16>
+__global__ __launch_bounds__(64 * WM* WN* KG) void k_int8_gemm(Int8Args a, int mtiles) {
   constexpr int kWaves = WM * WN, BM = 32 * TM * WM, BN = 32 * TN * WN;
   constexpr int kPieces = BK / 16, kRowsPer = 64 / kPieces;  // pieces of a row; rows of a load instruction
   constexpr int kLoadsA = BM / kRowsPer / kWaves, kLoadsB = BN / kRowsPer / kWaves;  // instructions of a wave per step
   static_assert(kLoadsA * kRowsPer * kWaves == BM && kLoadsB * kRowsPer * kWaves == BN, "rows divide among the waves");
   constexpr int kLoads = kLoadsA + kLoadsB;
-  __shared__ __attribute__((aligned(1024))) uint8_t sh[RING][(BM + BN) * BK];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  __shared__ __attribute__((aligned(1024))) uint8_t all[KG][RING][(BM + BN) * BK];
+  const int lane = threadIdx.x & 63, wave_id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = KG == 1 ? 0 : wave_id / kWaves, wave = KG == 1 ? wave_id : wave_id % kWaves;
+  uint8_t(*sh)[(BM + BN) * BK] = all[group];
   const int tile = xcd_order(blockIdx.x, gridDim.x);
   const int m0 = tile % mtiles * BM, n0 = tile / mtiles * (GATED ? BN / 2 : BN);
 
   __shared__ float rows_sx[BM];
-  for (int i = threadIdx.x; i < BM; i += 64 * kWaves) rows_sx[i] = a.o.sx[min(m0 + i, a.T - 1)];
+  for (int i = threadIdx.x; i < BM; i += 64 * kWaves * KG) rows_sx[i] = a.o.sx[min(m0 + i, a.T - 1)];
   // this lane's channels in the epilogue: columns c .. c + 3 of the wave's (gated: gate
   // columns; up's are 16 on), their scales and bias
   constexpr int kCols = 32 * TN, kRow = kCols + 4;
@@ -152,11 +157,11 @@ __global__ __launch_bounds__(64 * WM* WN) void k_int8_gemm(Int8Args a, int mtile
     int64_t row = in_a ? min(m0 + r, a.T - 1) : min(n0 + r, a.N - 1);
     if (GATED && !in_a) row = (int64_t)min(n0 + r / 32 * 16 + r % 16, a.N - 1) + (r & 16 ? a.N : 0);
     at[i] = (lane % kPieces ^ swizzle<BK>(r)) * 16;
-    p[i] = (in_a ? a.x + row * a.ld_x : a.w + row * a.ld_w) + at[i];
+    p[i] = (in_a ? a.x + row * a.ld_x : a.w + row * a.ld_w) + group * BK + at[i];
   }
   const int8_t* zeros = reinterpret_cast<const int8_t*>(&zero_piece);
   const uint32_t ring = (uint32_t)(uintptr_t)(lvoid*)&sh[0][0];
-  int kat = 0;  // K offset of the next step to load
+  int kat = group * BK;  // K offset of the next step to load
   // the part'th of `parts` parts of the next step's pieces into buffer `buf` (past the last
   // step: zeros)
   auto stage = [&](int buf, int part, int parts) {
@@ -166,14 +171,14 @@ __global__ __launch_bounds__(64 * WM* WN) void k_int8_gemm(Int8Args a, int mtile
         for (int i = 0; i < kLoads; ++i)
           if (kat + at[i] >= a.K) p[i] = zeros;
       }
-      kat += BK;
+      kat += KG * BK;
     }
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       if (i < kLoads * part / parts || i >= kLoads * (part + 1) / parts) continue;
       const int to = i < kLoadsA ? (wave * kLoadsA + i) * 1024 : BM * BK + (wave * kLoadsB + i - kLoadsA) * 1024;
       load_to_lds(p[i], ring + buf * (BM + BN) * BK + to);
-      p[i] += BK;
+      p[i] += KG * BK;
     }
   };
 
@@ -255,9 +260,9 @@ __global__ __launch_bounds__(64 * WM* WN) void k_int8_gemm(Int8Args a, int mtile
   fetch_rows(r0, 0, 0, 0, 1);
   fetch_cols(c0, 0, 0, 0, 1);
   if (BK == 128) {
-    for (int k = 0; k < a.K; k += BK) step(c0, c1);
+    for (int k = 0; k < a.K; k += KG * BK) step(c0, c1);
   } else {  // two steps a turn, so that each set of columns has its registers; the second may be zeros
-    for (int k = 0; k < a.K; k += 2 * BK) {
+    for (int k = 0; k < a.K; k += 2 * KG * BK) {
       step(c0, c1);
       step(c1, c0);
     }
@@ -268,8 +273,10 @@ __global__ __launch_bounds__(64 * WM* WN) void k_int8_gemm(Int8Args a, int mtile
   // channels of a row a lane: whole lines are read and written from there on.
   wait_loads_but<0>();
   __syncthreads();
-  static_assert(sizeof(sh) >= kWaves * 32 * kRow * 4, "the waves' blocks fit the buffers");
-  int* turn = reinterpret_cast<int*>(&sh[0][0]) + wave * 32 * kRow;
+  constexpr int kTurn = 32 * kRow;  // ints of a wave's block
+  static_assert(sizeof(all) >= KG * kWaves * kTurn * 4, "the waves' blocks fit the buffers");
+  int* blocks = reinterpret_cast<int*>(&all[0][0][0]);
+  int* turn = blocks + wave_id * kTurn;
   const bool whole = n0 + (GATED ? BN / 2 : BN) <= a.N;  // every channel of the tile is one
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
@@ -280,47 +287,45 @@ __global__ __launch_bounds__(64 * WM* WN) void k_int8_gemm(Int8Args a, int mtile
       for (int j = 0; j < kNB; ++j)
 #pragma unroll
         for (int v = 0; v < 4; ++v) turn[(16 * b + 4 * quarter + v) * kRow + 16 * j + l16] = acc[2 * i + b][j][v];
+    if (KG > 1) __syncthreads();
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    const int r0 = (wm * TM + i) * 32 + lane / kLanes;  // this lane's first row in the tile
-    const int* from = turn + lane / kLanes * kRow + c;
-    constexpr int kPasses = 32 / kRows;
+    constexpr int kPasses = 32 / kRows / KG;  // each group stores a part of the rows
+    const int rb = group * (32 / KG) + lane / kLanes;
+    const int r0 = (wm * TM + i) * 32 + rb;  // this lane's first row in the tile
+    const int* from = blocks + wave * kTurn + rb * kRow + c;
     if (whole && m0 + (wm * TM + i + 1) * 32 <= a.T)
-      store_rows<GATED, BF16, kPasses, kRows, kRow, true>(a, m0 + r0, n, rows_sx + r0, from, sw, su, bias);
+      store_rows<GATED, BF16, kPasses, kRows, kRow, KG, kWaves * kTurn, true>(a, m0 + r0, n, rows_sx + r0, from, sw, su, bias);
     else
-      store_rows<GATED, BF16, kPasses, kRows, kRow, false>(a, m0 + r0, n, rows_sx + r0, from, sw, su, bias);
+      store_rows<GATED, BF16, kPasses, kRows, kRow, KG, kWaves * kTurn, false>(a, m0 + r0, n, rows_sx + r0, from, sw, su, bias);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (KG > 1 && i + 1 < TM) __syncthreads();
   }
 }
 
 }  // namespace
 
-// The tiles, and what 128 bytes of K cost a CU in each (us, one tile on a CU, and two where
-// they fit), measured on products of 64 to 2048 tokens with 2048 to 7168 channels and K. A
+// The tiles, and what 128 bytes of K cost a CU in each (us), measured on products of 64 to 2048 tokens with 2048 to 7168 channels and K. A
 // large tile reads the fewest bytes per product, but too few of them leave CUs idle: the tile
 // whose rounds over the 256 CUs cost least is taken. Against the next best tile that gives,
-// at K = 7168: 2048 x 7168 105 us (128 x 256: 114), 2048 x 4096 62 (128 x 128: 66), 1024 x
-// 7168 58 (128 x 128: 63), 256 x 7168 23 (64 x 64: 25), 128 x 7168 17.5 (64 x 128: 22).
+// at K = 7168: 2048 x 7168 93 us (128 x 256: 99), 2048 x 4096 54 (128 x 128: 64), 1024 x 7168
+// 50 (128 x 128: 61), 512 x 7168 29 (64 x 128: 35), 256 x 7168 22 (64 x 64: 24), 128 x 7168
+// 14 (64 x 128: 21). The smallest tile is short of products to cover a step's LDS
+// reads and barrier, so that two groups of waves take the steps in turn (128 x 7168: 14.0
+// us, one group 18.3).
 struct Tile {
   int tokens, channels;
-  float one, two;  // two: of both tiles of a CU together, 0 where only one fits
+  float cost;
 };
-constexpr Tile kTiles[] = {{256, 256, 1.85f, 0.f}, {128, 256, 1.04f, 0.f}, {128, 128, 0.55f, 0.f}, {64, 128, 0.41f, 0.70f}, {64, 64, 0.31f, 0.41f}};
+constexpr int kCus = 256;
+constexpr Tile kTiles[] = {{256, 256, 1.65f}, {128, 256, 0.88f}, {128, 128, 0.53f}, {64, 128, 0.38f}, {64, 64, 0.25f}};
 
 static int choose_tile(int64_t T, int64_t channels) {
-  constexpr int kCus = 256;
   int best = 0;
   float least = 0.f;
   for (int i = 0; i < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++i) {
-    const Tile& c = kTiles[i];
-    const int64_t n = ((T - 1) / c.tokens + 1) * ((channels - 1) / c.channels + 1);
-    float cost;
-    if (c.two == 0.f) {
-      cost = (float)((n - 1) / kCus + 1) * c.one;
-    } else {
-      const int64_t rest = n % (2 * kCus);
-      cost = (float)(n / (2 * kCus)) * c.two + (rest == 0 ? 0.f : rest <= kCus ? c.one : c.two);
-    }
+    const int64_t n = ((T - 1) / kTiles[i].tokens + 1) * ((channels - 1) / kTiles[i].channels + 1);
+    const float cost = (float)((n - 1) / kCus + 1) * kTiles[i].cost;
     if (i == 0 || cost < least) {
       best = i;
       least = cost;
@@ -329,20 +334,20 @@ static int choose_tile(int64_t T, int64_t channels) {
   return best;
 }
 
-template <bool GATED, bool BF16, int WM, int WN, int TM, int TN, int BK, int RING>
+template <bool GATED, bool BF16, int WM, int WN, int TM, int TN, int BK, int RING, int KG>
 static void gemm_tile(const Int8Args& a, hipStream_t s) {
   const int mt = (a.T - 1) / (32 * TM * WM) + 1, nt = (a.N - 1) / (32 * TN * WN / (GATED ? 2 : 1)) + 1;
-  hipLaunchKernelGGL((k_int8_gemm<WM, WN, TM, TN, BK, RING, GATED, BF16>), dim3(mt * nt), dim3(64 * WM * WN), 0, s, a, mt);
+  hipLaunchKernelGGL((k_int8_gemm<WM, WN, TM, TN, BK, RING, KG, GATED, BF16>), dim3(mt * nt), dim3(64 * WM * WN * KG), 0, s, a, mt);
 }
 
 template <bool GATED, bool BF16>
 static void gemm(const Int8Args& a, hipStream_t s) {
   switch (choose_tile(a.T, GATED ? 2 * (int64_t)a.N : a.N)) {
-    case 0: return gemm_tile<GATED, BF16, 2, 4, 4, 2, 64, 4>(a, s);
-    case 1: return gemm_tile<GATED, BF16, 2, 4, 2, 2, 128, 3>(a, s);
-    case 2: return gemm_tile<GATED, BF16, 2, 4, 2, 1, 128, 4>(a, s);
-    case 3: return gemm_tile<GATED, BF16, 2, 4, 1, 1, 128, 3>(a, s);
-    default: return gemm_tile<GATED, BF16, 2, 2, 1, 1, 128, 4>(a, s);
+    case 0: return gemm_tile<GATED, BF16, 2, 4, 4, 2, 64, 4, 1>(a, s);
+    case 1: return gemm_tile<GATED, BF16, 2, 4, 2, 2, 128, 3, 1>(a, s);
+    case 2: return gemm_tile<GATED, BF16, 2, 4, 2, 1, 128, 4, 1>(a, s);
+    case 3: return gemm_tile<GATED, BF16, 2, 4, 1, 1, 128, 3, 1>(a, s);
+    default: return gemm_tile<GATED, BF16, 2, 2, 1, 1, 128, 4, 2>(a, s);
   }
 }
 

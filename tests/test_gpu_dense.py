@@ -202,7 +202,7 @@ MATMUL = [
     # enough tiles for each of the larger ones, ragged at both ends
     (2050, 6500, 144, "f32", 0), (2047, 7168, 1168, "bf16", 0), (1000, 6700, 272, "bf16", 16), (1023, 6401, 48, "f32", 0),
     (3, 6200, 208, "f32", 0), (16, 7165, 96, "bf16", 0), (29, 6163, 1040, "f32", 16), (32, 100, 64, "bf16", 0),
-    (520, 6401, 400, "f32", 0), (250, 7001, 784, "bf16", 0), (127, 7165, 320, "f32", 0),
+    (20000, 50, 64, "f32", 0), (520, 6401, 400, "bf16", 0), (520, 6401, 400, "f32", 0), (250, 7001, 784, "bf16", 0), (127, 7165, 320, "f32", 0),
 ]
 
 
@@ -305,7 +305,7 @@ FFN = [
     (1, 64, 16384, "f32", 0), (2, 48, 8192, "f32", 0), (4, 80, 4096, "bf16", 0), (3, 96, 4112, "f32", 0), (16, 256, 1024, "f32", 16),
     (16, 6160, 16, "bf16", 0), (7, 128, 2048, "f32", 0), (9, 6145 + 15, 96, "f32", 0), (16, 128, 1040, "f32", 0),
     (5, 96, 3280, "f32", 0), (19, 80, 3104, "bf16", 16), (31, 256, 96, "f32", 0),
-    (2050, 96, 3264, "f32", 0), (1001, 272, 3360, "bf16", 0), (515, 144, 3280, "f32", 16), (251, 80, 3504, "bf16", 0),
+    (300, 64, 3584, "f32", 0), (2050, 96, 3264, "f32", 0), (1001, 272, 3360, "bf16", 0), (515, 144, 3280, "f32", 16), (251, 80, 3504, "bf16", 0),
 ]
 
 
