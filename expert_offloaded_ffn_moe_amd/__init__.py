@@ -340,7 +340,12 @@ def _run(fn, name, args, dev, stream):
     """Enqueue on `stream`, by default torch's current stream of GPU `dev`."""
     if dev < 0:
         _refuse(name, "the tensors are not on a GPU")
-    s = _Torch.stream(dev) if stream is None else _stream(stream)
+    if stream is None:
+        s = _Torch.stream(dev)
+    else:
+        if getattr(stream, "device_index", dev) != dev:
+            _refuse(name, "the stream is on another GPU than the tensors")
+        s = _stream(stream)
     if dev == _Torch.device():
         status = fn(args, s)
     else:

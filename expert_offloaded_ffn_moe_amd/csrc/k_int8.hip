@@ -129,14 +129,19 @@ __global__ __launch_bounds__(64 * kWaves) void k_int8_down(Int8Args a, const flo
 #pragma unroll
   for (int c = 0; c < CT; ++c) w[c] = (gi32x4*)(a.w + min(n0 + 16 * c + i, a.N - 1) * a.ld_w);
   const int pieces = a.K / 16, blocks = (pieces + 4 * kStep - 1) / (4 * kStep);
-  i32x4 wv[CT][kStep];
-  auto load = [&](int b) {
+  // two blocks of weights ahead: all of them for K up to 2048
+  struct Weights {
+    i32x4 v[CT][kStep];
+  };
+  auto load = [&](Weights& f, int b) {
 #pragma unroll
     for (int s = 0; s < kStep; ++s)
 #pragma unroll
-      for (int c = 0; c < CT; ++c) wv[c][s] = w[c][min(b * 4 * kStep + 4 * s + q, pieces - 1)];
+      for (int c = 0; c < CT; ++c) f.v[c][s] = w[c][min(b * 4 * kStep + 4 * s + q, pieces - 1)];
   };
-  load(min(wave, blocks - 1));
+  Weights w0, w1;
+  load(w0, wave);
+  load(w1, wave + kWaves);
 
   const int wpr = waves_per_row(a.T), part_of_row = (wave % wpr) * 64 + lane;
   for (int r0 = 0; r0 < a.T; r0 += kWaves / wpr) {
@@ -185,21 +190,21 @@ __global__ __launch_bounds__(64 * kWaves) void k_int8_down(Int8Args a, const flo
   i32x4 acc[CT];
 #pragma unroll
   for (int c = 0; c < CT; ++c) acc[c] = i32x4{0, 0, 0, 0};
-  for (int b = wave; b < blocks; b += kWaves) {
-    i32x4 now[CT][kStep];
-#pragma unroll
-    for (int c = 0; c < CT; ++c)
-#pragma unroll
-      for (int s = 0; s < kStep; ++s) now[c][s] = wv[c][s];
-    if (b + kWaves < blocks) load(b + kWaves);
+  auto products = [&](const Weights& f, int b) {
 #pragma unroll
     for (int s = 0; s < kStep; ++s) {
       const int p = b * 4 * kStep + 4 * s + q;
       i32x4 xv = x[min(p, pieces - 1)];
       if (p >= pieces) xv = i32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int c = 0; c < CT; ++c) acc[c] = mfma16(now[c][s], xv, acc[c]);
+      for (int c = 0; c < CT; ++c) acc[c] = mfma16(f.v[c][s], xv, acc[c]);
     }
+  };
+  for (int b = wave; b < blocks; b += 2 * kWaves) {  // a block past the last is of zeros
+    products(w0, b);
+    if (b + 2 * kWaves < blocks) load(w0, b + 2 * kWaves);
+    products(w1, b + kWaves);
+    if (b + 3 * kWaves < blocks) load(w1, b + 3 * kWaves);
   }
 #pragma unroll
   for (int c = 0; c < CT; ++c) part[wave][c][lane] = acc[c];

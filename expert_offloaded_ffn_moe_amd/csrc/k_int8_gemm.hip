@@ -47,14 +47,16 @@ __device__ __forceinline__ int xcd_order(int b, int nb) {
   return x < rem ? x * (per + 1) + i : rem * (per + 1) + (x - rem) * per + i;
 }
 
+// All but the newest N of this wave's loads are in, every LDS read too, and so it is for every
+// wave of the workgroup. One block: what follows reads LDS that other waves' loads wrote.
 template <int N>
-__device__ __forceinline__ void wait_loads_but() {  // all but the newest N loads are in, and every LDS read
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+__device__ __forceinline__ void meet_with_loads_but() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
 // 16 bytes from each lane's address to LDS at `to` + 16 lane. Written as one block, so that
 // the compiler, which cannot tell the ring's buffers apart, adds no wait for it before the
-// LDS reads of the others: wait_loads_but counts these loads instead. It has no output
+// LDS reads of the others: meet_with_loads_but counts these loads instead. It has no output
 // register. (A write of M0 is followed by one wait state before its use.)
 __device__ __forceinline__ void load_to_lds(const int8_t* from, uint32_t to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory", "m0");
@@ -239,8 +241,7 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_int8_gemm(Int8Args a, int m
     __builtin_amdgcn_sched_barrier(0);
     const int done = buf;  // every wave has all of it in registers at the barrier
     buf = buf + 1 == RING ? 0 : buf + 1;
-    wait_loads_but<(RING - 2) * kLoads>();  // the next buffer is in, this one's operands too
-    __builtin_amdgcn_s_barrier();
+    meet_with_loads_but<(RING - 2) * kLoads>();  // the next buffer is in, this one's operands too
 #pragma unroll
     for (int i = 0; i < kHalfMB; ++i) {
       __builtin_amdgcn_sched_barrier(0);
@@ -255,8 +256,7 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_int8_gemm(Int8Args a, int m
   };
 #pragma unroll
   for (int r = 0; r < RING; ++r) stage(r, 0, 1);
-  wait_loads_but<(RING - 1) * kLoads>();
-  __builtin_amdgcn_s_barrier();
+  meet_with_loads_but<(RING - 1) * kLoads>();
   fetch_rows(r0, 0, 0, 0, 1);
   fetch_cols(c0, 0, 0, 0, 1);
   if (BK == 128) {
@@ -271,8 +271,7 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_int8_gemm(Int8Args a, int m
   // Each wave turns its sums in LDS, a block of 32 rows at a time (rows 16 bytes longer, so
   // that the four rows of a write use different banks), and reads four neighbouring
   // channels of a row a lane: whole lines are read and written from there on.
-  wait_loads_but<0>();
-  __syncthreads();
+  meet_with_loads_but<0>();
   constexpr int kTurn = 32 * kRow;  // ints of a wave's block
   static_assert(sizeof(all) >= KG * kWaves * kTurn * 4, "the waves' blocks fit the buffers");
   int* blocks = reinterpret_cast<int*>(&all[0][0][0]);
