@@ -11,8 +11,8 @@
 // ring of LDS buffers, filled by loads that go from memory to LDS directly (16 bytes a lane,
 // 1024 / BK rows an instruction). In LDS the 16-byte pieces of row r stand at places
 // piece ^ swizzle(r): an instruction writes its lanes' bytes in lane order, so each lane
-// fetches the piece that belongs at its place, and sixteen lanes that read one piece of
-// sixteen rows then use every bank once. Pieces past K come from a line of zeros.
+// fetches the piece that belongs at its place, and the lanes that a read serves at once use
+// every bank once. Pieces past K come from a line of zeros.
 //
 // A step is two halves: of 64 bytes of K each where a step has 128, else of half of the rows
 // each. The operands of one are read from LDS while the products of the other run; the
@@ -29,11 +29,14 @@ namespace {
 
 typedef __attribute__((address_space(3))) void lvoid;
 
-// place of row r's piece p: p ^ swizzle(r); sixteen rows' places of one piece, 256 bytes of
-// LDS apart or less, are in different banks
+// Place of row r's piece p: p ^ swizzle(r). A 16-byte read serves sixteen lanes at once, lanes
+// 0-3, 12-15, 20-23 and 24-27 of each half wave and then the others: of 64-byte rows those
+// are the row quads 0 and 3 of one piece and 1 and 2 of the next, which -(quad) % 4 keeps in
+// different banks (quad itself: every read took twice as long, 9.9 M conflict cycles in 2048
+// x 7168 x 7168); of 128-byte rows r / 2 does.
 template <int BK>
 __device__ __forceinline__ int swizzle(int r) {
-  return BK == 64 ? r >> 2 & 3 : r >> 1 & 7;
+  return BK == 64 ? -(r >> 2) & 3 : r >> 1 & 7;
 }
 
 // what pieces past K are read from
