@@ -42,15 +42,26 @@ __device__ __forceinline__ float int8_scaled(int acc, float sx, float sw, float 
   return (float)acc * sx * sw + bias;
 }
 
-// out[t][n] of the product whose sum is `acc`
+// What one output adds to its product, loaded before the sum is known (its latency would
+// otherwise follow the sum's: one token on 7168 x 7168 9.9 us, 9.3 with it).
 template <bool BF16>
-__device__ __forceinline__ void int8_store(const Int8Out& o, int t, int n, float sx, float sw, int acc) {
+struct OutTerms {
   typedef typename OutElem<BF16>::T E;
-  float v = int8_scaled(acc, sx, sw, o.bias ? o.bias[n] : 0.f);
-  if (o.y) v += o.y[t * o.ld_y + n];
-  if (o.res) v += OutElem<BF16>::load(static_cast<const E*>(o.res)[t * o.ld_res + n]);
-  static_cast<E*>(o.out)[t * o.ld_out + n] = OutElem<BF16>::rounded(v);
-}
+  float sw, bias, y;
+  E res;
+  __device__ __forceinline__ void load(const Int8Out& o, int t, int n) {
+    sw = o.sw[n];
+    bias = o.bias ? o.bias[n] : 0.f;
+    y = o.y ? o.y[t * o.ld_y + n] : 0.f;
+    res = o.res ? static_cast<const E*>(o.res)[t * o.ld_res + n] : E{};
+  }
+  __device__ __forceinline__ void store(const Int8Out& o, int t, int n, float sx, int acc) const {
+    float v = int8_scaled(acc, sx, sw, bias);
+    if (o.y) v += y;
+    if (o.res) v += OutElem<BF16>::load(res);
+    static_cast<E*>(o.out)[t * o.ld_out + n] = OutElem<BF16>::rounded(v);
+  }
+};
 
 // Four neighbouring elements of a row, at any element's alignment (gfx950 performs such
 // accesses whole).

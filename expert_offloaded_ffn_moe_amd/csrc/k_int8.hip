@@ -56,6 +56,32 @@ __global__ __launch_bounds__(64 * kWaves) void k_int8_skinny(Int8Args a) {
   for (int c = 0; c < CT; ++c)
 #pragma unroll
     for (int tt = 0; tt < TT; ++tt) acc[c][tt] = i32x4{0, 0, 0, 0};
+  // this thread's outputs (block c, token tile tt, token j, row r) and what they add
+  constexpr int kAll = CT * TT * 16 * kN, kMine = (kAll + 64 * kWaves - 1) / (64 * kWaves);
+  struct Mine {
+    int t, n, from;  // from: its sum in a wave's part
+    float sx, su;
+    bool is;
+    OutTerms<BF16> terms;
+  } mine[kMine];
+#pragma unroll
+  for (int k = 0; k < kMine; ++k) {
+    const int o = threadIdx.x + k * 64 * kWaves;
+    const int r = o % kN, c = o / kN % CT, j = o / (kN * CT) % 16, tt = o / (16 * kN * CT);
+    Mine& m = mine[k];
+    m.t = 16 * tt + j;
+    m.n = n0 + c * kN + r;
+    m.from = ((c * TT + tt) * 64 + 16 * (r / 4) + j) * 4 + r % 4;
+    m.is = o < kAll && m.t < a.T && m.n < a.N;
+    if (!m.is) continue;
+    m.sx = a.o.sx[m.t];
+    if (GATED) {
+      m.terms.sw = a.o.sw[m.n];
+      m.su = a.o.sw[m.n + a.N];
+    } else {
+      m.terms.load(a.o, m.t, m.n);
+    }
+  }
   const int blocks = (pieces + 4 * kStep - 1) / (4 * kStep);
   for (int b = wave; b < blocks; b += kWaves) {
     i32x4 wv[CT][kStep], xv[TT][kStep];
@@ -84,12 +110,11 @@ __global__ __launch_bounds__(64 * kWaves) void k_int8_skinny(Int8Args a) {
 #pragma unroll
     for (int tt = 0; tt < TT; ++tt) part[wave][c][tt][lane] = acc[c][tt];
   __syncthreads();
-  // output (block c, token tile tt, token j, row r): component r % 4 of lane 16 (r / 4) + j
-  for (int o = threadIdx.x; o < CT * TT * 16 * kN; o += 64 * kWaves) {
-    const int r = o % kN, c = o / kN % CT, j = o / (kN * CT) % 16, tt = o / (16 * kN * CT);
-    const int t = 16 * tt + j, n = n0 + c * kN + r;
-    if (t >= a.T || n >= a.N) continue;
-    const int* p = reinterpret_cast<const int*>(&part[0][c][tt][16 * (r / 4) + j]) + r % 4;
+#pragma unroll
+  for (int k = 0; k < kMine; ++k) {
+    const Mine& m = mine[k];
+    if (!m.is) continue;
+    const int* p = reinterpret_cast<const int*>(&part[0][0][0][0]) + m.from;
     constexpr int kWave = CT * TT * 64 * 4;  // ints from one wave's sums to the next's
     int sum = 0;
 #pragma unroll
@@ -98,10 +123,9 @@ __global__ __launch_bounds__(64 * kWaves) void k_int8_skinny(Int8Args a) {
       int up = 0;
 #pragma unroll
       for (int v = 0; v < kWaves; ++v) up += p[v * kWave + 32 * 4];
-      static_cast<float*>(a.o.out)[t * a.o.ld_out + n] =
-          gated_value(sum, up, a.o.sx[t], a.o.sw[n], a.o.sw[n + a.N]);
+      static_cast<float*>(a.o.out)[m.t * a.o.ld_out + m.n] = gated_value(sum, up, m.sx, m.terms.sw, m.su);
     } else {
-      int8_store<BF16>(a.o, t, n, a.o.sx[t], a.o.sw[n], sum);
+      m.terms.store(a.o, m.t, m.n, m.sx, sum);
     }
   }
 }
@@ -142,6 +166,13 @@ __global__ __launch_bounds__(64 * kWaves) void k_int8_down(Int8Args a, const flo
   Weights w0, w1;
   load(w0, wave);
   load(w1, wave + kWaves);
+  // this thread's output (block c, token t, row r), 512 of them at most, and what it adds
+  static_assert(CT * 16 * kDownTokens <= 64 * kWaves, "an output a thread");
+  const int out_r = threadIdx.x % 16, out_c = threadIdx.x / 16 % CT, out_t = threadIdx.x / (16 * CT);
+  const int out_n = n0 + out_c * 16 + out_r;
+  const bool out_is = out_t < a.T && out_n < a.N;
+  OutTerms<BF16> terms;
+  if (out_is) terms.load(a.o, out_t, out_n);
 
   const int wpr = waves_per_row(a.T), part_of_row = (wave % wpr) * 64 + lane;
   for (int r0 = 0; r0 < a.T; r0 += kWaves / wpr) {
@@ -209,15 +240,12 @@ __global__ __launch_bounds__(64 * kWaves) void k_int8_down(Int8Args a, const flo
 #pragma unroll
   for (int c = 0; c < CT; ++c) part[wave][c][lane] = acc[c];
   __syncthreads();
-  for (int o = threadIdx.x; o < CT * 16 * 16; o += 64 * kWaves) {
-    const int r = o % 16, c = o / 16 % CT, t = o / (16 * CT), n = n0 + c * 16 + r;
-    if (t >= a.T || n >= a.N) continue;
-    const int* p = reinterpret_cast<const int*>(&part[0][c][16 * (r / 4) + t]) + r % 4;
-    int sum = 0;
+  if (!out_is) return;
+  const int* p = reinterpret_cast<const int*>(&part[0][out_c][16 * (out_r / 4) + out_t]) + out_r % 4;
+  int sum = 0;
 #pragma unroll
-    for (int v = 0; v < kWaves; ++v) sum += p[v * CT * 64 * 4];
-    int8_store<BF16>(a.o, t, n, scale[t], a.o.sw[n], sum);
-  }
+  for (int v = 0; v < kWaves; ++v) sum += p[v * CT * 64 * 4];
+  terms.store(a.o, out_t, out_n, scale[out_t], sum);
 }
 
 // Two blocks a workgroup share each load of the activations, if that leaves three quarters of

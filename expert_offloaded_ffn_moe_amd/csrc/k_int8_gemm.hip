@@ -18,6 +18,13 @@
 // each. The operands of one are read from LDS while the products of the other run; the
 // barrier that frees the oldest buffer and opens the next stands between the two, so that
 // it, too, is covered by products.
+//
+// What bounds it: 2048 x 7168 x 7168 takes 93 us (2.27 POPS) in a loop over one set of
+// buffers, 99 us on inputs from HBM. A 64-byte step of the 256 x 256 tile is 1088 cycles of
+// its MFMAs and runs in about 1390, at the 1.8 GHz that the power limit leaves; without the
+// loads the same loop takes 73 us, on loads that all hit L2 98% of its time, so it is their
+// way into LDS beside the products that costs, not memory. The rest, about 10 us, is the
+// launch, the first loads and the epilogue's bytes.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>

@@ -10,6 +10,8 @@
  *   y[t]          = sum_j w[t][j] * Wd_e . rho( silu(Wg_e x[t]) * (Wu_e x[t]) ),  e = ids[t][j]
  * with W = q * s (int4 code times fp16 group scale) and rho rounding the
  * intermediate to the activation dtype; y is fp32.
+ * Beside it stand the dense operators of the same layer (norm, 8-bit products and the
+ * gated block on them), declared at the end.
  *
  * The pages describe the problem; the numerics above are the plain reading of
  * them. Page titles are abbreviated below as
@@ -398,6 +400,25 @@ moe_status moe_plan_kernel_times(moe_plan* plan, moe_kernel_times* out);
 moe_status moe_measure_link_ceilings(size_t hbm_bytes, size_t host_bytes, int32_t iters, moe_stream stream,
                                      moe_link_ceilings* out);
 
+/* Free everything the plan owns (synchronises the device first). NULL is a no-op. */
+void moe_plan_destroy(moe_plan* plan);
+
+const char* moe_status_str(moe_status s);
+
+/* Message of the last failed call on this thread ("" if none). */
+const char* moe_last_error(void);
+
+/* Test hook for the allocation-failure paths: after this call, the n-th next
+ * device allocation (kind 0) or pinned host allocation (kind 1) made by this
+ * library on any thread fails as if out of memory (n >= 1; n = 0 disarms).
+ * The failing call then returns MOE_E_NOMEM / MOE_E_HOST_NOMEM and frees what
+ * it had allocated. Errors: MOE_E_INVALID (kind or n out of range). */
+moe_status moe_debug_fail_alloc(int32_t kind, int32_t n);
+
+/* Test hook: the device and pinned host allocations this library currently holds
+ * (over all plans). Errors: MOE_E_INVALID (null argument). */
+moe_status moe_debug_live_allocs(int64_t* device, int64_t* host);
+
 /* ---- Dense operators beside the routed layer --------------------------------
  *
  * What stands before and beside moe_layer_forward in a transformer's layer: the norm
@@ -525,25 +546,6 @@ typedef struct {
 } moe_int8_ffn_args;
 moe_status moe_int8_ffn_workspace(int32_t T, int32_t H, int32_t I, size_t* bytes);
 moe_status moe_int8_ffn(const moe_int8_ffn_args* args, moe_stream stream);
-
-/* Free everything the plan owns (synchronises the device first). NULL is a no-op. */
-void moe_plan_destroy(moe_plan* plan);
-
-const char* moe_status_str(moe_status s);
-
-/* Message of the last failed call on this thread ("" if none). */
-const char* moe_last_error(void);
-
-/* Test hook for the allocation-failure paths: after this call, the n-th next
- * device allocation (kind 0) or pinned host allocation (kind 1) made by this
- * library on any thread fails as if out of memory (n >= 1; n = 0 disarms).
- * The failing call then returns MOE_E_NOMEM / MOE_E_HOST_NOMEM and frees what
- * it had allocated. Errors: MOE_E_INVALID (kind or n out of range). */
-moe_status moe_debug_fail_alloc(int32_t kind, int32_t n);
-
-/* Test hook: the device and pinned host allocations this library currently holds
- * (over all plans). Errors: MOE_E_INVALID (null argument). */
-moe_status moe_debug_live_allocs(int64_t* device, int64_t* host);
 
 #ifdef __cplusplus
 }
