@@ -1,4 +1,4 @@
-// 8-bit matrix product for few rows: out[t][n] = sum_k x[t][k] w[n][k] on
+// 8-bit matrix product for up to 16 rows: out[t][n] = sum_k x[t][k] w[n][k] on
 // v_mfma_i32_16x16x64_i8, and the gated form h = silu(x Wg) (x Wu).
 //
 // Lane layout of the 16x16x64 MFMA: lane l supplies 16 bytes of row l % 16 of each
@@ -7,13 +7,14 @@
 // so a lane ends with four neighbouring outputs of one token.
 //
 // Bound: the weights' bytes. A workgroup takes CT blocks of 16 weight rows (gated: 8 gate
-// rows and their 8 up rows) and 16 TT tokens; its eight waves split K, each reading blocks of
+// rows and their 8 up rows) and all tokens; its eight waves split K, each reading blocks of
 // two 64-byte steps, and meet in LDS. Weights go from memory to registers with 16-byte loads,
 // all loads of a block before its products; the activations, which every workgroup reads,
 // come from cache the same way. Measured with weights from HBM (a plain copy: 5.1 TB/s): one
-// token on 7168 x 7168 10.5 us (4.9 TB/s), gated 2 x 2048 x 7168 6.5 us (4.5 TB/s), 16 tokens
-// 14.2 and 8.4 us. Four steps a block: 11.6 us for the first; sixteen waves: the same within
-// 3%, four: 13.0.
+// token on 7168 x 7168 10.8 us (4.8 TB/s), on 4096 x 7168 6.1, gated 2 x 2048 x 7168 6.5
+// (4.5 TB/s), 16 tokens 14.5, 8.3 and 8.4 us. Four steps a block: 7% longer for the first;
+// sixteen waves: the same within 3%, four: 20% longer; the next block's loads ahead of this
+// one's products, in twice the registers: 15% longer.
 #include <hip/hip_runtime.h>
 
 #include "codes.h"
@@ -23,9 +24,9 @@
 namespace moe {
 namespace {
 
-// Tokens up to which these kernels run. 32 tokens on 4096 x 2048: 5.1 us, in tiles 6.5; on
-// 7168 x 7168: 18.6, in tiles 14.0 (16 tokens 14.2); 64 tokens on these: 7.1 and 28.
-constexpr int kSkinnyRows = 32;
+// Tokens up to which these kernels run: 16 on 7168 x 7168 14.5 us (in tiles 14.6), on 4096 x
+// 2048 4.1 (5.7); two token blocks a wave would take 20.0 us for 32 tokens on the first (15.2).
+constexpr int kSkinnyRows = 16;
 constexpr int kWaves = 8;  // of a workgroup, splitting K
 constexpr int kStep = 2;   // 64-byte K steps of a wave's load block
 
@@ -33,13 +34,13 @@ __device__ __forceinline__ i32x4 mfma16(const i32x4& a, const i32x4& b, const i3
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
 }
 
-template <int TT, int CT, bool GATED, bool BF16>
+template <int CT, bool GATED, bool BF16>
 __global__ __launch_bounds__(64 * kWaves) void k_int8_skinny(Int8Args a) {
-  __shared__ i32x4 part[kWaves][CT][TT][64];
+  __shared__ i32x4 part[kWaves][CT][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int i = lane & 15, q = lane >> 4;
   constexpr int kN = GATED ? 8 : 16;  // outputs of a block of weight rows
-  const int n0 = blockIdx.x * kN * CT;  // every token is in this workgroup's tiles
+  const int n0 = blockIdx.x * kN * CT;
   // this lane's weight rows (rows past the last one are read as the last: not stored)
   gi32x4* w[CT];
 #pragma unroll
@@ -47,86 +48,59 @@ __global__ __launch_bounds__(64 * kWaves) void k_int8_skinny(Int8Args a) {
     const int n = n0 + c * kN + (GATED ? i & 7 : i);
     w[c] = (gi32x4*)(a.w + ((int64_t)min(n, a.N - 1) + (GATED && i >= 8 ? a.N : 0)) * a.ld_w);
   }
-  gi32x4* x[TT];
-#pragma unroll
-  for (int tt = 0; tt < TT; ++tt) x[tt] = (gi32x4*)(a.x + min(16 * tt + i, a.T - 1) * a.ld_x);
+  gi32x4* x = (gi32x4*)(a.x + min(i, a.T - 1) * a.ld_x);
   const int pieces = a.K / 16;  // 16-byte pieces of a row; lane q of a step takes piece 4 step + q
-  i32x4 acc[CT][TT];
+  i32x4 acc[CT];
 #pragma unroll
-  for (int c = 0; c < CT; ++c)
-#pragma unroll
-    for (int tt = 0; tt < TT; ++tt) acc[c][tt] = i32x4{0, 0, 0, 0};
-  // this thread's outputs (block c, token tile tt, token j, row r) and what they add
-  constexpr int kAll = CT * TT * 16 * kN, kMine = (kAll + 64 * kWaves - 1) / (64 * kWaves);
-  struct Mine {
-    int t, n, from;  // from: its sum in a wave's part
-    float sx, su;
-    bool is;
-    OutTerms<BF16> terms;
-  } mine[kMine];
-#pragma unroll
-  for (int k = 0; k < kMine; ++k) {
-    const int o = threadIdx.x + k * 64 * kWaves;
-    const int r = o % kN, c = o / kN % CT, j = o / (kN * CT) % 16, tt = o / (16 * kN * CT);
-    Mine& m = mine[k];
-    m.t = 16 * tt + j;
-    m.n = n0 + c * kN + r;
-    m.from = ((c * TT + tt) * 64 + 16 * (r / 4) + j) * 4 + r % 4;
-    m.is = o < kAll && m.t < a.T && m.n < a.N;
-    if (!m.is) continue;
-    m.sx = a.o.sx[m.t];
+  for (int c = 0; c < CT; ++c) acc[c] = i32x4{0, 0, 0, 0};
+  // this thread's output (block c, token t, row r), one at most, and what it adds
+  static_assert(CT * 16 * kN <= 64 * kWaves, "an output a thread");
+  const int r = threadIdx.x % kN, oc = threadIdx.x / kN % CT, t = threadIdx.x / (kN * CT), n = n0 + oc * kN + r;
+  const bool is = t < a.T && n < a.N;
+  float sx = 0.f, su = 0.f;
+  OutTerms<BF16> terms;
+  if (is) {
+    sx = a.o.sx[t];
     if (GATED) {
-      m.terms.sw = a.o.sw[m.n];
-      m.su = a.o.sw[m.n + a.N];
+      terms.sw = a.o.sw[n];
+      su = a.o.sw[n + a.N];
     } else {
-      m.terms.load(a.o, m.t, m.n);
+      terms.load(a.o, t, n);
     }
   }
   const int blocks = (pieces + 4 * kStep - 1) / (4 * kStep);
   for (int b = wave; b < blocks; b += kWaves) {
-    i32x4 wv[CT][kStep], xv[TT][kStep];
+    i32x4 wv[CT][kStep], xv[kStep];
     const int p0 = b * 4 * kStep + q;
 #pragma unroll
     for (int s = 0; s < kStep; ++s)
 #pragma unroll
       for (int c = 0; c < CT; ++c) wv[c][s] = w[c][min(p0 + 4 * s, pieces - 1)];
 #pragma unroll
-    for (int s = 0; s < kStep; ++s)
-#pragma unroll
-      for (int tt = 0; tt < TT; ++tt) xv[tt][s] = x[tt][min(p0 + 4 * s, pieces - 1)];
+    for (int s = 0; s < kStep; ++s) xv[s] = x[min(p0 + 4 * s, pieces - 1)];
 #pragma unroll
     for (int s = 0; s < kStep; ++s) {
-      if (p0 + 4 * s >= pieces)
+      if (p0 + 4 * s >= pieces) xv[s] = i32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int c = 0; c < CT; ++c) wv[c][s] = i32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int c = 0; c < CT; ++c)
-#pragma unroll
-        for (int tt = 0; tt < TT; ++tt) acc[c][tt] = mfma16(wv[c][s], xv[tt][s], acc[c][tt]);
+      for (int c = 0; c < CT; ++c) acc[c] = mfma16(wv[c][s], xv[s], acc[c]);
     }
   }
 #pragma unroll
-  for (int c = 0; c < CT; ++c)
-#pragma unroll
-    for (int tt = 0; tt < TT; ++tt) part[wave][c][tt][lane] = acc[c][tt];
+  for (int c = 0; c < CT; ++c) part[wave][c][lane] = acc[c];
   __syncthreads();
+  if (!is) return;
+  // its sum: component r % 4 of lane 16 (r / 4) + t
+  const int* p = reinterpret_cast<const int*>(&part[0][oc][16 * (r / 4) + t]) + r % 4;
+  int sum = 0;
 #pragma unroll
-  for (int k = 0; k < kMine; ++k) {
-    const Mine& m = mine[k];
-    if (!m.is) continue;
-    const int* p = reinterpret_cast<const int*>(&part[0][0][0][0]) + m.from;
-    constexpr int kWave = CT * TT * 64 * 4;  // ints from one wave's sums to the next's
-    int sum = 0;
+  for (int v = 0; v < kWaves; ++v) sum += p[v * CT * 64 * 4];
+  if (GATED) {  // the up row is 8 rows on: lane 32 further
+    int up = 0;
 #pragma unroll
-    for (int v = 0; v < kWaves; ++v) sum += p[v * kWave];
-    if (GATED) {  // the up row is 8 rows on: lane 32 further
-      int up = 0;
-#pragma unroll
-      for (int v = 0; v < kWaves; ++v) up += p[v * kWave + 32 * 4];
-      static_cast<float*>(a.o.out)[m.t * a.o.ld_out + m.n] = gated_value(sum, up, m.sx, m.terms.sw, m.su);
-    } else {
-      m.terms.store(a.o, m.t, m.n, m.sx, sum);
-    }
+    for (int v = 0; v < kWaves; ++v) up += p[v * CT * 64 * 4 + 32 * 4];
+    static_cast<float*>(a.o.out)[t * a.o.ld_out + n] = gated_value(sum, up, sx, terms.sw, su);
+  } else {
+    terms.store(a.o, t, n, sx, sum);
   }
 }
 
@@ -254,21 +228,10 @@ __global__ __launch_bounds__(64 * kWaves) void k_int8_down(Int8Args a, const flo
 template <bool GATED, bool BF16>
 void skinny(const Int8Args& a, hipStream_t s) {
   const int blocks = (a.N - 1) / (GATED ? 8 : 16) + 1;
-  const bool two = blocks >= 2 * 192;
-#define SKINNY(TT, CT) \
-  hipLaunchKernelGGL((k_int8_skinny<TT, CT, GATED, BF16>), dim3((blocks - 1) / CT + 1), dim3(64 * kWaves), 0, s, a)
-  if (a.T <= 16) {
-    if (two)
-      SKINNY(1, 2);
-    else
-      SKINNY(1, 1);
-  } else {
-    if (two)
-      SKINNY(2, 2);
-    else
-      SKINNY(2, 1);
-  }
-#undef SKINNY
+  if (blocks >= 2 * 192)
+    hipLaunchKernelGGL((k_int8_skinny<2, GATED, BF16>), dim3((blocks - 1) / 2 + 1), dim3(64 * kWaves), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_int8_skinny<1, GATED, BF16>), dim3(blocks), dim3(64 * kWaves), 0, s, a);
 }
 
 }  // namespace
