@@ -78,6 +78,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_int8_skinny(Int8Args a) {
       for (int c = 0; c < CT; ++c) wv[c][s] = w[c][min(p0 + 4 * s, pieces - 1)];
 #pragma unroll
     for (int s = 0; s < kStep; ++s) xv[s] = x[min(p0 + 4 * s, pieces - 1)];
+    __builtin_amdgcn_sched_barrier(0);  // every load before the first product: the compiler put one behind it (9.3 us, 11.0)
 #pragma unroll
     for (int s = 0; s < kStep; ++s) {
       if (p0 + 4 * s >= pieces) xv[s] = i32x4{0, 0, 0, 0};

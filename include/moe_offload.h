@@ -450,7 +450,7 @@ moe_status moe_debug_live_allocs(int64_t* device, int64_t* host);
  * mean(s^2) is summed in fp64; the codes are those of s * weight exactly for bf16
  * activations, in fp64 for fp32 ones (the row's root mean square cancels in them).
  * `add` is in the activation's type or fp32, so that moe_layer_forward's y is added as it
- * stands. x_out, out may each be x or add themselves (same address, stride and type). */
+ * stands. x_out and out may each be x or add themselves (same address, stride and type). */
 typedef struct {
   int32_t T;              /* rows, 0..2^20 */
   int32_t H;              /* 1..16384 */
@@ -488,7 +488,8 @@ moe_status moe_quantize_rows(const moe_quantize_args* args, moe_stream stream);
 
 /* Product of 8-bit codes with a scale for each token and each channel:
  *   out[t][n] = act( s_x[t] s_w[n] sum_k q_x[t][k] q_w[n][k] + bias[n] + y_in[t][n] + res[t][n] )
- * The sum is exact in int32 (codes -128..127), the rest fp32, rounded once. y_in is
+ * The sum is exact in int32 (codes -128..127), the rest fp32, rounded once; a token's
+ * output does not depend on the call's other tokens. y_in is
  * what an operator such as moe_layer_forward left in fp32, res the residual stream in
  * out's type. out may be res or y_in themselves (same address, stride and type). */
 typedef struct {
@@ -518,7 +519,8 @@ moe_status moe_int8_matmul(const moe_int8_matmul_args* args, moe_stream stream);
  *   out[t][n] = act( (Wd h')[t][n] + y_in[t][n] + res[t][n] )
  * with x = q_x * s_x and each weight its code times its channel's scale. q_gu holds the
  * I gate rows, then the I up rows. A code of h may differ by one step from that of
- * exactly computed h where 127 h / max|h| lies next to a half. The workspace holds
+ * exactly computed h where 127 h / max|h| lies next to a half; a token's output does not
+ * depend on the call's other tokens. The workspace holds
  * what moe_int8_ffn_workspace says, 256-byte aligned; its contents need not be kept,
  * and calls that overlap in time need one each. out may be res or y_in themselves. */
 typedef struct {
