@@ -43,7 +43,7 @@ typedef __attribute__((address_space(3))) void lvoid;
 // x 7168 x 7168); of 128-byte rows r / 2 does.
 template <int BK>
 __device__ __forceinline__ int swizzle(int r) {
-  return BK == 64 ? -(r >> 2) & 3 : r >> 1 & 7;
+  return BK == 64 ? (-(r >> 2)) & 3 : (r >> 1) & 7;
 }
 
 // what pieces past K are read from
@@ -127,8 +127,9 @@ __device__ __forceinline__ void store_rows(const Int8Args& a, int t0, int n, con
 }
 
 // WM x WN waves, each 32 TM x 32 TN; RING buffers. KG such groups of waves take the steps of
-// K in turn, each with buffers of its own, and add their sums at the end. GATED: of every 32 channels of the tile
-// the first 16 are gate rows and the others the same rows of up, and h is stored in fp32.
+// K in turn, each with buffers of its own, and add their sums at the end. GATED: of every 32
+// channels of the tile the first 16 are gate rows and the others the same rows of up, and h
+// is stored in fp32.
 template <int WM, int WN, int TM, int TN, int BK, int RING, int KG, bool GATED, bool BF16>
 __global__ __launch_bounds__(64 * WM* WN* KG) void k_int8_gemm(Int8Args a, int mtiles) {
   constexpr int kWaves = WM * WN, BM = 32 * TM * WM, BN = 32 * TN * WN;
@@ -168,7 +169,7 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_int8_gemm(Int8Args a, int m
     const int r = (in_a ? wave * kLoadsA + i : wave * kLoadsB + i - kLoadsA) * kRowsPer + lrow;
     int64_t row = in_a ? min(m0 + r, a.T - 1) : min(n0 + r, a.N - 1);
     if (GATED && !in_a) row = (int64_t)min(n0 + r / 32 * 16 + r % 16, a.N - 1) + (r & 16 ? a.N : 0);
-    at[i] = (lane % kPieces ^ swizzle<BK>(r)) * 16;
+    at[i] = ((lane % kPieces) ^ swizzle<BK>(r)) * 16;
     p[i] = (in_a ? a.x + row * a.ld_x : a.w + row * a.ld_w) + group * BK + at[i];
   }
   const int8_t* zeros = reinterpret_cast<const int8_t*>(&zero_piece);
@@ -210,14 +211,14 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_int8_gemm(Int8Args a, int m
   // the part'th of `parts` parts of a half's rows, and of its columns
   auto fetch_rows = [&](Rows& f, int buf, int h, int part, int parts) {
     const int r0 = wm * 32 * TM + (BK == 128 ? 0 : h * kHalfMB * 16);
-    const int off = l16 * BK + (((BK == 128 ? 4 * h : 0) + quarter ^ swizzle<BK>(l16)) << 4);
+    const int off = l16 * BK + ((((BK == 128 ? 4 * h : 0) + quarter) ^ swizzle<BK>(l16)) << 4);
 #pragma unroll
     for (int i = 0; i < kHalfMB; ++i)
       if (i >= kHalfMB * part / parts && i < kHalfMB * (part + 1) / parts)
         f.v[i] = *reinterpret_cast<const i32x4*>(&sh[buf][(r0 + 16 * i) * BK + off]);
   };
   auto fetch_cols = [&](Cols& f, int buf, int h, int part, int parts) {
-    const int off = l16 * BK + (((BK == 128 ? 4 * h : 0) + quarter ^ swizzle<BK>(l16)) << 4);
+    const int off = l16 * BK + ((((BK == 128 ? 4 * h : 0) + quarter) ^ swizzle<BK>(l16)) << 4);
 #pragma unroll
     for (int j = 0; j < kNB; ++j)
       if (j >= kNB * part / parts && j < kNB * (part + 1) / parts)
@@ -317,21 +318,23 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_int8_gemm(Int8Args a, int m
 
 }  // namespace
 
-// The tiles, and what 128 bytes of K cost a CU in each (us), measured on products of 64 to 2048 tokens with 2048 to 7168 channels and K. A
-// large tile reads the fewest bytes per product, but too few of them leave CUs idle: the tile
-// whose rounds over the 256 CUs cost least is taken. Against the next best tile that gives,
-// at K = 7168: 2048 x 7168 93 us (128 x 256: 99), 2048 x 4096 54 (128 x 128: 64), 1024 x 7168
-// 50 (128 x 128: 61), 512 x 7168 29 (64 x 128: 35), 256 x 7168 22 (64 x 64: 24), 128 x 7168
-// 14 (64 x 128: 21). The smaller tiles are short of products to cover a step's
-// LDS reads and barrier, so that two, four or eight groups of waves take the steps in turn
-// (64 x 64 in one group: 18.3 us for 128 x 7168; 64 x 32 11.4 and 64 x 64 13.6 us for 128 x
-// 4096; 32 x 32 9.0, 64 x 32 10.2 and 64 x 64 13.0 us for 64 x 4096).
+// The tiles, and what 128 bytes of K cost a CU in each (us), measured on products of 64 to
+// 2048 tokens with 2048 to 7168 channels and K. A large tile reads the fewest bytes per
+// product, but too few of them leave CUs idle: the tile whose rounds over the 256 CUs cost
+// least is taken. Against the next best tile that gives, at K = 7168: 2048 x 7168 93 us (128
+// x 256: 99), 2048 x 4096 54 (128 x 128: 64), 1024 x 7168 50 (128 x 128: 61), 512 x 7168 29
+// (64 x 128: 35), 256 x 7168 22 (64 x 64: 24), 128 x 7168 14 (64 x 128: 21). The smaller
+// tiles are short of products to cover a step's LDS reads and barrier, so that two, four or
+// eight groups of waves take the steps in turn (64 x 64 in one group: 18.3 us for 128 x 7168;
+// 64 x 32 11.4 and 64 x 64 13.6 us for 128 x 4096; 32 x 32 9.0, 64 x 32 10.2 and 64 x 64 13.0
+// us for 64 x 4096).
 struct Tile {
   int tokens, channels;
   float cost;
 };
 constexpr int kCus = 256;
-constexpr Tile kTiles[] = {{256, 256, 1.65f}, {128, 256, 0.88f}, {128, 128, 0.53f}, {64, 128, 0.38f}, {64, 64, 0.25f}, {64, 32, 0.20f}, {32, 32, 0.16f}};
+constexpr Tile kTiles[] = {{256, 256, 1.65f}, {128, 256, 0.88f}, {128, 128, 0.53f}, {64, 128, 0.38f},
+                          {64, 64, 0.25f},   {64, 32, 0.20f},   {32, 32, 0.16f}};
 
 static int choose_tile(int64_t T, int64_t channels) {
   int best = 0;

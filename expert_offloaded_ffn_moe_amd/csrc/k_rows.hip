@@ -177,7 +177,6 @@ __device__ __forceinline__ double wave_max_pos(double v) {
   return lane63(v);
 }
 
-__device__ __forceinline__ uint32_t abs_bits(float f) { return __float_as_uint(f) & 0x7FFFFFFFu; }
 template <typename P>
 struct QuotientOf;
 template <>

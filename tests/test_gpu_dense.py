@@ -89,6 +89,9 @@ NORM = [
     (8, 2048, "f32", "act", 4), (1, 7168, "bf16", "f32", 0), (17, 7168, "bf16", "none", 8), (7, 4101, "bf16", "f32", 3),
     (6, 8192, "f32", "none", 0), (7, 8193, "bf16", "act", 7), (6, 16384, "bf16", "f32", 0), (3, 16383, "f32", "act", 1),
     (1025, 256, "bf16", "f32", 0), (261, 4096, "bf16", "f32", 0),
+    # more rows than workgroups: each goes on to further ones
+    (1300, 4100, "bf16", "f32", 1), (5000, 300, "bf16", "act", 0), (3000, 1030, "f32", "act", 2), (700, 9000, "bf16", "none", 0),
+    (4101, 512, "f32", "f32", 0),
 ]
 
 
@@ -135,13 +138,14 @@ def test_rms_norm(moe, T, H, act, add, pad):
 @pytest.mark.parametrize("act", ["bf16", "f32"])
 def test_rms_norm_in_place(moe, act):
     """x_out over x, out over add."""
-    g, dt, T, H = _gen(5), ACT[act], 33, 1000
-    x, r, w = _rn(g, T, H).to(dt), _rn(g, T, H).to(dt), _rn(g, H).to(dt)
-    xo, out = torch.empty_like(x), torch.empty_like(x)
-    moe.rms_norm(x, w, 1e-6, add=r, x_out=xo, out=out)
-    moe.rms_norm(x, w, 1e-6, add=r, x_out=x, out=r)
-    torch.cuda.synchronize()
-    assert torch.equal(x, xo) and torch.equal(r, out)
+    g, dt = _gen(5), ACT[act]
+    for T, H in [(33, 1000), (1301, 2100), (5001, 200)]:
+        x, r, w = _rn(g, T, H).to(dt), _rn(g, T, H).to(dt), _rn(g, H).to(dt)
+        xo, out = torch.empty_like(x), torch.empty_like(x)
+        moe.rms_norm(x, w, 1e-6, add=r, x_out=xo, out=out)
+        moe.rms_norm(x, w, 1e-6, add=r, x_out=x, out=r)
+        torch.cuda.synchronize()
+        assert torch.equal(x, xo) and torch.equal(r, out)
 
 
 @pytest.mark.parametrize("act", ["bf16", "f32"])
