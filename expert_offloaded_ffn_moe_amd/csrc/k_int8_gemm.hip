@@ -323,7 +323,7 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_int8_gemm(Int8Args a, int m
 // product, but too few of them leave CUs idle: the tile whose rounds over the 256 CUs cost
 // least is taken. Against the next best tile that gives, at K = 7168: 2048 x 7168 93 us (128
 // x 256: 99), 2048 x 4096 54 (128 x 128: 64), 1024 x 7168 50 (128 x 128: 61), 512 x 7168 29
-// (64 x 128: 35), 256 x 7168 22 (64 x 64: 24), 128 x 7168 14 (64 x 128: 21). The smaller
+// (64 x 128: 35), 256 x 7168 21 (64 x 64: 24), 128 x 7168 14 (64 x 128: 21). The smaller
 // tiles are short of products to cover a step's LDS reads and barrier, so that two, four or
 // eight groups of waves take the steps in turn (64 x 64 in one group: 18.3 us for 128 x 7168;
 // 64 x 32 11.4 and 64 x 64 13.6 us for 128 x 4096; 32 x 32 9.0, 64 x 32 10.2 and 64 x 64 13.0
@@ -333,7 +333,7 @@ struct Tile {
   float cost;
 };
 constexpr int kCus = 256;
-constexpr Tile kTiles[] = {{256, 256, 1.65f}, {128, 256, 0.88f}, {128, 128, 0.53f}, {64, 128, 0.38f},
+constexpr Tile kTiles[] = {{256, 256, 1.65f}, {128, 256, 0.88f}, {128, 128, 0.53f}, {64, 128, 0.35f},
                           {64, 64, 0.25f},   {64, 32, 0.20f},   {32, 32, 0.16f}};
 
 static int choose_tile(int64_t T, int64_t channels) {
@@ -362,7 +362,7 @@ static void gemm(const Int8Args& a, hipStream_t s) {
     case 0: return gemm_tile<GATED, BF16, 2, 4, 4, 2, 64, 4, 1>(a, s);
     case 1: return gemm_tile<GATED, BF16, 2, 4, 2, 2, 128, 3, 1>(a, s);
     case 2: return gemm_tile<GATED, BF16, 2, 4, 2, 1, 128, 4, 1>(a, s);
-    case 3: return gemm_tile<GATED, BF16, 2, 4, 1, 1, 128, 3, 1>(a, s);
+    case 3: return gemm_tile<GATED, BF16, 2, 4, 1, 1, 128, 4, 1>(a, s);
     case 4: return gemm_tile<GATED, BF16, 2, 2, 1, 1, 128, 4, 2>(a, s);
     case 5: return gemm_tile<GATED, BF16, 2, 1, 1, 1, 128, 3, 4>(a, s);
     default: return gemm_tile<GATED, BF16, 1, 1, 1, 1, 128, 2, 8>(a, s);
