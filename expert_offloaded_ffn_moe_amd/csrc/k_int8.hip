@@ -108,8 +108,10 @@ __global__ __launch_bounds__(64 * kWaves) void k_int8_skinny(Int8Args a) {
 // The second half of the gated block for up to 16 tokens: as k_int8_skinny, with the
 // activations' codes formed in LDS from h first, while the first weights are on their way.
 // Each workgroup reads and codes all of h, which costs less than a launch of its own for as
-// long as h is small. A row of h is shared by kWaves / T waves at least, in registers of
-// kHeld elements a lane.
+// long as h is small: one token of the 7168/2048 block 12.0 us (with the codes in a launch of
+// their own 14.4), 16 of the 2048/768 one 11.3 (14.9), but 16 of the first, 32768 elements,
+// 18.3 us on the GPU (17.8). A row of h is shared by kWaves / T waves at least, in registers
+// of kHeld elements a lane.
 constexpr int kHeld = 32;
 constexpr int kDownTokens = 16, kDownElements = 16384;
 
