@@ -195,26 +195,26 @@ __device__ __forceinline__ double rsqrt64(double m) {
   return r * fma(-0.5 * m * r, r, 1.5);
 }
 
-// TPR threads of a workgroup of BLOCK take one row, NC chunks of 8 elements each
-// (chunk c of thread t: elements 8 (t + c TPR) ..), then the row `gridDim.x` rows of
-// workgroups on, whose loads are under way before the first is reduced. ADD: 0 none, 1 act,
-// 2 fp32.
-template <typename ACT, bool NORM, int ADD, int TPR, int BLOCK, int NC>
-__global__ __launch_bounds__(BLOCK) void k_rows(RowArgs a) {
+// A row is taken by a workgroup of up to MAX threads, or, with WAVE, by one of its waves:
+// `tpr` threads with NC chunks of 8 elements each (chunk c of thread t: elements
+// 8 (t + c tpr) ..). Then follows the row `gridDim.x` workgroups on, whose loads are under way
+// before the first is reduced. ADD: 0 none, 1 act, 2 fp32.
+template <typename ACT, bool NORM, int ADD, bool WAVE, int MAX, int NC>
+__global__ __launch_bounds__(MAX) void k_rows(RowArgs a) {
   typedef typename Act<ACT>::P P;
   typedef typename std::conditional<ADD == 1, ACT, float>::type AddT;
-  constexpr int kRows = BLOCK / TPR, kWaves = TPR / 64;
-  const int t = threadIdx.x % TPR;
+  constexpr int kRows = WAVE ? MAX / 64 : 1, kMaxWaves = WAVE ? 1 : MAX / 64;
+  const int tpr = WAVE ? 64 : NC > 1 ? MAX : (int)blockDim.x, t = WAVE ? threadIdx.x % 64 : threadIdx.x;
   const int step = gridDim.x * kRows;
-  int row = blockIdx.x * kRows + (int)threadIdx.x / TPR;
-  if (kRows > 1 && row >= a.T) return;  // a row is one wave then: nothing waits for it
+  int row = WAVE ? blockIdx.x * kRows + (int)threadIdx.x / 64 : blockIdx.x;
+  if (WAVE && row >= a.T) return;  // nothing waits for it
 
   Raw<ACT> x[NC], g[NC];
   Raw<AddT> r[NC];
   auto load = [&](int at) {
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int j = kChunk * (t + c * TPR), n = a.H - j;
+      const int j = kChunk * (t + c * tpr), n = a.H - j;
       x[c].load(static_cast<const ACT*>(a.x) + at * a.ld_x + j, n);
       if (ADD) r[c].load(static_cast<const AddT*>(a.add) + at * a.ld_add + j, n);
     }
@@ -222,7 +222,7 @@ __global__ __launch_bounds__(BLOCK) void k_rows(RowArgs a) {
   load(row);
   if (NORM) {
 #pragma unroll
-    for (int c = 0; c < NC; ++c) g[c].load(static_cast<const ACT*>(a.weight) + kChunk * (t + c * TPR), a.H - kChunk * (t + c * TPR));
+    for (int c = 0; c < NC; ++c) g[c].load(static_cast<const ACT*>(a.weight) + kChunk * (t + c * tpr), a.H - kChunk * (t + c * tpr));
   }
   const double inv_h = 1.0 / a.H;
   for (int turn = 0; row < a.T; row += step, turn ^= 1) {
@@ -243,7 +243,7 @@ __global__ __launch_bounds__(BLOCK) void k_rows(RowArgs a) {
     P top = 0;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int j = kChunk * (t + c * TPR), n = a.H - j;
+      const int j = kChunk * (t + c * tpr), n = a.H - j;
       if (NORM) g[c].values(w[c]);
       if (NORM) {
 #pragma unroll
@@ -264,11 +264,11 @@ __global__ __launch_bounds__(BLOCK) void k_rows(RowArgs a) {
       top_bits = wave_max_u(top_bits);
       if (NORM && sizeof(P) == 8) top = wave_max_pos(top);
     }
-    if (kWaves > 1) {
+    if (!WAVE) {
       // two sets, so that a wave that is a row ahead writes another than the others read
-      __shared__ double part_sum[2][kWaves];
-      __shared__ uint32_t part_bits[2][kWaves];
-      __shared__ P part_top[2][kWaves];
+      __shared__ double part_sum[2][kMaxWaves];
+      __shared__ uint32_t part_bits[2][kMaxWaves];
+      __shared__ P part_top[2][kMaxWaves];
       if (t % 64 == 0) {
         part_sum[turn][t / 64] = sum;
         part_bits[turn][t / 64] = top_bits;
@@ -277,7 +277,8 @@ __global__ __launch_bounds__(BLOCK) void k_rows(RowArgs a) {
       __syncthreads();
       sum = 0.0;
 #pragma unroll
-      for (int i = 0; i < kWaves; ++i) {
+      for (int i = 0; i < kMaxWaves; ++i) {
+        if (64 * i >= tpr) break;
         if (NORM) sum += part_sum[turn][i];
         top_bits = max(top_bits, part_bits[turn][i]);
         if (NORM && sizeof(P) == 8) top = fmax((double)top, (double)part_top[turn][i]);
@@ -289,7 +290,7 @@ __global__ __launch_bounds__(BLOCK) void k_rows(RowArgs a) {
       const float rs = (float)rstd;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const int j = kChunk * (t + c * TPR), n = a.H - j;
+        const int j = kChunk * (t + c * tpr), n = a.H - j;
         float o[kChunk];
 #pragma unroll
         for (int i = 0; i < kChunk; ++i)
@@ -307,7 +308,7 @@ __global__ __launch_bounds__(BLOCK) void k_rows(RowArgs a) {
     const uint32_t keep = none ? 0u : ~0u;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int j = kChunk * (t + c * TPR), n = a.H - j;
+      const int j = kChunk * (t + c * tpr), n = a.H - j;
       uint32_t code[kChunk];
 #pragma unroll
       for (int i = 0; i < kChunk; ++i) code[i] = quot.code(NORM ? (P)v[c][i] * (P)w[c][i] : (P)v[c][i]) & keep;
@@ -326,27 +327,32 @@ __global__ __launch_bounds__(BLOCK) void k_rows(RowArgs a) {
   }
 }
 
-// Rows of up to 512 elements take a wave, of 2048 four waves and of 8192 eight (two chunks a
-// thread; 1024 threads of one chunk: 36.6 us against 35.8 for the norm of 2048 x 7168 bf16
-// rows with an fp32 addition and all outputs, 256 of four 43). The norm's workgroups are half
-// of what fits the 256 CUs and go on to further rows, their loads a row ahead (twice as many:
-// 37.5 us; one row each: 43 before rows were loaded ahead); the codes alone, with fewer
+// Rows of up to 512 elements take a wave each (8192 rows of 512, norm with all outputs: 10.8
+// us, a workgroup each 21.4), of up to 2048 as many waves as hold them at a chunk a thread
+// (4096 rows of 2048: 18.2 us, a wave of four chunks 23.5; 4000 rows of 1000: 12.0 us, four
+// waves whatever the length 15.2), longer ones 8 or 16 waves at two chunks a thread (2048 rows
+// of 7168: 35.8 us, with one chunk a thread 36.6, with four 43, and on the seven waves that
+// would hold them 42). The norm's workgroups are
+// half of what fits the 256 CUs and go on to further rows, their loads a row ahead (twice as
+// many: 37.5 us; one row each: 43 before rows were loaded ahead); the codes alone, with fewer
 // registers, take one row each (2048 x 7168 rows: 8.9 us, 10.6 as the norm does).
 template <typename ACT, bool NORM, int ADD>
 void launch(const RowArgs& a, hipStream_t s) {
-#define ROWS(TPR, BLOCK, NC)                                                                              \
-  {                                                                                                       \
-    const int all = (a.T - 1) / (BLOCK / TPR) + 1, grid = NORM ? std::min(all, 128 * 2048 / BLOCK) : all; \
-    hipLaunchKernelGGL((k_rows<ACT, NORM, ADD, TPR, BLOCK, NC>), dim3(grid), dim3(BLOCK), 0, s, a);       \
+#define ROWS(WAVE, MAX, NC)                                                                                        \
+  {                                                                                                                \
+    const int block = WAVE || NC > 1 ? MAX : ((a.H - 1) / (64 * kChunk) + 1) * 64;                                 \
+    const int all = WAVE ? (a.T - 1) / (MAX / 64) + 1 : a.T;                                                       \
+    const int grid = NORM ? std::min(all, 128 * 2048 / block) : all;                                               \
+    hipLaunchKernelGGL((k_rows<ACT, NORM, ADD, WAVE, MAX, NC>), dim3(grid), dim3(block), 0, s, a);                 \
   }
   if (a.H <= 512)
-    ROWS(64, 256, 1)
+    ROWS(true, 256, 1)
   else if (a.H <= 2048)
-    ROWS(256, 256, 1)
+    ROWS(false, 256, 1)
   else if (a.H <= 8192)
-    ROWS(512, 512, 2)
+    ROWS(false, 512, 2)
   else
-    ROWS(1024, 1024, 2)
+    ROWS(false, 1024, 2)
 #undef ROWS
 }
 
