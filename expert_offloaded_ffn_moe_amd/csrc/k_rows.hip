@@ -328,10 +328,10 @@ __global__ __launch_bounds__(MAX) void k_rows(RowArgs a) {
 }
 
 // Rows of up to 512 elements take a wave each (8192 rows of 512, norm with all outputs: 10.8
-// us, a workgroup each 21.4), of up to 2048 as many waves as hold them at a chunk a thread
-// (4096 rows of 2048: 18.2 us, a wave of four chunks 23.5; 4000 rows of 1000: 12.0 us, four
-// waves whatever the length 15.2), longer ones 8 or 16 waves at two chunks a thread (2048 rows
-// of 7168: 35.8 us, with one chunk a thread 36.6, with four 43, and on the seven waves that
+// us, a workgroup each 21.4), of up to 4096 as many waves as hold them at a chunk a thread
+// (4096 rows of 2048: 18.2 us, a wave of four chunks 23.5; 2048 rows of 2560: 14.8 us, eight
+// waves of two chunks 20.6), longer ones 8 or 16 waves at two chunks a thread (2048 rows of
+// 7168: 35.8 us, with one chunk a thread 36.6, with four 43, and on the seven waves that
 // would hold them 42). The norm's workgroups are
 // half of what fits the 256 CUs and go on to further rows, their loads a row ahead (twice as
 // many: 37.5 us; one row each: 43 before rows were loaded ahead); the codes alone, with fewer
@@ -347,8 +347,8 @@ void launch(const RowArgs& a, hipStream_t s) {
   }
   if (a.H <= 512)
     ROWS(true, 256, 1)
-  else if (a.H <= 2048)
-    ROWS(false, 256, 1)
+  else if (a.H <= 4096)
+    ROWS(false, 512, 1)
   else if (a.H <= 8192)
     ROWS(false, 512, 2)
   else

@@ -90,7 +90,8 @@ NORM = [
     (6, 8192, "f32", "none", 0), (7, 8193, "bf16", "act", 7), (6, 16384, "bf16", "f32", 0), (3, 16383, "f32", "act", 1),
     (1025, 256, "bf16", "f32", 0), (261, 4096, "bf16", "f32", 0),
     # more rows than workgroups: each goes on to further ones
-    (1300, 4100, "bf16", "f32", 1), (5000, 300, "bf16", "act", 0), (3000, 1030, "f32", "act", 2), (700, 9000, "bf16", "none", 0),
+    (1300, 4100, "bf16", "f32", 1), (5000, 300, "bf16", "act", 0), (3000, 1030, "f32", "act", 2), (1500, 3000, "bf16", "act", 0),
+    (7, 2561, "f32", "f32", 1), (5, 4096, "f32", "act", 0), (700, 9000, "bf16", "none", 0),
     (4101, 512, "f32", "f32", 0),
 ]
 
