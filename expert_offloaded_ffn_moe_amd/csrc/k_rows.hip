@@ -332,10 +332,10 @@ __global__ __launch_bounds__(MAX) void k_rows(RowArgs a) {
 // (4096 rows of 2048: 18.2 us, a wave of four chunks 23.5; 2048 rows of 2560: 14.8 us, eight
 // waves of two chunks 20.6), longer ones 8 or 16 waves at two chunks a thread (2048 rows of
 // 7168: 35.8 us, with one chunk a thread 36.6, with four 43, and on the seven waves that
-// would hold them 42). The norm's workgroups are
-// half of what fits the 256 CUs and go on to further rows, their loads a row ahead (twice as
-// many: 37.5 us; one row each: 43 before rows were loaded ahead); the codes alone, with fewer
-// registers, take one row each (2048 x 7168 rows: 8.9 us, 10.6 as the norm does).
+// would hold them 42). The norm's workgroups are half of what fits the 256 CUs and go on to
+// further rows, their loads a row ahead (twice as many: 37.5 us; one row each: 43 before rows
+// were loaded ahead); the codes alone, with fewer registers, take one row each (2048 x 7168
+// rows: 8.9 us, 10.6 as the norm does).
 template <typename ACT, bool NORM, int ADD>
 void launch(const RowArgs& a, hipStream_t s) {
 #define ROWS(WAVE, MAX, NC)                                                                                        \

@@ -68,7 +68,7 @@ BAD_NORM = [dict(T=-1), dict(T=(1 << 20) + 1), dict(H=0), dict(H=16385), dict(ac
             dict(act_dtype=0, add_dtype=1), dict(eps=0.0), dict(eps=-1.0), dict(eps=float("nan")),
             dict(eps=float("inf")), dict(x=None), dict(weight=None), dict(x=MB + 1), dict(add=2 * MB + 2),
             dict(x_out=None, out=None, q_out=None, s_out=None), dict(q_out=None), dict(s_out=None), dict(add=None),
-            dict(ld_x=255), dict(ld_q=-1), dict(x_out=5 * MB + 16), dict(out=MB + 64), dict(out=MB, ld_out=512),
+            dict(ld_x=255), dict(ld_q=-1), dict(ld_out=(1 << 36) + 1), dict(x_out=5 * MB + 16), dict(out=MB + 64), dict(out=MB, ld_out=512),
             dict(q_out=MB), dict(s_out=MB), dict(weight=5 * MB), dict(out=2 * MB), dict(s_out=6 * MB + 256),
             # scales at the place of fp32 activations of the same stride
             dict(T=256, act_dtype=0, s_out=MB)]
