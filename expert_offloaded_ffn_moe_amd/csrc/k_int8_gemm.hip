@@ -332,9 +332,9 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_int8_gemm(Int8Args a, int m
 // least is taken. Against the next best tile that gives, at K = 7168: 2048 x 7168 93 us (128
 // x 256: 99), 2048 x 4096 54 (128 x 128: 64), 1024 x 7168 50 (128 x 128: 61), 512 x 7168 29
 // (64 x 128: 35), 256 x 7168 21 (64 x 64: 24), 128 x 7168 14 (64 x 128: 21). The smaller
-// tiles are short of products to cover a step's LDS reads and barrier, so that two, four or
-// eight groups of waves take the steps in turn (64 x 64 in one group: 18.3 us for 128 x 7168;
-// 64 x 32 11.4 and 64 x 64 13.6 us for 128 x 4096; 32 x 32 9.0, 64 x 32 10.2 and 64 x 64 13.0
+// tiles are short of products to cover a step's LDS reads and barrier, so that two or four
+// groups of waves take the steps in turn (64 x 64 in one group: 18.3 us for 128 x 7168;
+// 64 x 32 11.2 and 64 x 64 13.1 us for 128 x 4096; 32 x 32 8.2, 64 x 32 9.1 and 64 x 64 11.1
 // us for 64 x 4096).
 struct Tile {
   int tokens, channels;
@@ -373,7 +373,7 @@ static void gemm(const Int8Args& a, hipStream_t s) {
     case 3: return gemm_tile<GATED, BF16, 2, 4, 1, 1, 128, 4, 1>(a, s);
     case 4: return gemm_tile<GATED, BF16, 2, 2, 1, 1, 128, 4, 2>(a, s);
     case 5: return gemm_tile<GATED, BF16, 2, 1, 1, 1, 128, 3, 4>(a, s);
-    default: return gemm_tile<GATED, BF16, 1, 1, 1, 1, 128, 2, 8>(a, s);
+    default: return gemm_tile<GATED, BF16, 1, 1, 1, 1, 128, 4, 4>(a, s);
   }
 }
 
