@@ -12,7 +12,7 @@
 // all loads of a block before its products; the activations, which every workgroup reads,
 // come from cache the same way. Measured with weights from HBM (a plain copy: 5.1 TB/s): one
 // token on 7168 x 7168 10.8 us (4.8 TB/s), on 4096 x 7168 6.1, gated 2 x 2048 x 7168 6.5
-// (4.5 TB/s), 16 tokens 14.5, 8.3 and 8.4 us. Four steps a block: 7% longer for the first;
+// (4.5 TB/s), 16 tokens 13.2, 8.3 and 8.4 us. Four steps a block: 7% longer for the first;
 // sixteen waves: the same within 3%, four: 20% longer; the next block's loads ahead of this
 // one's products, in twice the registers: 15% longer.
 #include <hip/hip_runtime.h>
@@ -24,8 +24,10 @@
 namespace moe {
 namespace {
 
-// Tokens up to which these kernels run: 16 on 7168 x 7168 14.5 us (in tiles 14.6), on 4096 x
-// 2048 4.1 (5.7); two token blocks a wave would take 20.0 us for 32 tokens on the first (15.2).
+// Tokens up to which these kernels run, against the tiles, on 7168 x 7168, 4096 x 7168 and 4096
+// x 2048: 9 to 12 tokens 12.0, 7.4 and 3.9 us (tiles 11.8 to 12.3, 8.2, 5.2), 16 tokens 13.2,
+// 8.3 and 4.1 (12.1, 8.2, 5.3), gated blocks of 16 on 7168 / 2048 and 2048 / 768 17.9 and 9.2
+// (19.2, 10.1). Two token blocks a wave would take 20.0 us for 32 tokens on the first (10.8).
 constexpr int kSkinnyRows = 16;
 constexpr int kWaves = 8;  // of a workgroup, splitting K
 constexpr int kStep = 2;   // 64-byte K steps of a wave's load block
