@@ -12,7 +12,7 @@
 // all loads of a block before its products; the activations, which every workgroup reads,
 // come from cache the same way. Measured with weights from HBM (a plain copy: 5.1 TB/s): one
 // token on 7168 x 7168 10.8 us (4.8 TB/s), on 4096 x 7168 6.1, gated 2 x 2048 x 7168 6.5
-// (4.5 TB/s), 16 tokens 13.2, 8.3 and 8.4 us. Four steps a block: 7% longer for the first;
+// (4.5 TB/s), 16 tokens on the last two 8.3 and 8.4 us. Four steps a block: 7% longer for the first;
 // sixteen waves: the same within 3%, four: 20% longer; the next block's loads ahead of this
 // one's products, in twice the registers: 15% longer.
 #include <hip/hip_runtime.h>
@@ -24,11 +24,13 @@
 namespace moe {
 namespace {
 
-// Tokens up to which these kernels run, against the tiles, on 7168 x 7168, 4096 x 7168 and 4096
-// x 2048: 9 to 12 tokens 12.0, 7.4 and 3.9 us (tiles 11.8 to 12.3, 8.2, 5.2), 16 tokens 13.2,
-// 8.3 and 4.1 (12.1, 8.2, 5.3), gated blocks of 16 on 7168 / 2048 and 2048 / 768 17.9 and 9.2
-// (19.2, 10.1). Two token blocks a wave would take 20.0 us for 32 tokens on the first (10.8).
-constexpr int kSkinnyRows = 16;
+// Tokens up to which these kernels run. 16 tokens: 4096 x 7168 8.3 us (in tiles 8.2), 4096 x
+// 2048 4.1 (5.3), gated blocks of 7168 / 2048 and 2048 / 768 17.4 and 9.2 (19.2, 10.1); two
+// token blocks a wave would take 20.0 us for 32 tokens on 7168 x 7168 (10.8). Long rows of many
+// channels, where two blocks a workgroup fill the chip, go to tiles sooner: 7168 x 7168 12.1
+// (tiles 11.8), 13.3 (12.1) us for 12 and 16 tokens, 6144 x 4096 8.4 (7.2) and 14336 x 4096 16.9
+// (15.1 to 15.7) for 16, but 10000 x 2064 7.2 (8.1), and 7168 x 7168 12.0 (12.3) for 9.
+constexpr int kSkinnyRows = 16, kSkinnyRowsWide = 12, kWideK = 4096;
 constexpr int kWaves = 8;  // of a workgroup, splitting K
 constexpr int kStep = 2;   // 64-byte K steps of a wave's load block
 
@@ -230,10 +232,12 @@ __global__ __launch_bounds__(64 * kWaves) void k_int8_down(Int8Args a, const flo
 // Two blocks a workgroup share each load of the activations, if that leaves three quarters of
 // the 256 CUs a workgroup: 16 tokens on 7168 x 7168 14.2 us (one block: 16.9), on 4096 x 2048
 // 5.2 us (4.0).
+bool two_blocks(int blocks) { return blocks >= 2 * 192; }
+
 template <bool GATED, bool BF16>
 void skinny(const Int8Args& a, hipStream_t s) {
   const int blocks = (a.N - 1) / (GATED ? 8 : 16) + 1;
-  if (blocks >= 2 * 192)
+  if (two_blocks(blocks))
     hipLaunchKernelGGL((k_int8_skinny<2, GATED, BF16>), dim3((blocks - 1) / 2 + 1), dim3(64 * kWaves), 0, s, a);
   else
     hipLaunchKernelGGL((k_int8_skinny<1, GATED, BF16>), dim3(blocks), dim3(64 * kWaves), 0, s, a);
@@ -242,7 +246,8 @@ void skinny(const Int8Args& a, hipStream_t s) {
 }  // namespace
 
 void launch_int8_matmul(const Int8Args& a, bool out_bf16, hipStream_t s) {
-  if (a.T > kSkinnyRows) return launch_int8_gemm(a, out_bf16, s);
+  const bool wide = a.K >= kWideK && two_blocks((a.N - 1) / 16 + 1);
+  if (a.T > (wide ? kSkinnyRowsWide : kSkinnyRows)) return launch_int8_gemm(a, out_bf16, s);
   if (out_bf16)
     skinny<false, true>(a, s);
   else
@@ -258,7 +263,7 @@ void launch_int8_down(const Int8Args& a, const float* h, bool out_bf16, hipStrea
   const size_t lds = (size_t)a.T * (a.K + 16);
 #define DOWN(CT, BF16) \
   hipLaunchKernelGGL((k_int8_down<CT, BF16>), dim3((blocks - 1) / CT + 1), dim3(64 * kWaves), lds, s, a, h)
-  if (blocks >= 2 * 192) {
+  if (two_blocks(blocks)) {
     if (out_bf16)
       DOWN(2, true);
     else

@@ -208,6 +208,9 @@ MATMUL = [
     (2050, 6500, 144, "f32", 0), (2047, 7168, 1168, "bf16", 0), (1000, 6700, 272, "bf16", 16), (1023, 6401, 48, "f32", 0),
     (3, 6200, 208, "f32", 0), (16, 7165, 96, "bf16", 0), (29, 6163, 1040, "f32", 16), (32, 100, 64, "bf16", 0),
     (20000, 50, 64, "f32", 0), (520, 6401, 400, "bf16", 0), (520, 6401, 400, "f32", 0), (250, 7001, 784, "bf16", 0), (127, 7165, 320, "f32", 0),
+    # at the rule that takes a few tokens to tiles
+    (12, 6129, 4096, "bf16", 0), (13, 6129, 4096, "f32", 16), (13, 6128, 4096, "bf16", 0), (13, 6129, 4080, "f32", 0),
+    (16, 7165, 4112, "bf16", 0),
 ]
 
 
