@@ -247,8 +247,9 @@ def _layer_weights(router_w, router_b, experts):
 
 # ---- dense operators beside the routed layer
 #
-# Tensors are on one GPU, matrices two-dimensional with consecutive elements in a row
-# (any row stride), vectors packed. The work runs on `stream` (default: torch's current
+# Tensors are on one GPU, matrices two-dimensional with consecutive elements in a row and
+# rows that do not overlap (any row stride from their length on; an expanded row is
+# refused), vectors packed. The work runs on `stream` (default: torch's current
 # stream of that GPU); the GPU need not be the current one.
 
 
@@ -307,8 +308,12 @@ def _mat(fn, name, t, rows, cols, dtype, dev):
             return t.data_ptr(), cols
         ld, step = t.stride()
         if step == 1 or cols == 1:
-            # a single row's stride says nothing (and may be less than its length)
-            return t.data_ptr(), ld if rows > 1 else cols
+            if rows == 1:  # its stride says nothing, and may be less than its length
+                return t.data_ptr(), cols
+            if ld >= cols:
+                return t.data_ptr(), ld
+            # a broadcast row among them: the ABI's stride of 0 stands for packed rows
+            _refuse(fn, "%s: its rows overlap (row stride %d for %d elements): pass a tensor that holds every row" % (name, ld, cols))
     _refuse_tensor(fn, name, t, (rows, cols), dtype, dev)
 
 
