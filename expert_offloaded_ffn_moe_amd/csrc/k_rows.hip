@@ -195,6 +195,15 @@ __device__ __forceinline__ double rsqrt64(double m) {
   return r * fma(-0.5 * m * r, r, 1.5);
 }
 
+// v w 2^e for bf16 v and w, with e the exponent of 1 / rms, at least -128 (-140 for a row whose
+// rms is infinite): exact unless the result itself leaves fp32's normal range. Where e < 0 the
+// larger factor is scaled: its 8 bits stay whole down to 2^-142, and under that both factors
+// are under 2^-14 and the result is 0. Else the smaller one, which stays under 2^8, as |v| 2^e does.
+__device__ __forceinline__ float product_far(float v, float w, int e) {
+  const bool v_larger = fabsf(v) >= fabsf(w);
+  return ldexpf(v_larger ? v : w, min(e, 0)) * ldexpf(v_larger ? w : v, max(e, 0));
+}
+
 // A row is taken by a workgroup of up to MAX threads, or, with WAVE, by one of its waves:
 // `tpr` threads with NC chunks of 8 elements each (chunk c of thread t: elements
 // 8 (t + c tpr) ..). Then follows the row `gridDim.x` workgroups on, whose loads are under way
@@ -298,30 +307,54 @@ __global__ __launch_bounds__(MAX) void k_rows(RowArgs a) {
         if (n > 0) store8(static_cast<ACT*>(a.out) + row * a.ld_out + j, n, o);
       }
     }
-    if (NORM && !a.q) continue;
-    // A NaN or an infinity in the row: scale NaN and codes 0, so that every product
-    // with the row is NaN. A row of (next to) nothing: scale and codes 0.
-    if (NORM && !(rstd > 0.0)) top_bits = kNotFinite;
-    const bool none = top_bits >= kNotFinite || top_bits < kNoCodes;
-    if (t == 0) a.s[row] = code_scale(top_bits, (double)top * rstd);
-    const typename QuotientOf<P>::T quot(none ? (P)1 : top);
-    const uint32_t keep = none ? 0u : ~0u;
+    if (!NORM || a.q) {
+      // A NaN or an infinity in the row: scale NaN and codes 0, so that every product
+      // with the row is NaN. A row of (next to) nothing: scale and codes 0.
+      if (NORM && !(rstd > 0.0)) top_bits = kNotFinite;
+      const bool none = top_bits >= kNotFinite || top_bits < kNoCodes;
+      if (t == 0) a.s[row] = code_scale(top_bits, (double)top * rstd);
+      const typename QuotientOf<P>::T quot(none ? (P)1 : top);
+      const uint32_t keep = none ? 0u : ~0u;
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int j = kChunk * (t + c * tpr), n = a.H - j;
-      uint32_t code[kChunk];
+      for (int c = 0; c < NC; ++c) {
+        const int j = kChunk * (t + c * tpr), n = a.H - j;
+        uint32_t code[kChunk];
 #pragma unroll
-      for (int i = 0; i < kChunk; ++i) code[i] = quot.code(NORM ? (P)v[c][i] * (P)w[c][i] : (P)v[c][i]) & keep;
-      int8_t* q = a.q + row * a.ld_q + j;
-      if (n >= kChunk) {
-        I8x8 o;
-        o.v[0] = code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24;
-        o.v[1] = code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24;
-        *reinterpret_cast<I8x8*>(q) = o;
-      } else {
+        for (int i = 0; i < kChunk; ++i) code[i] = quot.code(NORM ? (P)v[c][i] * (P)w[c][i] : (P)v[c][i]) & keep;
+        int8_t* q = a.q + row * a.ld_q + j;
+        if (n >= kChunk) {
+          I8x8 o;
+          o.v[0] = code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24;
+          o.v[1] = code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24;
+          *reinterpret_cast<I8x8*>(q) = o;
+        } else {
 #pragma unroll
-        for (int i = 0; i < kChunk; ++i)
-          if (i < n) q[i] = (int8_t)code[i];
+          for (int i = 0; i < kChunk; ++i)
+            if (i < n) q[i] = (int8_t)code[i];
+        }
+      }
+    }
+    // bf16: v w is exact in fp32 where |v| <= sqrt(H) / rstd and |w| keep it under 2^127; where it
+    // falls among the subnormals, it is off by 2^-150 and n by 2^-140, 1/64 of what n's own
+    // rounding to bf16's subnormals may be. Elsewhere the norm is formed once more, behind
+    // the usual stores, which costs one row of 7168 0.09 us (chosen ahead of them: 0.15).
+    if (NORM && sizeof(P) == 4 && a.out) {
+      uint32_t top_w = 0;  // of this thread's |weight|
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) top_w = max(top_w, abs_bits(w[c][i]));
+      if (__builtin_expect(!(rstd >= 0x1p-60 && rstd <= 0x1p10 && top_w < (127u + 60u) << 23), 0)) {
+        const int e = rstd < 0x1p80 ? max(ilogb(rstd), -140) : 0;  // rstd is under 2^75, or NaN
+        const float m = (float)ldexp(rstd, -e);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const int j = kChunk * (t + c * tpr), n = a.H - j;
+          float o[kChunk];
+#pragma unroll
+          for (int i = 0; i < kChunk; ++i) o[i] = product_far(v[c][i], w[c][i], e) * m;
+          if (n > 0) store8(static_cast<ACT*>(a.out) + row * a.ld_out + j, n, o);
+        }
       }
     }
   }

@@ -447,10 +447,10 @@ moe_status moe_debug_live_allocs(int64_t* device, int64_t* host);
  *   s = act(x + add) (fp32 sum, rounded once; x itself without add)
  *   n[t][j] = s[t][j] * weight[j] / sqrt(mean_j(s[t][j]^2) + eps)
  * and any of the outputs x_out = s, out = act(n), and the codes of n with their scales.
- * out follows the formula where s is not finite: a NaN makes its row NaN, an infinity makes
- * itself NaN and the rest of its row 0. mean(s^2) is summed in fp64; the codes are those of
- * s * weight exactly for bf16 activations, in fp64 for fp32 ones (the row's root mean square
- * cancels in them).
+ * out follows the formula where s * weight alone is beyond fp32's range, and where s is not
+ * finite: a NaN makes its row NaN, an infinity makes itself NaN and the rest of its row 0.
+ * mean(s^2) is summed in fp64; the codes are those of s * weight exactly for bf16
+ * activations, in fp64 for fp32 ones (the row's root mean square cancels in them).
  * `add` is in the activation's type or fp32, so that moe_layer_forward's y is added as it
  * stands. x_out and out may each be x or add themselves (same address, stride and type). */
 typedef struct {
