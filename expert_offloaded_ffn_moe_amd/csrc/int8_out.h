@@ -35,11 +35,20 @@ struct OutElem<true> {
   }
 };
 
-// The product's value before the output's rounding: each step rounded on its own, so that
-// every kernel gives a token the same bits, whatever other tokens a call has.
+// acc sx sw, each step rounded on its own, so that every kernel gives a token the same bits,
+// whatever other tokens a call has. A sum of up to 2^31 times a token's scale of 2^96 and more
+// may leave fp32 where the product does not: such a scale is taken 2^-32 fold and the product
+// 2^32 fold, which changes no bit of what is finite.
+__device__ __forceinline__ float int8_product(int acc, float sx, float sw) {
+#pragma clang fp contract(off)
+  const bool large = fabsf(sx) >= 0x1p96f;
+  return (float)acc * (large ? sx * 0x1p-32f : sx) * sw * (large ? 0x1p32f : 1.f);
+}
+
+// The product's value before the output's rounding.
 __device__ __forceinline__ float int8_scaled(int acc, float sx, float sw, float bias) {
 #pragma clang fp contract(off)
-  return (float)acc * sx * sw + bias;
+  return int8_product(acc, sx, sw) + bias;
 }
 
 // What one output adds to its product, loaded before the sum is known (its latency would
@@ -122,7 +131,7 @@ __device__ __forceinline__ void store4(uint16_t* p, int n, const float* v) {
 
 // silu(g) u, each from its exact sum; exp(-g) past fp32's range gives the limit 0
 __device__ __forceinline__ float gated_value(int g_acc, int u_acc, float sx, float sg, float su) {
-  const float g = (float)g_acc * sx * sg, u = (float)u_acc * sx * su;
+  const float g = int8_product(g_acc, sx, sg), u = int8_product(u_acc, sx, su);
   return g / (1.f + __expf(-g)) * u;
 }
 

@@ -59,6 +59,61 @@ def test_norm_whose_products_leave_fp32(moe, act, eps, H):
     assert bool((err <= tol).all()), [(sizes[i], int((~(err <= tol))[i].sum())) for i in range(len(sizes))]
 
 
+def _out(moe, T, N, dt):
+    return torch.full((T, N), 77, device="cuda", dtype=dt)
+
+
+@pytest.mark.parametrize("out_act", ["bf16", "f32"])
+@pytest.mark.parametrize("T,N,K", [(1, 100, 256), (5, 33, 7168), (16, 6200, 256), (40, 100, 256), (300, 130, 512)])
+def test_matmul_whose_scaled_sums_leave_fp32(moe, T, N, K, out_act):
+    """Powers of two moved from a channel's scale to a token's change no bit, also where the
+    sum times the token's scale alone is beyond fp32."""
+    g, dt = _gen(T + N), ACT[out_act]
+    q, w = _codes(g, T, K), _codes(g, N, K)
+    q[0], w[0] = 127, 127  # a sum of 127 127 K
+    sx, sw = torch.rand(T, device="cuda", generator=g) + 0.5, torch.rand(N, device="cuda", generator=g) + 0.5
+    bias, y, res = _rn(g, N), _rn(g, T, N), _rn(g, T, N).to(dt)
+    for more in ({}, dict(bias=bias, y_in=y, res=res)):
+        want = moe.int8_matmul(q, sx, w, sw, _out(moe, T, N, dt), **more)
+        for k in (64, 95, 96, 97, 110, 125):
+            got = moe.int8_matmul(q, sx * 2.0 ** k, w, sw * 2.0 ** -k, _out(moe, T, N, dt), **more)
+            torch.cuda.synchronize()
+            assert torch.equal(got, want), k
+    # and as it should be: what is finite comes out finite, what is not does not
+    got = moe.int8_matmul(q, sx * 2.0 ** 110, w, sw * 2.0 ** -60, _out(moe, T, N, dt))
+    v = (q.to(D) @ w.to(D).t()) * sx.to(D)[:, None] * sw.to(D) * 2.0 ** 50
+    assert bool(((got.to(D) - v).abs() <= (3.03 * R32 + (RBF if out_act == "bf16" else 0)) * v.abs()).all())
+    got = moe.int8_matmul(q, sx * 2.0 ** 110, w, sw * 2.0 ** 60, _out(moe, T, N, dt))
+    acc = q.to(D) @ w.to(D).t()
+    assert torch.equal(got, torch.where(acc == 0, acc, acc.sign() * float("inf")).to(dt))
+    sx[0] = float("nan")
+    sx[T - 1] = float("inf") if T > 1 else sx[0]
+    got = moe.int8_matmul(q, sx, w, sw, _out(moe, T, N, dt))
+    assert got[0].isnan().all() and int(got.isnan().sum()) == N + int((T > 1) * (acc[T - 1] == 0).sum())
+
+
+@pytest.mark.parametrize("T,H,I", [(1, 2048, 128), (16, 2048, 768), (16, 96, 2048), (40, 2048, 272), (300, 2048, 128)])
+def test_ffn_whose_scaled_sums_leave_fp32(moe, T, H, I):
+    """As above for the block: between the token's scale and the gate and up channels', and
+    between the up channels' (and so h, and the scales of its codes) and the down channels'."""
+    g = _gen(T + I)
+    q, gu, dn = _codes(g, T, H), _codes(g, 2 * I, H), _codes(g, H, I)
+    q[0], gu[I] = 127, 127
+    sx = torch.rand(T, device="cuda", generator=g) + 0.5
+    sgu = (torch.rand(2 * I, device="cuda", generator=g) + 0.5) / (5000 * H ** 0.5)
+    sdn = torch.rand(H, device="cuda", generator=g) + 0.5
+    ws = torch.empty(moe.int8_ffn_workspace(T, H, I), dtype=torch.uint8, device="cuda")
+    want = moe.int8_ffn(q, sx, gu, sgu, dn, sdn, _out(moe, T, H, torch.float32), ws)
+    assert bool(want.isfinite().all()) and bool(want.any())
+    for k in (64, 105):  # sgu stays above 2^-126
+        got = moe.int8_ffn(q, sx * 2.0 ** k, gu, sgu * 2.0 ** -k, dn, sdn, _out(moe, T, H, torch.float32), ws)
+        assert torch.equal(got, want), k
+    up = sgu.clone()
+    up[I:] *= 2.0 ** 114  # h under 2^126
+    got = moe.int8_ffn(q, sx, gu, up, dn, sdn * 2.0 ** -114, _out(moe, T, H, torch.float32), ws)
+    assert torch.equal(got, want)
+
+
 def test_broadcast_rows_are_refused(moe):
     g, T, H, N = _gen(2), 4, 32, 8
     q, s, w, sw = _codes(g, T, H), torch.ones(T, device="cuda"), _codes(g, N, H), torch.ones(N, device="cuda")
