@@ -64,19 +64,32 @@ moe_status apart_or_same(const Mat& out, const Mat& in) { return same(out, in) ?
     if (_s != MOE_OK) return _s;      \
   } while (0)
 
+moe_status hip_failed(const char* what, hipError_t e) {
+  char msg[256];
+  std::snprintf(msg, sizeof(msg), "%s: %s", what, hipGetErrorString(e));
+  return report_error(MOE_E_HIP, msg);
+}
+
 // Work is enqueued with the stream's device current, whichever the caller's is.
 class OnStreamDevice {
  public:
   explicit OnStreamDevice(hipStream_t s) {
     hipDevice_t dev = 0;
-    if (!s || hipGetDevice(&prev_) != hipSuccess || hipStreamGetDevice(s, &dev) != hipSuccess || dev == prev_) return;
-    changed_ = hipSetDevice(dev) == hipSuccess;
+    if (s && (error_ = hipGetDevice(&prev_)) == hipSuccess && (error_ = hipStreamGetDevice(s, &dev)) == hipSuccess && dev != prev_) {
+      error_ = hipSetDevice(dev);
+      changed_ = error_ == hipSuccess;
+    }
+    // launched() asks for the thread's last error: what the caller's own calls left there is
+    // not a launch's
+    (void)hipGetLastError();
   }
   ~OnStreamDevice() {
     if (changed_) (void)hipSetDevice(prev_);
   }
+  moe_status ready() const { return error_ == hipSuccess ? MOE_OK : hip_failed("the stream's device", error_); }
 
  private:
+  hipError_t error_ = hipSuccess;
   int prev_ = 0;
   bool changed_ = false;
 };
@@ -84,9 +97,9 @@ class OnStreamDevice {
 moe_status launched(const char* what) {
   const hipError_t e = hipGetLastError();
   if (e == hipSuccess) return MOE_OK;
-  char msg[256];
-  std::snprintf(msg, sizeof(msg), "launching %s: %s", what, hipGetErrorString(e));
-  return report_error(MOE_E_HIP, msg);
+  char msg[64];
+  std::snprintf(msg, sizeof(msg), "launching %s", what);
+  return hip_failed(msg, e);
 }
 
 int act_size(int dtype) { return dtype == MOE_ACT_BF16 ? 2 : 4; }
@@ -181,6 +194,7 @@ moe_status moe_rms_norm(const moe_rms_norm_args* a, moe_stream stream) {
             a->s_out, x.ld, add.ld, xo.ld, out.ld, q.ld, T, H, a->act_dtype == MOE_ACT_BF16,
             a->add_dtype == MOE_ACT_F32, a->eps};
   const OnStreamDevice on(static_cast<hipStream_t>(stream));
+  CHECK(on.ready());
   launch_rms_norm(r, static_cast<hipStream_t>(stream));
   return launched("the norm");
 }
@@ -208,6 +222,7 @@ moe_status moe_quantize_rows(const moe_quantize_args* a, moe_stream stream) {
   r.H = a->H;
   r.act_bf16 = a->act_dtype == MOE_ACT_BF16;
   const OnStreamDevice on(static_cast<hipStream_t>(stream));
+  CHECK(on.ready());
   launch_quantize_rows(r, static_cast<hipStream_t>(stream));
   return launched("the rows' codes");
 }
@@ -233,6 +248,7 @@ moe_status moe_int8_matmul(const moe_int8_matmul_args* a, moe_stream stream) {
   const Int8Args g{a->q_x, a->q_w, x.ld, w.ld, T, N, K,
                    {a->s_x, a->s_w, a->bias, a->y_in, a->res, a->out, e.y.ld, e.res.ld, e.out.ld}};
   const OnStreamDevice on(static_cast<hipStream_t>(stream));
+  CHECK(on.ready());
   launch_int8_matmul(g, a->out_dtype == MOE_ACT_BF16, static_cast<hipStream_t>(stream));
   return launched("the 8-bit product");
 }
@@ -277,13 +293,15 @@ moe_status moe_int8_ffn(const moe_int8_ffn_args* a, moe_stream stream) {
   float* s = reinterpret_cast<float*>(base + f.s);
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const OnStreamDevice on(st);
+  CHECK(on.ready());
   Int8Args g{a->q_x, a->q_gu, x.ld, gu.ld, T, I, H, {a->s_x, a->s_gu, nullptr, nullptr, nullptr, h, 0, 0, I}};
   launch_int8_gated(g, st);
+  CHECK(launched("the gated product"));
   Int8Args d{q, a->q_dn, I, dn.ld, T, H, I,
              {s, a->s_dn, nullptr, a->y_in, a->res, a->out, e.y.ld, e.res.ld, e.out.ld}};
   if (int8_down_fits(T, I)) {
     launch_int8_down(d, h, a->out_dtype == MOE_ACT_BF16, st);
-    return launched("the gated block");
+    return launched("the block's second product");
   }
   RowArgs r{};
   r.x = h;
@@ -293,8 +311,9 @@ moe_status moe_int8_ffn(const moe_int8_ffn_args* a, moe_stream stream) {
   r.T = T;
   r.H = I;
   launch_quantize_rows(r, st);
+  CHECK(launched("the codes of h"));
   launch_int8_matmul(d, a->out_dtype == MOE_ACT_BF16, st);
-  return launched("the gated block");
+  return launched("the block's second product");
 }
 
 }  // extern "C"

@@ -1,8 +1,10 @@
 """The dense operators at the ends of their ranges: values whose intermediate products leave
-fp32, and arguments that are refused.
+fp32, arguments that are refused, and calls after an error of the caller's own.
 
 Tolerances count roundings: one to fp32 is off by at most 2^-24 of its value, one to bf16 by
 2^-8; a bf16 result under 2^-126 is a multiple of 2^-133 and off by half of that."""
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -112,6 +114,50 @@ def test_ffn_whose_scaled_sums_leave_fp32(moe, T, H, I):
     up[I:] *= 2.0 ** 114  # h under 2^126
     got = moe.int8_ffn(q, sx, gu, up, dn, sdn * 2.0 ** -114, _out(moe, T, H, torch.float32), ws)
     assert torch.equal(got, want)
+
+
+def _hip():
+    """The HIP runtime that this process runs on."""
+    for line in open("/proc/self/maps"):
+        if "libamdhip64" in line:
+            return ctypes.CDLL(line.split()[-1])
+    raise AssertionError("no HIP runtime is loaded")
+
+
+def test_an_error_of_the_callers_own(moe):
+    """A failed HIP call of the caller's (a device that there is not), its error not yet asked
+    for: the operators report their own launches alone."""
+    g, hip = _gen(1), _hip()
+    x, w = _rn(g, 20, 256).bfloat16(), _rn(g, 256).bfloat16()
+    q, s, out = torch.empty(20, 256, dtype=torch.int8, device="cuda"), torch.empty(20, device="cuda"), torch.empty_like(x)
+    wq, ws = _codes(g, 256, 256), torch.ones(256, device="cuda")
+    block = torch.empty(moe.int8_ffn_workspace(20, 256, 128), dtype=torch.uint8, device="cuda")
+    calls = [lambda: moe.rms_norm(x, w, out=out), lambda: moe.quantize_rows(x, q, s),
+             lambda: moe.int8_matmul(q, s, wq, ws, out),
+             lambda: moe.int8_ffn(q, s, wq, ws, wq[:, :128], ws, out, block)]
+    side = torch.cuda.Stream()
+    for f in calls:
+        f()
+    torch.cuda.synchronize()
+    for f in calls:
+        for stream in (None, side):
+            with torch.cuda.stream(stream):
+                assert hip.hipSetDevice(1 << 20) != 0
+                f()
+                assert hip.hipGetLastError() == 0  # and leave nothing behind
+            torch.cuda.synchronize()
+
+
+def test_on_the_per_thread_stream(moe):
+    """HIP's handle of the thread's own default stream."""
+    g, per_thread = _gen(4), 2
+    x, w = _rn(g, 20, 256).bfloat16(), _rn(g, 256).bfloat16()
+    out, want = torch.empty_like(x), torch.empty_like(x)
+    moe.rms_norm(x, w, out=want)
+    torch.cuda.synchronize()
+    moe.rms_norm(x, w, out=out, stream=per_thread)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
 
 
 def test_broadcast_rows_are_refused(moe):
