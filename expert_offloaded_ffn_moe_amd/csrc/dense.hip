@@ -41,7 +41,8 @@ struct Mat {
 moe_status check_mat(Mat& m, bool required, int align) {
   if (!m.p) return required ? bad("%s is required", m.name) : MOE_OK;
   if (m.ld == 0) m.ld = m.cols;
-  if (m.ld < m.cols || m.ld > (int64_t(1) << 36)) return bad("%s: row stride %lld is under %lld or too large", m.name, (long long)m.ld, (long long)m.cols);
+  // (a single row, such as a large workspace, has no stride that an address is formed with)
+  if (m.ld < m.cols || (m.rows > 1 && m.ld > (int64_t(1) << 36))) return bad("%s: row stride %lld is under %lld or too large", m.name, (long long)m.ld, (long long)m.cols);
   if (reinterpret_cast<uintptr_t>(m.p) % align) return bad("%s must be %d-byte aligned", m.name, align);
   if (m.rows > 1 && m.ld * m.size % align) return bad("%s: rows must be %d-byte aligned", m.name, align);
   return MOE_OK;

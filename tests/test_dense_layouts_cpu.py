@@ -1,5 +1,7 @@
 """The layouts of the dense operators' arguments, on the CPU: every call here is turned down
 before any GPU work, for the reason that its message names."""
+import ctypes
+
 import pytest
 
 import expert_offloaded_ffn_moe_amd as moe
@@ -73,3 +75,26 @@ def test_a_single_row_may_have_any_stride():
     m = torch.zeros(1, H, dtype=BF)
     for rows in (m.expand(1, H), m.as_strided((1, H), (0, 1)), m.as_strided((1, H), (5, 1))):
         assert moe._mat("moe_rms_norm", "x", rows, 1, H, BF, -1) == (rows.data_ptr(), H)
+
+
+MB = 1 << 20
+
+
+def _c_refusal(fn, args):
+    """The message of a refused call of the C interface (its made-up addresses are never looked at)."""
+    lib = moe.load_library()
+    assert getattr(lib, fn)(ctypes.byref(args), None) == moe.MOE_E_INVALID
+    return lib.moe_last_error().decode()
+
+
+def test_largest_workspace_of_the_block():
+    """2^20 tokens of 16384 intermediate channels, 80 GiB of workspace, within the documented
+    sizes: the call gets past the workspace, to an output that overlaps it."""
+    n, G = ctypes.c_size_t(), 1 << 30
+    assert moe.load_library().moe_int8_ffn_workspace(1 << 20, 16, 16384, ctypes.byref(n)) == moe.MOE_OK
+    assert n.value >= (1 << 20) * 16384 * 5
+    a = dict(T=1 << 20, H=16, I=16384, out_dtype=1, q_x=MB, s_x=64 * MB, q_gu=96 * MB, s_gu=97 * MB, q_dn=98 * MB, s_dn=99 * MB,
+             out=G, workspace=2 * G, workspace_bytes=n.value)
+    assert _c_refusal("moe_int8_ffn", moe.Int8FfnArgs(**{**a, "out": 3 * G})) == "workspace overlaps out"
+    assert "are needed" in _c_refusal("moe_int8_ffn", moe.Int8FfnArgs(**{**a, "workspace_bytes": n.value - 1}))
+    assert _c_refusal("moe_int8_ffn", moe.Int8FfnArgs(**{**a, "workspace": 2 * G + 16})) == "workspace must be 256-byte aligned"
