@@ -48,7 +48,17 @@ moe_status check_mat(Mat& m, bool required, int align) {
   return MOE_OK;
 }
 
-bool overlap(const Mat& a, const Mat& b) { return a.p && b.p && a.begin() < b.end() && b.begin() < a.end(); }
+// Whether two matrices share elements. Rows of one stride side by side, as in a fused
+// projection's output, do not; rows of unlike strides are taken to where their extents meet.
+bool overlap(const Mat& a, const Mat& b) {
+  if (!a.p || !b.p || a.begin() >= b.end() || b.begin() >= a.end()) return false;
+  const int64_t la = a.rows > 1 ? a.ld * a.size : 0, lb = b.rows > 1 ? b.ld * b.size : 0;
+  const int64_t ld = la ? la : lb;  // a single row may stand beside the other's
+  if (!ld || (la && lb && la != lb)) return true;
+  // a's rows are at 0 .. of every ld bytes, b's at d ..
+  const int64_t d = ((b.begin() - a.begin()) % ld + ld) % ld;
+  return d < a.cols * a.size || d + b.cols * b.size > ld;
+}
 // the same elements at the same places: a row's reader may write them
 bool same(const Mat& a, const Mat& b) {
   return a.p == b.p && a.size == b.size && a.rows == b.rows && a.cols == b.cols && (a.ld == b.ld || a.rows == 1);

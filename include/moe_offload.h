@@ -441,6 +441,8 @@ moe_status moe_debug_live_allocs(int64_t* device, int64_t* host);
  *  - Work is enqueued on the device of `stream` (the null stream: the current device).
  *  - T == 0 is a no-op: no pointer is looked at then.
  *  - An output may not overlap an input or another output, but for the cases named.
+ *    Matrices of one row stride (in bytes) may stand side by side in one buffer; of
+ *    unlike strides, they may not interleave.
  *  - Errors: MOE_E_INVALID (arguments), MOE_E_HIP (the stream's device, a launch). An
  *    error that an earlier HIP call left on the thread, not yet asked for, is cleared and
  *    not reported. */

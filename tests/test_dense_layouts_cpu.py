@@ -1,6 +1,7 @@
 """The layouts of the dense operators' arguments, on the CPU: every call here is turned down
 before any GPU work, for the reason that its message names."""
 import ctypes
+import random
 
 import pytest
 
@@ -98,3 +99,57 @@ def test_largest_workspace_of_the_block():
     assert _c_refusal("moe_int8_ffn", moe.Int8FfnArgs(**{**a, "out": 3 * G})) == "workspace overlaps out"
     assert "are needed" in _c_refusal("moe_int8_ffn", moe.Int8FfnArgs(**{**a, "workspace_bytes": n.value - 1}))
     assert _c_refusal("moe_int8_ffn", moe.Int8FfnArgs(**{**a, "workspace": 2 * G + 16})) == "workspace must be 256-byte aligned"
+
+
+def _bytes(at, rows, cols, ld, size):
+    return {at + r * ld * size + c for r in range(rows) for c in range(cols * size)}
+
+
+def test_overlap_is_of_elements():
+    """Codes at every kind of place beside their rows: refused where they share a byte, let by
+    where the strides are equal and they do not (two unlike strides that interleave are refused
+    as well). Calls that get by the check are turned down for the scales, which stand in the codes."""
+    rng, seen = random.Random(5), [0, 0, 0]
+    for _ in range(4000):
+        rows, cols, f32 = rng.randint(1, 4), rng.randint(1, 6), rng.random() < 0.5
+        size = 4 if f32 else 2
+        ld_x = cols + rng.randint(0, 8)
+        ld_q = ld_x * size if rng.random() < 0.7 else cols + rng.randint(0, 30)
+        at = MB + rng.randint(-2 * ld_x * size - 8, (rows + 1) * ld_x * size)
+        args = moe.QuantizeArgs(T=rows, H=cols, act_dtype=0 if f32 else 1, x=MB, ld_x=ld_x, q_out=at, ld_q=max(ld_q, cols),
+                                s_out=at // 4 * 4)
+        x, q = _bytes(MB, rows, cols, ld_x, size), _bytes(at, rows, cols, max(ld_q, cols), 1)
+        if x & _bytes(args.s_out, 1, rows, rows, 4) and not x & q:
+            continue  # the scales stand in x as well
+        msg = _c_refusal("moe_quantize_rows", args)
+        if x & q:
+            assert msg == "q_out overlaps x", (rows, cols, size, ld_x, ld_q, at - MB)
+            seen[0] += 1
+        elif rows == 1 or ld_q == ld_x * size:
+            assert msg != "q_out overlaps x", (rows, cols, size, ld_x, ld_q, at - MB)
+            seen[1] += 1
+        else:
+            assert msg in ("q_out overlaps x", "s_out overlaps x", "s_out overlaps q_out")
+            seen[2] += 1
+    assert min(seen) > 200, seen
+
+
+def test_columns_of_one_buffer_get_by():
+    """Every operator's matrices side by side in one buffer; the scales (the bias, the
+    workspace) stand in an output, for which the call is turned down in the end."""
+    H, ld = 256, 1024
+    a = dict(T=4, H=H, act_dtype=1, add_dtype=1, eps=1e-6, x=MB, ld_x=ld, add=MB + 2 * H, ld_add=ld, weight=3 * MB,
+             x_out=MB + 4 * H, ld_x_out=ld, out=MB + 6 * H, ld_out=ld, q_out=6 * MB, s_out=6 * MB)
+    assert _c_refusal("moe_rms_norm", moe.RmsNormArgs(**a)) == "s_out overlaps q_out"
+    assert _c_refusal("moe_rms_norm", moe.RmsNormArgs(**{**a, "out": MB + 6 * H - 2})) == "out overlaps x_out"
+    assert _c_refusal("moe_rms_norm", moe.RmsNormArgs(**{**a, "out": MB + 6 * H + 2})) == "out overlaps x"
+    assert _c_refusal("moe_rms_norm", moe.RmsNormArgs(**{**a, "weight": MB + 4 * H})) == "x_out overlaps weight"
+    a = dict(T=4, N=100, K=256, out_dtype=1, q_x=MB, s_x=2 * MB, q_w=3 * MB, s_w=4 * MB, res=8 * MB, ld_res=250, out=8 * MB + 200,
+             ld_out=250, y_in=8 * MB + 400, ld_y=125, bias=8 * MB + 200)
+    assert _c_refusal("moe_int8_matmul", moe.Int8MatmulArgs(**a)) == "out overlaps y_in"
+    a["ld_res"], a["ld_out"], a["ld_y"] = 400, 400, 200
+    assert _c_refusal("moe_int8_matmul", moe.Int8MatmulArgs(**a)) == "out overlaps bias"
+    a = dict(T=4, H=256, I=64, out_dtype=1, q_x=MB, s_x=2 * MB, q_gu=3 * MB, s_gu=4 * MB, q_dn=5 * MB, s_dn=6 * MB, res=8 * MB,
+             ld_res=512, out=8 * MB + 512, ld_out=512, workspace=8 * MB + 512, workspace_bytes=MB)
+    assert _c_refusal("moe_int8_ffn", moe.Int8FfnArgs(**a)).startswith("workspace overlaps")
+    assert _c_refusal("moe_int8_ffn", moe.Int8FfnArgs(**{**a, "out": 8 * MB + 2})) == "out overlaps res"

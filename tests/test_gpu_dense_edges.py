@@ -1,5 +1,5 @@
 """The dense operators at the ends of their ranges: values whose intermediate products leave
-fp32, arguments that are refused, and calls after an error of the caller's own.
+fp32, layouts that share a buffer, and calls after an error of the caller's own.
 
 Tolerances count roundings: one to fp32 is off by at most 2^-24 of its value, one to bf16 by
 2^-8; a bf16 result under 2^-126 is a multiple of 2^-133 and off by half of that."""
@@ -177,3 +177,30 @@ def test_broadcast_rows_are_refused(moe):
     a = moe.int8_matmul(q, s, w, sw, torch.empty(T, N, device="cuda"), y_in=v.expand(T, N).contiguous())
     b = moe.int8_matmul(q, s, w, sw, torch.empty(T, N, device="cuda"), bias=v)
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T", [1, 5, 37, 300])
+def test_columns_of_one_buffer(moe, T):
+    """Matrices side by side in one buffer, as a fused projection leaves them."""
+    g, H, N = _gen(T), 128, 256
+    both = torch.full((T, 2 * H + 3), 77, device="cuda", dtype=torch.bfloat16)
+    x, n = both[:, :H], both[:, H: 2 * H]
+    x.copy_(_rn(g, T, H))
+    w, one = _rn(g, H).bfloat16(), torch.empty(T, H, device="cuda", dtype=torch.bfloat16)
+    moe.rms_norm(x, w, out=one)
+    moe.rms_norm(x, w, out=n)
+    torch.cuda.synchronize()
+    assert torch.equal(n, one) and bool((both[:, 2 * H:] == 77).all())
+    # codes of both halves into one buffer, and a product from one half over a part of the other
+    codes = torch.full((T, 2 * H), 77, device="cuda", dtype=torch.int8)
+    s, s2 = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    moe.rms_norm(x, w, x_out=None, q_out=codes[:, H:], s_out=s)
+    assert bool((codes[:, :H] == 77).all())
+    moe.quantize_rows(x, codes[:, :H], s2)
+    q, sw = _codes(g, N, H), torch.rand(N, device="cuda", generator=g)
+    outs = torch.full((T, 3 * N), 77.0, device="cuda")
+    outs[:, N: 2 * N] = _rn(g, T, N)
+    want = moe.int8_matmul(codes[:, :H].contiguous(), s2, q, sw, torch.empty(T, N, device="cuda"), y_in=outs[:, N: 2 * N])
+    moe.int8_matmul(codes[:, :H], s2, q, sw, outs[:, 2 * N:], y_in=outs[:, N: 2 * N])
+    torch.cuda.synchronize()
+    assert torch.equal(outs[:, 2 * N:], want) and bool((outs[:, :N] == 77).all())
