@@ -204,3 +204,24 @@ def test_columns_of_one_buffer(moe, T):
     moe.int8_matmul(codes[:, :H], s2, q, sw, outs[:, 2 * N:], y_in=outs[:, N: 2 * N])
     torch.cuda.synchronize()
     assert torch.equal(outs[:, 2 * N:], want) and bool((outs[:, :N] == 77).all())
+
+
+def test_block_of_the_largest_workspace(moe):
+    """2^20 tokens of 16384 intermediate channels: 80 GiB of workspace, offsets past 2^36 bytes.
+    Tokens from all over are bit for bit what they are in small calls."""
+    T, H, I = 1 << 20, 16, 16384  # noqa: E741
+    n = moe.int8_ffn_workspace(T, H, I)
+    if torch.cuda.mem_get_info()[0] < n + (4 << 30):
+        pytest.skip("needs %d GiB of device memory" % ((n >> 30) + 4))
+    g = _gen(3)
+    q, gu, dn = _codes(g, T, H), _codes(g, 2 * I, H), _codes(g, H, I)
+    sx, sgu, sdn = (torch.rand(k, device="cuda", generator=g) * 0.01 + 0.01 for k in (T, 2 * I, H))
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    out = moe.int8_ffn(q, sx, gu, sgu, dn, sdn, _out(moe, T, H, torch.float32), ws)
+    torch.cuda.synchronize()
+    assert bool(out.isfinite().all())
+    for a, b in [(0, 300), (T // 2 - 9, T // 2 + 7), (T * 13 // 16, T * 13 // 16 + 1), (T - 40, T)]:
+        part = moe.int8_ffn(q[a:b], sx[a:b], gu, sgu, dn, sdn, _out(moe, b - a, H, torch.float32), ws)
+        assert torch.equal(part, out[a:b]), (a, b)
+    del ws
+    torch.cuda.empty_cache()
