@@ -232,10 +232,9 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_int8_gemm(Int8Args a, int m
   // A half has kHalfMB slots of kNB products; the operands of the next are asked for in the
   // first of them, so that they are in when its products start, and loads follow.
   // A freed buffer is filled in this half and the next (at once, 128 x 256 tiles on 112 CUs
-  // take 43 us for 39, on 256 CUs 58 for 56.5), where the ring gives it the time.
-  constexpr int kReadSlots = kHalfMB / 2, kParts = kHalfMB - kReadSlots;
-  constexpr bool kSpread = RING > 2;
-  constexpr int kAllParts = kSpread ? 2 * kParts : kParts;
+  // take 43 us for 39, on 256 CUs 58 for 56.5), for which the ring has to hold another.
+  static_assert(RING > 2, "the next step's buffer is full before the freed one is");
+  constexpr int kReadSlots = kHalfMB / 2, kParts = kHalfMB - kReadSlots, kAllParts = 2 * kParts;
   Rows r0, r1;
   Cols c0, c1;
   int buf = 0, fill = RING - 1;
@@ -252,7 +251,7 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_int8_gemm(Int8Args a, int m
         if (BK == 128) fetch_cols(next, buf, 1, i, kReadSlots);
         fetch_rows(r1, buf, 1, i, kReadSlots);
       }
-      if (kSpread && i >= kReadSlots) stage(fill, kParts + i - kReadSlots, kAllParts);
+      if (i >= kReadSlots) stage(fill, kParts + i - kReadSlots, kAllParts);
     }
     __builtin_amdgcn_sched_barrier(0);
     const int done = buf;  // every wave has all of it in registers at the barrier
@@ -275,7 +274,7 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_int8_gemm(Int8Args a, int m
   for (int r = 0; r < RING - 1; ++r) stage(r, 0, 1);
 #pragma unroll
   for (int q = 0; q < kParts; ++q) stage(RING - 1, q, kAllParts);
-  meet_with_loads_but<(RING - 2) * kLoads + (kSpread ? kLoads / 2 : kLoads)>();
+  meet_with_loads_but<(RING - 2) * kLoads + kLoads / 2>();
   fetch_rows(r0, 0, 0, 0, 1);
   fetch_cols(c0, 0, 0, 0, 1);
   if (BK == 128) {
