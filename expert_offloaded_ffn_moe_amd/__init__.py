@@ -287,6 +287,11 @@ def _refuse(fn, msg):
     raise MoeError(MOE_E_INVALID, fn, msg)
 
 
+def _refuse_numbers(fn, **numbers):
+    """For what struct.error says of a number that its field of the ABI cannot hold."""
+    _refuse(fn, "out of range: %s" % ", ".join("%s = %s" % n for n in numbers.items()))
+
+
 def _refuse_tensor(fn, name, t, shape, dtype, dev):
     if t.dtype is not dtype:
         _refuse(fn, "%s has dtype %s, not %s" % (name, t.dtype, dtype))
@@ -374,10 +379,13 @@ def rms_norm(x, weight, eps=1e-6, add=None, x_out=None, out=None, q_out=None, s_
     adt = dt if add is None else add.dtype
     if adt is not dt and adt is not f32:
         _refuse(fn, "add has dtype %s, not %s or float32" % (adt, dt))
-    a = _pack_norm(T, H, act, act if adt is dt else ACT_F32, eps, *_mat(fn, "x", x, T, H, dt, dev),
-                   *_mat(fn, "add", add, T, H, adt, dev), _vec(fn, "weight", weight, H, dt, dev),
-                   *_mat(fn, "x_out", x_out, T, H, dt, dev), *_mat(fn, "out", out, T, H, dt, dev),
-                   *_mat(fn, "q_out", q_out, T, H, _Torch.i8, dev), _vec(fn, "s_out", s_out, T, f32, dev))
+    try:
+        a = _pack_norm(T, H, act, act if adt is dt else ACT_F32, eps, *_mat(fn, "x", x, T, H, dt, dev),
+                       *_mat(fn, "add", add, T, H, adt, dev), _vec(fn, "weight", weight, H, dt, dev),
+                       *_mat(fn, "x_out", x_out, T, H, dt, dev), *_mat(fn, "out", out, T, H, dt, dev),
+                       *_mat(fn, "q_out", q_out, T, H, _Torch.i8, dev), _vec(fn, "s_out", s_out, T, f32, dev))
+    except struct.error:
+        _refuse_numbers(fn, T=T, H=H, eps=eps)
     _run(_lib.moe_rms_norm, fn, a, dev, stream)
 
 
@@ -389,8 +397,11 @@ def quantize_rows(x, q_out, s_out, stream=None):
     fn = "moe_quantize_rows"
     T, H = _shape2(fn, "x", x)
     dev = x.get_device()
-    a = _pack_quantize(T, H, _act_of(fn, "x", x), *_mat(fn, "x", x, T, H, x.dtype, dev),
-                       *_mat(fn, "q_out", q_out, T, H, _Torch.i8, dev), _vec(fn, "s_out", s_out, T, _Torch.f32, dev))
+    try:
+        a = _pack_quantize(T, H, _act_of(fn, "x", x), *_mat(fn, "x", x, T, H, x.dtype, dev),
+                           *_mat(fn, "q_out", q_out, T, H, _Torch.i8, dev), _vec(fn, "s_out", s_out, T, _Torch.f32, dev))
+    except struct.error:
+        _refuse_numbers(fn, T=T, H=H)
     _run(_lib.moe_quantize_rows, fn, a, dev, stream)
 
 
@@ -404,11 +415,14 @@ def int8_matmul(q_x, s_x, q_w, s_w, out, bias=None, y_in=None, res=None, stream=
     T, K = _shape2(fn, "q_x", q_x)
     N = _shape2(fn, "q_w", q_w)[0]
     dt, dev = out.dtype, q_x.get_device()
-    a = _pack_matmul(T, N, K, _act_of(fn, "out", out), *_mat(fn, "q_x", q_x, T, K, i8, dev),
-                     _vec(fn, "s_x", s_x, T, f32, dev), *_mat(fn, "q_w", q_w, N, K, i8, dev),
-                     _vec(fn, "s_w", s_w, N, f32, dev), _vec(fn, "bias", bias, N, f32, dev),
-                     *_mat(fn, "y_in", y_in, T, N, f32, dev), *_mat(fn, "res", res, T, N, dt, dev),
-                     *_mat(fn, "out", out, T, N, dt, dev))
+    try:
+        a = _pack_matmul(T, N, K, _act_of(fn, "out", out), *_mat(fn, "q_x", q_x, T, K, i8, dev),
+                         _vec(fn, "s_x", s_x, T, f32, dev), *_mat(fn, "q_w", q_w, N, K, i8, dev),
+                         _vec(fn, "s_w", s_w, N, f32, dev), _vec(fn, "bias", bias, N, f32, dev),
+                         *_mat(fn, "y_in", y_in, T, N, f32, dev), *_mat(fn, "res", res, T, N, dt, dev),
+                         *_mat(fn, "out", out, T, N, dt, dev))
+    except struct.error:
+        _refuse_numbers(fn, T=T, N=N, K=K)
     _run(_lib.moe_int8_matmul, fn, a, dev, stream)
     return out
 
@@ -417,6 +431,8 @@ def int8_ffn_workspace(T, H, I) -> int:
     """Bytes of workspace that int8_ffn needs for T tokens (moe_int8_ffn_workspace)."""
     lib = load_library()
     n = ctypes.c_size_t()
+    if not all(-(1 << 31) <= v < 1 << 31 for v in (T, H, I)):  # ctypes would drop their high bits
+        _refuse_numbers("moe_int8_ffn_workspace", T=T, H=H, I=I)
     _check(lib.moe_int8_ffn_workspace(T, H, I, ctypes.byref(n)), "moe_int8_ffn_workspace")
     return int(n.value)
 
@@ -431,12 +447,15 @@ def int8_ffn(q_x, s_x, q_gu, s_gu, q_dn, s_dn, out, workspace, y_in=None, res=No
     T, H = _shape2(fn, "q_x", q_x)
     I = _shape2(fn, "q_dn", q_dn)[1]
     dt, dev, n = out.dtype, q_x.get_device(), workspace.numel()
-    a = _pack_ffn(T, H, I, _act_of(fn, "out", out), *_mat(fn, "q_x", q_x, T, H, i8, dev),
-                  _vec(fn, "s_x", s_x, T, f32, dev), *_mat(fn, "q_gu", q_gu, 2 * I, H, i8, dev),
-                  _vec(fn, "s_gu", s_gu, 2 * I, f32, dev), *_mat(fn, "q_dn", q_dn, H, I, i8, dev),
-                  _vec(fn, "s_dn", s_dn, H, f32, dev), *_mat(fn, "y_in", y_in, T, H, f32, dev),
-                  *_mat(fn, "res", res, T, H, dt, dev), *_mat(fn, "out", out, T, H, dt, dev),
-                  _vec(fn, "workspace", workspace, n, _Torch.u8, dev), n)
+    try:
+        a = _pack_ffn(T, H, I, _act_of(fn, "out", out), *_mat(fn, "q_x", q_x, T, H, i8, dev),
+                      _vec(fn, "s_x", s_x, T, f32, dev), *_mat(fn, "q_gu", q_gu, 2 * I, H, i8, dev),
+                      _vec(fn, "s_gu", s_gu, 2 * I, f32, dev), *_mat(fn, "q_dn", q_dn, H, I, i8, dev),
+                      _vec(fn, "s_dn", s_dn, H, f32, dev), *_mat(fn, "y_in", y_in, T, H, f32, dev),
+                      *_mat(fn, "res", res, T, H, dt, dev), *_mat(fn, "out", out, T, H, dt, dev),
+                      _vec(fn, "workspace", workspace, n, _Torch.u8, dev), n)
+    except struct.error:
+        _refuse_numbers(fn, T=T, H=H, I=I)
     _run(_lib.moe_int8_ffn, fn, a, dev, stream)
     return out
 

@@ -153,3 +153,26 @@ def test_columns_of_one_buffer_get_by():
              ld_res=512, out=8 * MB + 512, ld_out=512, workspace=8 * MB + 512, workspace_bytes=MB)
     assert _c_refusal("moe_int8_ffn", moe.Int8FfnArgs(**a)).startswith("workspace overlaps")
     assert _c_refusal("moe_int8_ffn", moe.Int8FfnArgs(**{**a, "out": 8 * MB + 2})) == "out overlaps res"
+
+
+def test_sizes_beyond_the_abi():
+    """Sizes and numbers that the C structs cannot hold are refused like others out of range."""
+    for sizes in [((1 << 32) + 3, 256, 64), (3, (1 << 32) + 256, 64), (3, 256, (1 << 32) + 64), (-(1 << 32) + 3, 256, 64)]:
+        with pytest.raises(moe.MoeError) as e:
+            moe.int8_ffn_workspace(*sizes)
+        assert e.value.status == moe.MOE_E_INVALID
+    rows = (1 << 31) + 16
+    far = lambda *n, dt=I8: torch.empty(*n, dtype=dt, device="meta")  # noqa: E731
+    many = dict(T=far(rows, 16), v=far(rows, dt=F32), out=far(rows, 16, dt=BF))
+    calls = [
+        lambda: moe.rms_norm(many["out"], far(16, dt=BF), out=many["out"]),
+        lambda: moe.quantize_rows(many["out"], many["T"], many["v"]),
+        lambda: moe.int8_matmul(many["T"], many["v"], far(16, 16), far(16, dt=F32), many["out"]),
+        lambda: moe.int8_matmul(far(16, 16), far(16, dt=F32), many["T"], many["v"], far(16, rows, dt=BF)),
+        lambda: moe.int8_ffn(many["T"], many["v"], far(32, 16), far(32, dt=F32), far(16, 16), far(16, dt=F32), many["out"],
+                             far(256, dt=U8)),
+    ]
+    for f in calls:
+        with pytest.raises(moe.MoeError) as e:
+            f()
+        assert e.value.status == moe.MOE_E_INVALID
