@@ -225,3 +225,141 @@ def test_block_of_the_largest_workspace(moe):
         assert torch.equal(part, out[a:b]), (a, b)
     del ws
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 1 << 24, 16), (17, 1 << 24, 16), (1 << 20, 1, 16), (1 << 20, 33, 32), (5, 1 << 24, 32)])
+def test_matmul_of_the_largest_sizes(moe, T, N, K):
+    g = _gen(6)
+    q, w = _codes(g, T, K), _codes(g, N, K)
+    out = moe.int8_matmul(q, torch.ones(T, device="cuda"), w, torch.ones(N, device="cuda"), _out(moe, T, N, torch.float32))
+    # sums under 2^24, exact in fp32
+    assert torch.equal(out, q.float() @ w.float().t())
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_norm_and_codes_of_the_most_rows(moe, act):
+    T, H, g, dt = 1 << 20, 5, _gen(7), ACT[act]
+    x, w = _rn(g, T, H).to(dt), (1 + 0.1 * _rn(g, H)).to(dt)
+    out, q, s = torch.empty_like(x), torch.empty(T, H, dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+    moe.rms_norm(x, w, 1e-6, out=out, q_out=q, s_out=s)
+    n = x.to(D) / (x.to(D).square().mean(1, keepdim=True) + float(np.float32(1e-6))).sqrt() * w.to(D)
+    assert bool(((out.to(D) - n).abs() <= (RBF + 2.02 * R32 if act == "bf16" else 1.01 * R32) * n.abs() + 2.0 ** -134).all())
+    p = x.to(D) * w.to(D)
+    assert torch.equal(q.to(D), torch.round(127 * p / p.abs().amax(1, keepdim=True)))
+    moe.quantize_rows(x, q, s)
+    top = x.to(D).abs().amax(1)
+    assert torch.equal(q.to(D), torch.round(127 * x.to(D) / top[:, None]))
+    assert bool(((s.to(D) - top / 127).abs() <= 1.01 * R32 * top / 127).all())
+
+
+def test_block_of_the_longest_rows(moe):
+    """131056 channels, the most: a sum of K for the gated product, channels for the second."""
+    T, H, I = 20, 131056, 32  # noqa: E741
+    g = _gen(8)
+    q, gu, dn = _codes(g, T, H), _codes(g, 2 * I, H), _codes(g, H, I)
+    sx, sgu, sdn = (torch.rand(k, device="cuda", generator=g) + 0.5 for k in (T, 2 * I, H))
+    sgu /= 5000 * H ** 0.5
+    run = lambda a, b: moe.int8_ffn(q[a:b], sx[a:b], gu, sgu, dn, sdn, _out(moe, b - a, H, torch.float32),  # noqa: E731
+                                    torch.empty(moe.int8_ffn_workspace(b - a, H, I), dtype=torch.uint8, device="cuda"))
+    whole = run(0, T)
+    for a, b in [(0, 1), (3, 19), (7, 9)]:
+        assert torch.equal(run(a, b), whole[a:b])
+    import test_gpu_dense as TD
+    p, tol, _ = TD._ffn_ref(q, sx, gu, sgu, dn, sdn)
+    assert bool(((whole.to(D) - p).abs() <= tol * 1.01 + TD._product_tol(p.abs() + tol, [], "f32")).all())
+
+
+def test_over_every_input_that_may_be(moe):
+    """The norm over its x (the sum over its addend), a product over y_in and res at once."""
+    g, H = _gen(9), 900
+    for T in (1, 6, 700):
+        x, r, w = _rn(g, T, H), _rn(g, T, H), _rn(g, H)
+        xo, out = torch.empty_like(x), torch.empty_like(x)
+        moe.rms_norm(x, w, add=r, x_out=xo, out=out)
+        moe.rms_norm(x, w, add=r, x_out=r, out=x)
+        assert torch.equal(x, out) and torch.equal(r, xo)
+        moe.rms_norm(x, w, out=out)
+        moe.rms_norm(x, w, out=x)
+        assert torch.equal(x, out)
+        moe.rms_norm(x, w, add=x, out=out)
+        moe.rms_norm(x, w, add=x, out=x)
+        assert torch.equal(x, out)
+        q, wq, y = _codes(g, T, 64), _codes(g, H, 64), _rn(g, T, H)
+        sx, sw = torch.rand(T, device="cuda", generator=g), torch.rand(H, device="cuda", generator=g)
+        want = moe.int8_matmul(q, sx, wq, sw, torch.empty_like(y), y_in=y, res=y)
+        assert torch.equal(moe.int8_matmul(q, sx, wq, sw, y, y_in=y, res=y), want)
+
+
+def test_two_threads_at_once(moe):
+    """Calls from two threads, refused ones among them, each with its own stream and buffers."""
+    import threading
+    cases, wants, faults = [], [], []
+    for k, (T, H, I) in enumerate([(2, 1024, 256), (90, 512, 768)]):  # noqa: E741
+        g = _gen(30 + k)
+        q, gu, dn = _codes(g, T, H), _codes(g, 2 * I, H), _codes(g, H, I)
+        sx, sgu, sdn = (torch.rand(n, device="cuda", generator=g) * 0.01 for n in (T, 2 * I, H))
+        ws = torch.empty(moe.int8_ffn_workspace(T, H, I), dtype=torch.uint8, device="cuda")
+        cases.append((q, sx, gu, sgu, dn, sdn, _out(moe, T, H, torch.float32), ws))
+        wants.append(moe.int8_ffn(*cases[k]).clone())
+    torch.cuda.synchronize()
+
+    def work(k):
+        stream = torch.cuda.Stream()
+        for _ in range(200):
+            moe.int8_ffn(*cases[k], stream=stream)
+            try:
+                moe.int8_ffn(*cases[k][:6], cases[k][6][:, : 16 * (k + 1)], cases[k][7], stream=stream)
+                faults.append("not refused")
+            except moe.MoeError as e:
+                if "%d)" % (16 * (k + 1)) not in str(e):
+                    faults.append(str(e))
+        stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not faults
+    for k in range(2):
+        assert torch.equal(cases[k][6], wants[k])
+
+
+def test_tiles_captured_twice_on_one_workspace(moe):
+    """Two graphs that share a workspace and a stream, replayed in turn with eager calls between."""
+    T, H, I = 300, 512, 256  # noqa: E741
+    g = _gen(40)
+    gu, dn, q, sx = _codes(g, 2 * I, H), _codes(g, H, I), _codes(g, 2 * T, H), torch.rand(2 * T, device="cuda", generator=g) * 0.01
+    sgu, sdn = torch.rand(2 * I, device="cuda", generator=g) * 0.01, torch.rand(H, device="cuda", generator=g)
+    ws = torch.empty(moe.int8_ffn_workspace(T, H, I), dtype=torch.uint8, device="cuda")
+    x, w = _rn(g, T, H), _rn(g, H)
+    codes, scales, side = torch.empty(T, H, dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda"), torch.cuda.Stream()
+    outs = [_out(moe, T, H, torch.float32) for _ in range(2)]
+    calls = [lambda: moe.int8_ffn(q[:T], sx[:T], gu, sgu, dn, sdn, outs[0], ws),
+             lambda: (moe.rms_norm(x, w, q_out=codes, s_out=scales),
+                      moe.int8_ffn(codes, scales, gu, sgu, dn, sdn, outs[1], ws, res=x))]
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in calls]
+    with torch.cuda.stream(side):
+        for graph, call in zip(graphs, calls):
+            call()
+            torch.cuda.synchronize()
+            with torch.cuda.graph(graph, stream=side):
+                call()
+    torch.cuda.synchronize()
+    for i in range(4):
+        x.copy_(_rn(g, T, H))
+        q.copy_(_codes(g, 2 * T, H))
+        wants = []
+        for call, out in zip(calls, outs):
+            call()
+            torch.cuda.synchronize()
+            wants.append(out.clone())
+            out.zero_()
+        ws.fill_(255)
+        with torch.cuda.stream(side):
+            for graph in graphs:
+                graph.replay()
+        torch.cuda.synchronize()
+        for out, want in zip(outs, wants):
+            assert torch.equal(out, want), i
