@@ -10,9 +10,9 @@
 // rows and their 8 up rows) and all tokens; its eight waves split K, each reading blocks of
 // two 64-byte steps, and meet in LDS. Weights go from memory to registers with 16-byte loads,
 // all loads of a block before its products; the activations, which every workgroup reads,
-// come from cache the same way. Measured with weights from HBM (a plain copy: 5.1 TB/s): one
-// token on 7168 x 7168 10.8 us (4.8 TB/s), on 4096 x 7168 6.1, gated 2 x 2048 x 7168 6.5
-// (4.5 TB/s), 16 tokens on the last two 8.3 and 8.4 us. Four steps a block: 7% longer for the first;
+// come from cache the same way. Measured with inputs and outputs all from HBM (a plain copy:
+// 5.1 TB/s): one token on 7168 x 7168 10.9 us (4.7 TB/s), on 4096 x 7168 8.1, 16 tokens 9.4 us (one
+// set of buffers in a loop: 9.6, 5.9 and 8.2). Four steps a block: 7% longer for the first;
 // sixteen waves: the same within 3%, four: 20% longer; the next block's loads ahead of this
 // one's products, in twice the registers: 15% longer.
 #include <hip/hip_runtime.h>
@@ -112,9 +112,9 @@ __global__ __launch_bounds__(64 * kWaves) void k_int8_skinny(Int8Args a) {
 // The second half of the gated block for up to 16 tokens: as k_int8_skinny, with the
 // activations' codes formed in LDS from h first, while the first weights are on their way.
 // Each workgroup reads and codes all of h, which costs less than a launch of its own for as
-// long as h is small: one token of the 7168/2048 block 12.0 us (with the codes in a launch of
-// their own 14.4), 16 of the 2048/768 one 11.3 (14.9), but 16 of the first, 32768 elements,
-// 18.3 us on the GPU (17.8). A row of h is shared by kWaves / T waves at least, in registers
+// long as h is small: calls of one token of the 7168/2048 block 12.3 us (with the codes in a
+// launch of their own 14.7), of 16 of the 2048/768 one 11.3 (15.0), but of 16 of the first,
+// 32768 elements, 17.4 (17.0). A row of h is shared by kWaves / T waves at least, in registers
 // of kHeld elements a lane.
 constexpr int kHeld = 32;
 constexpr int kDownTokens = 16, kDownElements = 16384;
@@ -230,8 +230,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_int8_down(Int8Args a, const flo
 }
 
 // Two blocks a workgroup share each load of the activations, if that leaves three quarters of
-// the 256 CUs a workgroup: 16 tokens on 7168 x 7168 14.2 us (one block: 16.9), on 4096 x 2048
-// 5.2 us (4.0).
+// the 256 CUs a workgroup: 12 tokens on 7168 x 7168 12.4 us (one block: 15.1), on 4096 x 2048
+// 16 tokens take 5.9 us that way (4.8); for one token it makes no difference.
 bool two_blocks(int blocks) { return blocks >= 2 * 192; }
 
 template <bool GATED, bool BF16>

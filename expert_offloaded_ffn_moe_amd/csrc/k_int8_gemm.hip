@@ -19,12 +19,12 @@
 // barrier that frees the oldest buffer and opens the next stands between the two, so that
 // it, too, is covered by products.
 //
-// What bounds it: 2048 x 7168 x 7168 takes 93 us (2.27 POPS) in a loop over one set of
-// buffers, 99 us on inputs from HBM. A 64-byte step of the 256 x 256 tile is 1088 cycles of
-// its MFMAs and runs in about 1390, at the 1.8 GHz that the power limit leaves; without the
-// loads the same loop takes 73 us, on loads that all hit L2 98% of its time, so it is their
-// way into LDS beside the products that costs, not memory. The rest, about 10 us, is the
-// launch, the first loads and the epilogue's bytes.
+// What bounds it: 2048 x 7168 x 7168 takes 97 us (2.17 POPS) in a loop over one set of
+// buffers, 103 us with inputs and outputs all from HBM. A 64-byte step of the 256 x 256 tile is
+// 1088 cycles of its MFMAs and runs in about 1390, at the 1.8 GHz that the power limit
+// leaves; without the loads the same loop takes 73 us, and on loads that all hit L2 98% of
+// its time, so it is their way into LDS beside the products that costs, not memory. The
+// rest, about 10 us, is the launch, the first loads and the epilogue's bytes.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -328,13 +328,14 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_int8_gemm(Int8Args a, int m
 // The tiles, and what 128 bytes of K cost a CU in each (us), measured on products of 64 to
 // 2048 tokens with 2048 to 7168 channels and K. A large tile reads the fewest bytes per
 // product, but too few of them leave CUs idle: the tile whose rounds over the 256 CUs cost
-// least is taken. Against the next best tile that gives, at K = 7168: 2048 x 7168 93 us (128
-// x 256: 99), 2048 x 4096 54 (128 x 128: 64), 1024 x 7168 50 (128 x 128: 61), 512 x 7168 29
-// (64 x 128: 35), 256 x 7168 21 (64 x 64: 24), 128 x 7168 14 (64 x 128: 21). The smaller
-// tiles are short of products to cover a step's LDS reads and barrier, so that two or four
-// groups of waves take the steps in turn (64 x 64 in one group: 18.3 us for 128 x 7168;
-// 64 x 32 11.2 and 64 x 64 13.1 us for 128 x 4096; 32 x 32 8.2, 64 x 32 9.1 and 64 x 64 11.1
-// us for 64 x 4096).
+// least is taken. Against the next best tile that gives, at K = 7168, in a loop over one set
+// of buffers: 2048 x 7168 97 us (128 x 256: 99), 2048 x 4096 59 (128 x 128: 66), 1024 x 7168
+// 54 (128 x 128: 59), 512 x 7168 33 (64 x 128: 39), 300 x 7168 28 (64 x 128: 36), 256 x 7168
+// 21 (64 x 64: 26), 128 x 7168 14.8 (64 x 128: 18.4), 64 x 7168 12.5 (64 x 64: 13.7). The
+// smaller tiles are short of products to cover a step's LDS reads and barrier, so that two or
+// four groups of waves take the steps in turn (64 x 64 in one group: 18.3 us for 128 x 7168;
+// 64 x 32 11.3 and 64 x 64 13.2 us for 128 x 4096; 32 x 32 8.4, 64 x 32 9.1 and 64 x 64 11.1
+// us for 64 x 4096). 257 to 384 tokens run as 384 rows, on 160 to 168 CUs of the larger shapes.
 struct Tile {
   int tokens, channels;
   float cost;

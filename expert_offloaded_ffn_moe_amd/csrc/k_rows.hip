@@ -365,10 +365,14 @@ __global__ __launch_bounds__(MAX) void k_rows(RowArgs a) {
 // (4096 rows of 2048: 18.2 us, a wave of four chunks 23.5; 2048 rows of 2560: 14.8 us, eight
 // waves of two chunks 20.6), longer ones 8 or 16 waves at two chunks a thread (2048 rows of
 // 7168: 35.8 us, with one chunk a thread 36.6, with four 43, and on the seven waves that
-// would hold them 42). The norm's workgroups are half of what fits the 256 CUs and go on to
-// further rows, their loads a row ahead (twice as many: 37.5 us; one row each: 43 before rows
-// were loaded ahead); the codes alone, with fewer registers, take one row each (2048 x 7168
-// rows: 8.9 us, 10.6 as the norm does).
+// would hold them 42). The norm runs 16 waves a CU, which go on to further rows, their loads a
+// row ahead (twice as many: 37.5 us; one row each: 43 before rows were loaded ahead). That is
+// what the registers let on a CU for rows of more than 4096, about half of it for shorter ones,
+// and twice of it for fp32 rows of 4097 to 8192, whose halves run one after the other (2048 rows
+// of 7168, norm with the sum: 58 us, 4.0 TB/s). fp32 rows above 8192 spill 30 to 62 registers a
+// lane (1024 rows of 16384: 106 us, 2.5 TB/s; 2048 of bf16, with codes, 74 us, 5.0 TB/s). The
+// codes alone, with fewer registers, take one row each (2048 x 7168 rows: 8.9 us, 10.6 as the
+// norm does).
 template <typename ACT, bool NORM, int ADD>
 void launch(const RowArgs& a, hipStream_t s) {
 #define ROWS(WAVE, MAX, NC)                                                                                        \

@@ -431,7 +431,8 @@ moe_status moe_debug_live_allocs(int64_t* device, int64_t* host);
  * Codes of a row v: scale = max|v| / 127 (fp32), code = round half even(127 v / max|v|),
  * in -127..127; the value is code * scale. A row with a NaN or an infinity (a product of
  * the norm beyond fp32's range counts as one) has scale NaN and codes 0, so that every
- * product with it is NaN; one whose largest size is under 2^-100 has scale and codes 0.
+ * product with it is NaN; one whose largest size (of the norm: of s * weight, before the
+ * row's size divides it) is under 2^-100 has scale and codes 0.
  *
  * Conventions, besides those above:
  *  - A matrix has rows of consecutive elements and a row stride ld_* in elements; 0
@@ -524,11 +525,12 @@ moe_status moe_int8_matmul(const moe_int8_matmul_args* args, moe_stream stream);
  *   h = silu(Wg x) * (Wu x) in fp32, from exact sums; h' = codes of each token's h
  *   out[t][n] = act( (Wd h')[t][n] + y_in[t][n] + res[t][n] )
  * with x = q_x * s_x and each weight its code times its channel's scale. q_gu holds the
- * I gate rows, then the I up rows. A code of h may differ by one step from that of
- * exactly computed h where 127 h / max|h| lies next to a half; a token's output does not
- * depend on the call's other tokens. The workspace holds
- * what moe_int8_ffn_workspace says, 256-byte aligned; its contents need not be kept,
- * and calls that overlap in time need one each. out may be res or y_in themselves. */
+ * I gate rows, then the I up rows. silu of less than -88.7, under 2^-121 in size, is taken
+ * for 0, and a token whose h leaves fp32's range is NaN. A code of h may differ by one
+ * step from that of exactly computed h where 127 h / max|h| lies next to a half; a token's
+ * output does not depend on the call's other tokens. The workspace holds what
+ * moe_int8_ffn_workspace says, 256-byte aligned; its contents need not be kept, and calls
+ * that overlap in time need one each. out may be res or y_in themselves. */
 typedef struct {
   int32_t T;              /* tokens, 0..2^20 */
   int32_t H;              /* multiple of 16, 16..131056 */
