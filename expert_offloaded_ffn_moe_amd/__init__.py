@@ -101,6 +101,33 @@ class Int8FfnArgs(ctypes.Structure):
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
+class Fp8QuantizeArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("act_dtype", ctypes.c_int32),
+                ("block_rows", ctypes.c_int32), ("x", ctypes.c_void_p), ("ld_x", ctypes.c_int64),
+                ("q_out", ctypes.c_void_p), ("ld_q", ctypes.c_int64), ("s_out", ctypes.c_void_p),
+                ("ld_s", ctypes.c_int64)]
+
+
+class Fp8MatmulArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("q_x", ctypes.c_void_p), ("ld_x", ctypes.c_int64), ("s_x", ctypes.c_void_p),
+                ("ld_sx", ctypes.c_int64), ("q_w", ctypes.c_void_p), ("ld_w", ctypes.c_int64),
+                ("s_w", ctypes.c_void_p), ("ld_sw", ctypes.c_int64), ("bias", ctypes.c_void_p),
+                ("y_in", ctypes.c_void_p), ("ld_y", ctypes.c_int64), ("res", ctypes.c_void_p),
+                ("ld_res", ctypes.c_int64), ("out", ctypes.c_void_p), ("ld_out", ctypes.c_int64)]
+
+
+class Fp8LayerArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("I", ctypes.c_int32), ("E", ctypes.c_int32),
+                ("k", ctypes.c_int32), ("act_dtype", ctypes.c_int32), ("x", ctypes.c_void_p),
+                ("ld_x", ctypes.c_int64), ("router_w", ctypes.c_void_p), ("ld_router", ctypes.c_int64),
+                ("router_b", ctypes.c_void_p), ("logits_in", ctypes.c_void_p), ("q_gu", ctypes.c_void_p),
+                ("s_gu", ctypes.c_void_p), ("q_dn", ctypes.c_void_p), ("s_dn", ctypes.c_void_p),
+                ("y", ctypes.c_void_p), ("ld_y", ctypes.c_int64), ("x_out", ctypes.c_void_p),
+                ("ld_x_out", ctypes.c_int64), ("logits", ctypes.c_void_p), ("topk_ids", ctypes.c_void_p),
+                ("topk_w", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
 KERNELS = ["router", "route", "gateup", "down", "combine", "gemm_gateup", "gemm_down", "stage"]
 
 
@@ -159,6 +186,10 @@ def load_library(path: str = LIB_PATH, with_torch: bool = True):
     lib.moe_int8_matmul.argtypes = [vp, vp]  # a Int8MatmulArgs
     lib.moe_int8_ffn_workspace.argtypes = [i32, i32, i32, ctypes.POINTER(ctypes.c_size_t)]
     lib.moe_int8_ffn.argtypes = [vp, vp]  # a Int8FfnArgs
+    lib.moe_fp8_quantize.argtypes = [vp, vp]  # a Fp8QuantizeArgs
+    lib.moe_fp8_matmul.argtypes = [vp, vp]  # a Fp8MatmulArgs
+    lib.moe_fp8_layer_workspace.argtypes = [i32] * 5 + [ctypes.POINTER(ctypes.c_size_t)]
+    lib.moe_fp8_layer.argtypes = [vp, vp]  # a Fp8LayerArgs
     lib.moe_plan_destroy.argtypes = [vp]
     lib.moe_plan_destroy.restype = None
     lib.moe_status_str.argtypes = [st]
@@ -170,7 +201,8 @@ def load_library(path: str = LIB_PATH, with_torch: bool = True):
                "moe_plan_profile", "moe_plan_kernel_times", "moe_plan_get_info", "moe_measure_link_ceilings",
                "moe_debug_fail_alloc", "moe_debug_live_allocs", "moe_plan_set_host_compute",
                "moe_prefetch", "moe_plan_prefetch_slots", "moe_rms_norm", "moe_quantize_rows", "moe_int8_matmul",
-               "moe_int8_ffn_workspace", "moe_int8_ffn"):
+               "moe_int8_ffn_workspace", "moe_int8_ffn", "moe_fp8_quantize", "moe_fp8_matmul",
+               "moe_fp8_layer_workspace", "moe_fp8_layer"):
         getattr(lib, fn).restype = st
     _lib = lib
     return lib
@@ -268,6 +300,7 @@ def _packer(mirror):
 
 _pack_norm, _pack_quantize = _packer(RmsNormArgs), _packer(QuantizeArgs)
 _pack_matmul, _pack_ffn = _packer(Int8MatmulArgs), _packer(Int8FfnArgs)
+_pack_fp8_quantize, _pack_fp8_matmul, _pack_fp8_layer = _packer(Fp8QuantizeArgs), _packer(Fp8MatmulArgs), _packer(Fp8LayerArgs)
 
 
 class _Torch:
@@ -279,6 +312,7 @@ def _load_torch():
     import torch
     load_library()
     _Torch.f32, _Torch.bf16, _Torch.i8, _Torch.u8 = torch.float32, torch.bfloat16, torch.int8, torch.uint8
+    _Torch.f8, _Torch.i32 = torch.float8_e4m3fn, torch.int32
     _Torch.stream, _Torch.device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
     _Torch.acts = {torch.bfloat16: ACT_BF16, torch.float32: ACT_F32}
 
@@ -292,7 +326,7 @@ def _refuse_numbers(fn, **numbers):
     _refuse(fn, "out of range: %s" % ", ".join("%s = %s" % n for n in numbers.items()))
 
 
-def _refuse_tensor(fn, name, t, shape, dtype, dev):
+def _refuse_tensor(fn, name, t, shape, dtype, dev, layout="the elements of a row are not consecutive"):
     if t.dtype is not dtype:
         _refuse(fn, "%s has dtype %s, not %s" % (name, t.dtype, dtype))
     if t.get_device() < 0:
@@ -301,7 +335,7 @@ def _refuse_tensor(fn, name, t, shape, dtype, dev):
         _refuse(fn, "%s is on another GPU than the other tensors" % name)
     if t.shape != shape:
         _refuse(fn, "%s has shape %s, not %s" % (name, tuple(t.shape), shape))
-    _refuse(fn, "%s: the elements of a row are not consecutive" % name)
+    _refuse(fn, "%s: %s" % (name, layout))
 
 
 def _mat(fn, name, t, rows, cols, dtype, dev):
@@ -329,6 +363,15 @@ def _vec(fn, name, t, n, dtype, dev):
     if t.dtype is dtype and t.get_device() == dev and t.shape == (n,) and t.is_contiguous():
         return t.data_ptr()
     _refuse_tensor(fn, name, t, (n,), dtype, dev)
+
+
+def _packed(fn, name, t, shape, dtype, dev):
+    """Address of a packed tensor of any number of dimensions, 0 for None."""
+    if t is None:
+        return 0
+    if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    _refuse_tensor(fn, name, t, shape, dtype, dev, "it is not packed")
 
 
 def _act_of(fn, name, t):
@@ -458,6 +501,94 @@ def int8_ffn(q_x, s_x, q_gu, s_gu, q_dn, s_dn, out, workspace, y_in=None, res=No
         _refuse_numbers(fn, T=T, H=H, I=I)
     _run(_lib.moe_int8_ffn, fn, a, dev, stream)
     return out
+
+
+# ---- operators on e4m3 codes (torch.float8_e4m3fn) with a float32 scale for each block of 128
+
+
+def fp8_quantize(x, q_out, s_out, block_rows=1, stream=None):
+    """e4m3 codes q_out [T, H] of x [T, H] and their scales: block_rows 1, s_out float32 [T,
+    ceil(H/128)] (activations); 128, [ceil(T/128), ceil(H/128)] (a weight matrix)
+    (moe_fp8_quantize)."""
+    if _Torch.acts is None:
+        _load_torch()
+    fn = "moe_fp8_quantize"
+    T, H = _shape2(fn, "x", x)
+    dev = x.get_device()
+    if block_rows != 1 and block_rows != 128:
+        _refuse(fn, "block_rows is %s, neither 1 nor 128" % (block_rows,))
+    try:
+        a = _pack_fp8_quantize(T, H, _act_of(fn, "x", x), block_rows, *_mat(fn, "x", x, T, H, x.dtype, dev),
+                               *_mat(fn, "q_out", q_out, T, H, _Torch.f8, dev),
+                               *_mat(fn, "s_out", s_out, -(-T // block_rows), (H + 127) // 128, _Torch.f32, dev))
+    except struct.error:
+        _refuse_numbers(fn, T=T, H=H)
+    _run(_lib.moe_fp8_quantize, fn, a, dev, stream)
+
+
+def fp8_matmul(q_x, s_x, q_w, s_w, out, bias=None, y_in=None, res=None, stream=None):
+    """out [T, N] = act(x @ w.T + bias + y_in + res) of e4m3 codes q_x [T, K] with scales s_x
+    [T, ceil(K/128)] and q_w [N, K] with scales s_w [ceil(N/128), ceil(K/128)]; bias float32
+    [N], y_in float32 [T, N], res in out's dtype; out may be y_in or res (moe_fp8_matmul)."""
+    if _Torch.acts is None:
+        _load_torch()
+    fn, f32, f8 = "moe_fp8_matmul", _Torch.f32, _Torch.f8
+    T, K = _shape2(fn, "q_x", q_x)
+    N = _shape2(fn, "q_w", q_w)[0]
+    dt, dev, KB = out.dtype, q_x.get_device(), (K + 127) // 128
+    try:
+        a = _pack_fp8_matmul(T, N, K, _act_of(fn, "out", out), *_mat(fn, "q_x", q_x, T, K, f8, dev),
+                             *_mat(fn, "s_x", s_x, T, KB, f32, dev), *_mat(fn, "q_w", q_w, N, K, f8, dev),
+                             *_mat(fn, "s_w", s_w, (N + 127) // 128, KB, f32, dev), _vec(fn, "bias", bias, N, f32, dev),
+                             *_mat(fn, "y_in", y_in, T, N, f32, dev), *_mat(fn, "res", res, T, N, dt, dev),
+                             *_mat(fn, "out", out, T, N, dt, dev))
+    except struct.error:
+        _refuse_numbers(fn, T=T, N=N, K=K)
+    _run(_lib.moe_fp8_matmul, fn, a, dev, stream)
+    return out
+
+
+def fp8_layer_workspace(T, H, I, E, k) -> int:
+    """Bytes of workspace that fp8_layer needs for T tokens (moe_fp8_layer_workspace)."""
+    lib = load_library()
+    n = ctypes.c_size_t()
+    if not all(-(1 << 31) <= v < 1 << 31 for v in (T, H, I, E, k)):  # ctypes would drop their high bits
+        _refuse_numbers("moe_fp8_layer_workspace", T=T, H=H, I=I, E=E, k=k)
+    _check(lib.moe_fp8_layer_workspace(T, H, I, E, k, ctypes.byref(n)), "moe_fp8_layer_workspace")
+    return int(n.value)
+
+
+def fp8_layer(x, router_w, q_gu, s_gu, q_dn, s_dn, k, y, workspace, router_b=None, logits_in=None, x_out=None,
+              logits=None, topk_ids=None, topk_w=None, stream=None):
+    """A whole routed layer of up to 64 tokens on e4m3 experts, without a plan: x [T, H],
+    router_w [E, H] in its dtype (or float32 logits_in [T, E]), q_gu [E, 2I, H] (gate rows, then
+    up rows) with s_gu [E, 2, ceil(I/128), ceil(H/128)], q_dn [E, H, I] with s_dn [E, ceil(H/128),
+    ceil(I/128)]; writes y float32 [T, H] and, where given, x_out = x + y, logits [T, E],
+    topk_ids int32 and topk_w [T, k]. workspace: a uint8 tensor of fp8_layer_workspace(T, H, I,
+    E, k) bytes, one for each call in flight (moe_fp8_layer)."""
+    if _Torch.acts is None:
+        _load_torch()
+    fn, f32, f8 = "moe_fp8_layer", _Torch.f32, _Torch.f8
+    T, H = _shape2(fn, "x", x)
+    if q_dn.dim() != 3:
+        _refuse(fn, "q_dn has %d dimensions, not 3" % q_dn.dim())
+    E, _, I = q_dn.shape  # noqa: E741
+    dt, dev, n, HB, IB = x.dtype, x.get_device(), workspace.numel(), (H + 127) // 128, (I + 127) // 128
+    try:
+        a = _pack_fp8_layer(T, H, I, E, k, _act_of(fn, "x", x), *_mat(fn, "x", x, T, H, dt, dev),
+                            *_mat(fn, "router_w", router_w, E, H, dt, dev), _vec(fn, "router_b", router_b, E, f32, dev),
+                            _packed(fn, "logits_in", logits_in, (T, E), f32, dev),
+                            _packed(fn, "q_gu", q_gu, (E, 2 * I, H), f8, dev),
+                            _packed(fn, "s_gu", s_gu, (E, 2, IB, HB), f32, dev),
+                            _packed(fn, "q_dn", q_dn, (E, H, I), f8, dev),
+                            _packed(fn, "s_dn", s_dn, (E, HB, IB), f32, dev), *_mat(fn, "y", y, T, H, f32, dev),
+                            *_mat(fn, "x_out", x_out, T, H, dt, dev), _packed(fn, "logits", logits, (T, E), f32, dev),
+                            _packed(fn, "topk_ids", topk_ids, (T, k), _Torch.i32, dev),
+                            _packed(fn, "topk_w", topk_w, (T, k), f32, dev), _vec(fn, "workspace", workspace, n, _Torch.u8, dev), n)
+    except struct.error:
+        _refuse_numbers(fn, T=T, H=H, I=I, E=E, k=k)
+    _run(_lib.moe_fp8_layer, fn, a, dev, stream)
+    return y
 
 
 class Plan:

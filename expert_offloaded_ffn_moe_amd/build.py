@@ -15,7 +15,8 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["api.hip", "k_route.hip", "k_gemv.hip", "k_gemv_gateup_bf16.hip", "k_gemv_gateup_f32.hip",
            "k_gemv_down_bf16.hip", "k_gemv_down_f32.hip", "k_gemm.hip", "k_stage.hip", "k_util.hip", "k_gemv_lowbit_gateup.hip",
-           "k_gemv_lowbit_down.hip", "dense.hip", "k_rows.hip", "k_int8.hip", "k_int8_gemm.hip",
+           "k_gemv_lowbit_down.hip", "dense.hip", "k_rows.hip", "k_int8.hip", "k_int8_gemm.hip", "fp8.hip", "k_fp8_quant.hip", "k_fp8.hip",
+           "k_fp8_gemm.hip", "k_fp8_layer.hip",
            "host_logic.cpp", "host_ffn.cpp"]
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-I" + os.path.join(ROOT, "include"), "-I" + CSRC]
 # packed fp32 math is kept out of every kernel

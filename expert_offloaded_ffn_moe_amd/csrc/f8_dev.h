@@ -1,0 +1,34 @@
+// e4m3 codes as operands of the bf16 matrix instruction, on which their products are exact.
+//
+// Lane layout of the 16x16x32 bf16 MFMA: lane l supplies 8 values of row l % 16 of each
+// operand at K offset 8 (l / 16), and receives the sums of column l % 16 and rows 4 (l / 16)
+// .. + 3. Which of a block's K a lane supplies is free as long as both operands agree: here
+// lane quarter q = l / 16 takes the 16-byte pieces q and 4 + q of a block of 128 codes, each of
+// which is two of the instruction's steps.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+namespace moe {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t f8i4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8v __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(1))) const f8i4 g_f8i4;
+
+// Eight codes as bf16 (every e4m3 number is one; a NaN stays one).
+__device__ __forceinline__ bf16x8v f8_to_bf16(int lo, int hi) {
+  const bf16x2v a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true);
+  const bf16x2v c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true);
+  return bf16x8v{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+__device__ __forceinline__ f32x4 mfma_bf16(const bf16x8v& a, const bf16x8v& b, const f32x4& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+}  // namespace moe

@@ -557,6 +557,113 @@ typedef struct {
 moe_status moe_int8_ffn_workspace(int32_t T, int32_t H, int32_t I, size_t* bytes);
 moe_status moe_int8_ffn(const moe_int8_ffn_args* args, moe_stream stream);
 
+/* ---- Operators on 8-bit floating-point codes with a scale for each block of 128 ----
+ *
+ * The same places in a transformer's layer as the dense operators above, on weights that
+ * are kept as e4m3 numbers (OCP: 1 sign, 4 exponent and 3 mantissa bits, largest 448, 0x7F
+ * and 0xFF are NaN) with an fp32 scale for each 128 x 128 block, and a whole routed layer
+ * of a few tokens on experts kept so. The dense operators' conventions hold.
+ *
+ * Codes of a block v: scale = max|v| / 448 (fp32), code = the e4m3 number nearest to
+ * 448 v / max|v|, ties to even; the value is code * scale. A block with a NaN or an infinity
+ * has scale NaN and codes 0, one whose largest size is under 2^-100 scale and codes 0.
+ * A matrix's last blocks are cut short where 128 does not divide its sizes; its scales
+ * have ceil(columns / 128) columns. */
+
+/* Codes and scales of a matrix: block_rows = 1, blocks of 128 neighbours in a row
+ * (activations; s_out [T][ceil(H/128)]), or block_rows = 128, blocks of 128 x 128 (a weight
+ * matrix [N][K]; s_out [ceil(T/128)][ceil(H/128)]). */
+typedef struct {
+  int32_t T;              /* rows, 0..2^20 */
+  int32_t H;              /* 1..2^20 */
+  int32_t act_dtype;      /* moe_act_dtype of x */
+  int32_t block_rows;     /* 1 or 128 */
+  const void* x;          /* device [T][H] */
+  int64_t ld_x;
+  uint8_t* q_out;         /* device [T][H] e4m3 */
+  int64_t ld_q;
+  float* s_out;           /* device, as above */
+  int64_t ld_s;
+} moe_fp8_quantize_args;
+moe_status moe_fp8_quantize(const moe_fp8_quantize_args* args, moe_stream stream);
+
+/* Product of such codes:
+ *   out[t][n] = act( sum_b s_x[t][b] s_w[n/128][b] sum_{k in block b} q_x[t][k] q_w[n][k]
+ *                    + bias[n] + y_in[t][n] + res[t][n] )
+ * summed in fp32, rounded once. For bf16 outputs of more than 16 tokens a block's inner sum
+ * may come from the 8-bit matrix instruction, which keeps about 17 bits below the
+ * largest of its products (2e-5 of the sum on normal codes, where the output's own rounding
+ * is 2^-8); fp32 outputs, and up to 16 tokens, are summed from exact products. A block's
+ * scales are multiplied with each other first. y_in, res and in-place outputs as in
+ * moe_int8_matmul. */
+typedef struct {
+  int32_t T;              /* tokens, 0..2^20 */
+  int32_t N;              /* channels, 1..2^24 */
+  int32_t K;              /* multiple of 16, 16..131056 */
+  int32_t out_dtype;      /* moe_act_dtype of out and res */
+  const uint8_t* q_x;     /* device [T][K] e4m3 */
+  int64_t ld_x;
+  const float* s_x;       /* device [T][ceil(K/128)] */
+  int64_t ld_sx;
+  const uint8_t* q_w;     /* device [N][K] e4m3 */
+  int64_t ld_w;
+  const float* s_w;       /* device [ceil(N/128)][ceil(K/128)] */
+  int64_t ld_sw;
+  const float* bias;      /* device [N], or NULL */
+  const float* y_in;      /* device [T][N], or NULL */
+  int64_t ld_y;
+  const void* res;        /* device [T][N], or NULL */
+  int64_t ld_res;
+  void* out;              /* device [T][N] */
+  int64_t ld_out;
+} moe_fp8_matmul_args;
+moe_status moe_fp8_matmul(const moe_fp8_matmul_args* args, moe_stream stream);
+
+/* A whole routed layer for up to 64 tokens, without a plan: every expert is in device
+ * memory, in the caller's buffers.
+ *   logits[t][e] = sum_h x[t][h] router_w[e][h] + router_b[e], summed in fp64 and rounded
+ *                  to fp32, or logits_in
+ *   ids[t][0..k) = the k largest logits, descending, ties to the lower expert id, a NaN
+ *                  before every number; w[t] = the softmax of the chosen ones
+ *   y[t] = sum_j w[t][j] Wd_e ( silu(Wg_e x[t]) * (Wu_e x[t]) ),  e = ids[t][j]
+ *   x_out[t] = act(x[t] + y[t])
+ * with each weight its code times its block's scale, all sums in fp32 and the
+ * intermediate kept in fp32. A logit of -infinity keeps its expert from counting: it has
+ * weight 0 and is not computed, also where fewer than k others are left, and a token
+ * whose logits are all -infinity has weights and y 0. Nothing of a token reaches another
+ * token's outputs, which have the same bits in any batch. Experts that no token chose
+ * are not read. The workspace holds what moe_fp8_layer_workspace says, 256-byte aligned;
+ * its contents need not be kept or set, and calls that overlap in time need one each. */
+typedef struct {
+  int32_t T;              /* tokens, 0..64 */
+  int32_t H;              /* multiple of 16, 16..131056 */
+  int32_t I;              /* multiple of 16, 16..16384 */
+  int32_t E;              /* experts, 1..1024 */
+  int32_t k;              /* experts of a token, 1..min(E, 32) */
+  int32_t act_dtype;      /* moe_act_dtype of x, router_w and x_out */
+  const void* x;          /* device [T][H] */
+  int64_t ld_x;
+  const void* router_w;   /* device [E][H]; not read with logits_in */
+  int64_t ld_router;
+  const float* router_b;  /* device [E], or NULL */
+  const float* logits_in; /* device [T][E], or NULL */
+  const uint8_t* q_gu;    /* device [E][2I][H] e4m3: an expert's gate rows, then its up rows */
+  const float* s_gu;      /* device [E][2][ceil(I/128)][ceil(H/128)]: of gate, of up */
+  const uint8_t* q_dn;    /* device [E][H][I] e4m3 */
+  const float* s_dn;      /* device [E][ceil(H/128)][ceil(I/128)] */
+  float* y;               /* device [T][H] */
+  int64_t ld_y;
+  void* x_out;            /* device [T][H], or NULL; may be x itself */
+  int64_t ld_x_out;
+  float* logits;          /* device [T][E], or NULL */
+  int32_t* topk_ids;      /* device [T][k], or NULL */
+  float* topk_w;          /* device [T][k], or NULL */
+  void* workspace;        /* device */
+  size_t workspace_bytes;
+} moe_fp8_layer_args;
+moe_status moe_fp8_layer_workspace(int32_t T, int32_t H, int32_t I, int32_t E, int32_t k, size_t* bytes);
+moe_status moe_fp8_layer(const moe_fp8_layer_args* args, moe_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,567 @@
+"""The operators on e4m3 codes with a scale for each block of 128 against their definitions in
+64 bits: codes, the matrix product, the whole routed layer of a few tokens, and a run of
+them with the dense operators.
+
+Tolerances count roundings. A rounding to fp32 is off by at most 2^-24 of its value, one to
+bf16 by 2^-8 (half of finfo.eps). A sum of n fp32 terms is off by at most n 2^-24 of the sum
+of their sizes, in any order; the matrix instructions may cut where they add, which counts
+twice."""
+import sys
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+R32, RBF = 2.0 ** -24, 2.0 ** -8
+ACT = {"bf16": torch.bfloat16, "f32": torch.float32}
+F8, D = torch.float8_e4m3fn, torch.float64
+B = 128
+
+
+def _say(*a):
+    print(*a, file=sys.stderr, flush=True)
+
+
+@pytest.fixture(scope="module")
+def moe():
+    import expert_offloaded_ffn_moe_amd as m
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    m.load_library()
+    return m
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _rn(g, *n):
+    return torch.randn(*n, device="cuda", generator=g)
+
+
+def _codes(g, *n):
+    """Every finite code alike: sizes over the whole range."""
+    c = torch.randint(0, 254, n, device="cuda", dtype=torch.uint8, generator=g)
+    return (c + (c >= 127).to(torch.uint8)).view(F8)  # without 0x7F; 0xFF is not drawn
+
+
+def _normal(g, *n):
+    return (_rn(g, *n) * 100).clamp(-448, 448).to(F8)
+
+
+def _up(n):
+    return -(-n // B)
+
+
+def _full(q, s, rows=1):
+    """The values in fp64 of codes [..., R, C] with scales [..., ceil(R/rows), ceil(C/128)]."""
+    R, C = q.shape[-2:]
+    return q.to(D) * s.to(D).repeat_interleave(rows, -2)[..., :R, :].repeat_interleave(B, -1)[..., :C]
+
+
+class Padded:
+    """A matrix inside a larger buffer: a row stride of its own, rows behind the last one,
+    and a fill whose bytes must survive (and, as 0x7F bytes, is NaN for codes)."""
+
+    def __init__(self, rows, cols, ld, dtype, value=None):
+        self.buf = torch.empty((rows + 2, ld), device="cuda", dtype=dtype)
+        self.buf.view(torch.uint8).fill_(0x7F)
+        self.m = self.buf[:rows, :cols]
+        if value is not None:
+            self.m.copy_(value)
+
+    def untouched(self):
+        rows, cols = self.m.shape
+        return all(bool((t.contiguous().view(torch.uint8) == 0x7F).all()) for t in (self.buf[rows:], self.buf[:, cols:]))
+
+
+# ----------------------------------------------------------------------------- codes
+
+
+def _want_codes(v, rows):
+    """(codes' numbers, scales) of v in fp64, by the distance to every e4m3 number."""
+    T, H = v.shape
+    table = [i / 512.0 if i < 8 else (8 + i % 8) * 2.0 ** (i // 8 - 10) for i in range(127)]
+    table, c = torch.tensor(table, dtype=D, device=v.device), torch.arange(127, device=v.device)
+    q, s = torch.zeros_like(v), torch.zeros(-(-T // rows), _up(H), dtype=D, device=v.device)
+    for i in range(s.shape[0]):
+        for j in range(s.shape[1]):
+            at = (slice(i * rows, (i + 1) * rows), slice(j * B, (j + 1) * B))
+            p, top = v[at], v[at].abs().amax()
+            if not bool(torch.isfinite(v[at]).all()):
+                s[i, j] = float("nan")
+            elif top >= 2.0 ** -100:
+                s[i, j] = top / 448
+                # a tie is a quotient that fp64 holds, and so are both distances there
+                d = (448 * p.abs() / top).unsqueeze(-1).sub(table).abs()
+                near = torch.where(d == d.amin(-1, keepdim=True), c, -1)
+                even = torch.where(near % 2 == 0, near, -1).amax(-1)
+                k = torch.where(even >= 0, even, near.amax(-1))
+                q[at] = torch.copysign(table[k], p)
+    return q, s
+
+
+def _special(v):
+    """Blocks of unlike kinds at the front rows: nothing, next to nothing, huge, ties of every
+    size, numbers under the smallest, and blocks that are not finite."""
+    T, H = v.shape
+    j = torch.arange(H, dtype=torch.float32)
+    kinds = [torch.zeros(H), torch.full((H,), 2.0 ** -110), torch.full((H,), 2.0 ** 120), torch.linspace(-1, 1, H) * 2.0 ** -60]
+    ties = (8.5 + j % 8) * 2.0 ** (j % 5 + 1)  # halfway between two numbers of three bits
+    ties[0::128] = 448.0
+    small = (j % 16 + 0.5) / 512  # halfway between the subnormal numbers
+    small[0::128] = 448.0
+    kinds += [ties, -ties * 2.0 ** 100, small]
+    bad = torch.ones(H)
+    bad[H // 2] = float("inf")
+    worse = torch.ones(H)
+    worse[H - 1] = float("nan")
+    kinds += [bad, worse]
+    for i, k in enumerate(kinds):
+        if i + 1 < T:
+            v[i + 1] = k.to(v.dtype).to(v.device)
+    return v
+
+
+@pytest.mark.parametrize("T,H,act,pad", [(1, 1, "bf16", 0), (12, 7, "f32", 1), (12, 128, "bf16", 0), (11, 129, "f32", 3),
+                                         (12, 1000, "bf16", 5), (12, 1003, "f32", 0), (1, 7168, "bf16", 0), (40, 2064, "bf16", 8)])
+def test_codes_of_rows(moe, T, H, act, pad):
+    _say("codes of rows:", T, H, act, pad)
+    g, dt = _gen(T * 1009 + H), ACT[act]
+    x = Padded(T, H, H + pad, dt, _special((_rn(g, T, H) * torch.exp(_rn(g, H))).to(dt)))
+    q, s = Padded(T, H, H + 3 * pad, F8), Padded(T, _up(H), _up(H) + pad, torch.float32)
+    moe.fp8_quantize(x.m, q.m, s.m)
+    wq, ws = _want_codes(x.m.to(D), 1)
+    assert torch.equal(q.m.to(D), wq)
+    assert torch.equal(torch.isnan(s.m), torch.isnan(ws))
+    assert bool(((s.m.to(D) - ws).abs().nan_to_num() <= ws.nan_to_num() * R32).all())
+    assert x.untouched() and q.untouched() and s.untouched()
+
+
+@pytest.mark.parametrize("T,H,act,pad", [(1, 1, "f32", 0), (12, 130, "bf16", 1), (128, 128, "bf16", 0), (129, 260, "f32", 3),
+                                         (300, 513, "bf16", 0), (260, 1024, "bf16", 8)])
+def test_codes_of_squares(moe, T, H, act, pad):
+    _say("codes of squares:", T, H, act, pad)
+    g, dt = _gen(T * 1013 + H), ACT[act]
+    v = _rn(g, T, H) * torch.exp(_rn(g, H))
+    v[:128, 128:256] = 0
+    if T > 128:
+        v[128:, :128] *= 2.0 ** -105
+        v[T - 1, H - 1] = float("-inf")
+    x = Padded(T, H, H + pad, dt, v.to(dt))
+    q, s = Padded(T, H, H + 3 * pad, F8), Padded(_up(T), _up(H), _up(H) + pad, torch.float32)
+    moe.fp8_quantize(x.m, q.m, s.m, block_rows=128)
+    wq, ws = _want_codes(x.m.to(D), 128)
+    assert torch.equal(q.m.to(D), wq)
+    assert torch.equal(torch.isnan(s.m), torch.isnan(ws))
+    assert bool(((s.m.to(D) - ws).abs().nan_to_num() <= ws.nan_to_num() * R32).all())
+    assert x.untouched() and q.untouched() and s.untouched()
+
+
+def test_codes_of_many_rows(moe):
+    """More rows than a table of distances holds: against torch's own rounding, away from its ties."""
+    g = _gen(3)
+    x = _rn(g, 70000, 513).to(torch.bfloat16)
+    q, s = torch.empty(70000, 513, device="cuda", dtype=F8), torch.empty(70000, 5, device="cuda")
+    moe.fp8_quantize(x, q, s)
+    top = torch.stack([x[:, j:j + B].float().abs().amax(1) for j in range(0, 513, B)], 1)
+    assert bool(((s.to(D) - top.to(D) / 448).abs() <= top.to(D) / 448 * R32).all())
+    # 448 v / top of bf16 numbers is a tie or 2^-13 from one (their products hold 16 bits), which fp32 keeps
+    want = (x.to(D) * 448 / top.to(D).repeat_interleave(B, 1)[:, :513]).float().to(F8).float()
+    want[x == 0] = 0  # the last column's blocks hold one value, which may be 0
+    assert torch.equal(q.float(), want)
+
+
+# ----------------------------------------------------------------------------- the product
+
+PRODUCT = [
+    # T, N, K, out, bias, y, res, pad, wide codes
+    (1, 1, 16, "f32", False, False, False, 0, True), (1, 16, 128, "bf16", True, False, True, 0, True),
+    (2, 17, 144, "f32", True, True, True, 16, True), (5, 130, 2064, "bf16", False, True, False, 32, False),
+    (16, 300, 1024, "f32", False, False, True, 0, True), (1, 7168, 7168, "bf16", False, False, True, 0, False),
+    (15, 33, 16, "bf16", False, False, False, 16, True), (16, 1000, 4112, "bf16", True, True, True, 0, False),
+    (17, 130, 2064, "f32", True, True, True, 16, True), (17, 16, 16, "bf16", False, False, False, 0, True),
+    (33, 65, 272, "bf16", True, False, True, 48, True), (64, 4096, 1024, "bf16", False, True, True, 0, False),
+    (128, 257, 400, "f32", False, False, False, 16, False), (129, 384, 1040, "bf16", True, True, False, 0, True),
+    (333, 1001, 2064, "f32", True, False, False, 0, False), (300, 520, 3200, "bf16", False, False, True, 16, False),
+    (520, 1000, 512, "bf16", True, True, True, 0, True), (1025, 2049, 656, "f32", False, True, False, 0, False),
+    (2048, 4096, 512, "bf16", False, False, False, 0, False), (2100, 3800, 144, "f32", True, False, True, 0, False),
+]
+
+
+def _product_tolerance(x, w, sx, sw, K, exact):
+    """How far the sum over K may be off: each block's products are added in at most 128 + 1 steps
+    that may cut (2^-23 of the sum of their sizes each), scaled by a product of two scales (two
+    roundings), and the blocks and the parts of K added in at most KB + 16."""
+    KB = _up(K)
+    sizes = x.abs() @ w.abs().T
+    return sizes * ((B + 1) * 2 + 2 + KB + 16) * R32
+
+
+@pytest.mark.parametrize("T,N,K,out,bias,y,res,pad,wide", PRODUCT)
+def test_product(moe, T, N, K, out, bias, y, res, pad, wide):
+    _say("product:", T, N, K, out, bias, y, res, pad, wide)
+    g, dt, KB = _gen(T * 7 + N * 11 + K), ACT[out], _up(K)
+    make = _codes if wide else _normal
+    qx, qw = Padded(T, K, K + pad, F8, make(g, T, K)), Padded(N, K, K + pad, F8, make(g, N, K))
+    sx = Padded(T, KB, KB + pad // 16, torch.float32, torch.exp(_rn(g, T, KB)) / 100)
+    sw = Padded(_up(N), KB, KB + pad // 8, torch.float32, torch.exp(_rn(g, _up(N), KB)) / 100)
+    b = _rn(g, N) * 10 if bias else None
+    ym = Padded(T, N, N + pad, torch.float32, _rn(g, T, N) * 10) if y else None
+    rm = Padded(T, N, N + pad // 2, dt, (_rn(g, T, N) * 10).to(dt)) if res else None
+    o = Padded(T, N, N + 2 * pad, dt)
+    moe.fp8_matmul(qx.m, sx.m, qw.m, sw.m, o.m, bias=b, y_in=ym.m if y else None, res=rm.m if res else None)
+    x, w = _full(qx.m, sx.m), _full(qw.m, sw.m, B)
+    want, tol = x @ w.T, _product_tolerance(x, w, sx, sw, K, out == "f32")
+    for more in (b, ym.m if y else None, rm.m if res else None):
+        if more is not None:
+            want = want + more.to(D)
+            tol = tol + (want.abs() + more.to(D).abs()) * R32
+    tol = tol * (1 + RBF) + want.abs() * (R32 if out == "f32" else RBF)
+    err = (o.m.to(D) - want).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
+    assert all(m is None or m.untouched() for m in (qx, qw, sx, sw, ym, rm, o))
+
+
+@pytest.mark.parametrize("T", [1, 16, 40])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_product_in_place_and_not_finite(moe, T, out):
+    """out may be res or y_in; a NaN of a token's stays with the token, of a channel's with the channel."""
+    g, dt, N, K = _gen(T), ACT[out], 200, 272
+    qx, qw, sx, sw = _normal(g, T, K), _normal(g, N, K), torch.exp(_rn(g, T, 3)), torch.exp(_rn(g, 2, 3))
+    want = torch.empty(T, N, device="cuda", dtype=dt)
+    res, y = _rn(g, T, N).to(dt), _rn(g, T, N)
+    moe.fp8_matmul(qx, sx, qw, sw, want, y_in=y, res=res)
+    got = res.clone()
+    moe.fp8_matmul(qx, sx, qw, sw, got, y_in=y, res=got)
+    assert torch.equal(got, want)
+    if out == "f32":
+        got = y.clone()
+        moe.fp8_matmul(qx, sx, qw, sw, got, y_in=got, res=res)
+        assert torch.equal(got, want)
+    qw[7].view(torch.uint8)[200] = 0x7F
+    sx[T - 1, 1] = float("nan")
+    moe.fp8_matmul(qx, sx, qw, sw, got, y_in=y, res=res)
+    bad = torch.zeros(T, N, dtype=torch.bool, device="cuda")
+    bad[:, 7] = bad[T - 1] = True
+    assert torch.equal(torch.isnan(got), bad) and torch.equal(got[~bad], want[~bad])
+
+
+# ----------------------------------------------------------------------------- the layer
+
+
+def _layer_inputs(T, H, I, E, k, act, seed, wide=False, pad=0):  # noqa: E741
+    g, dt = _gen(seed), ACT[act]
+    make = _codes if wide else _normal
+    s = dict(q_gu=make(g, E, 2 * I, H), q_dn=make(g, E, H, I))
+    s["s_gu"] = torch.exp(0.5 * _rn(g, E, 2, _up(I), _up(H))) / (100 * H ** 0.5)
+    s["s_dn"] = torch.exp(0.5 * _rn(g, E, _up(H), _up(I))) / (100 * I ** 0.5)
+    s["x"] = Padded(T, H, H + pad, dt, (_rn(g, T, H) * torch.exp(0.3 * _rn(g, H))).to(dt)).m
+    s["router_w"] = Padded(E, H, H + 2 * pad, dt, (_rn(g, E, H) / H ** 0.5).to(dt)).m
+    s["router_b"] = _rn(g, E)
+    s["k"] = k
+    return s
+
+
+def _outputs(T, H, E, k, dt, pad=0):
+    o = dict(y=Padded(T, H, H + pad, torch.float32), x_out=Padded(T, H, H + 3 * pad, dt))
+    flat = dict(logits=torch.full((T, E), 7.0, device="cuda"), topk_ids=torch.full((T, k), -7, device="cuda", dtype=torch.int32),
+                topk_w=torch.full((T, k), 7.0, device="cuda"))
+    return o, flat
+
+
+def _workspace(moe, T, H, I, E, k):  # noqa: E741
+    return torch.full((moe.fp8_layer_workspace(T, H, I, E, k),), 0xFF, device="cuda", dtype=torch.uint8)
+
+
+def _check_layer(s, logits, y, x_out, ids, gate):
+    """Every output against its definition, from the logits that the operator ranked."""
+    x, k = s["x"].to(D), s["k"]
+    (T, H), E, I = x.shape, s["q_dn"].shape[0], s["q_dn"].shape[2]  # noqa: E741
+    key = torch.where(torch.isnan(logits), torch.full_like(logits, float("inf")), logits).to(D)
+    best, order = torch.sort(key, dim=1, descending=True, stable=True)
+    assert torch.equal(ids.long(), order[:, :k])
+    chosen = logits.to(D).gather(1, order[:, :k])
+    want_gate = torch.softmax(chosen, 1)
+    want_gate = torch.where((chosen == float("-inf")).all(1, keepdim=True), torch.zeros_like(want_gate), want_gate)
+    assert torch.equal(torch.isnan(gate), torch.isnan(want_gate))
+    # the exponent's argument is rounded once (2^-24 of a size under 104), exp, the sum of k and the quotient after it; what
+    # is under fp32's normal range may be lost
+    spread = (chosen - chosen[:, :1]).abs().clamp(max=104).nan_to_num(posinf=0)
+    tol = want_gate * (spread + k + 8) * R32 + 2.0 ** -126
+    assert bool(((gate.to(D) - want_gate).abs() <= tol).nan_to_num().logical_or(torch.isnan(want_gate)).all())
+    want, off = torch.zeros(T, H, dtype=D, device="cuda"), torch.zeros(T, H, dtype=D, device="cuda")
+    HB, IB = _up(H), _up(I)
+    for e in sorted(set(ids.flatten().tolist())):
+        t, j = (ids == e).nonzero(as_tuple=True)
+        some = gate[t, j] != 0
+        t, j = t[some], j[some]
+        if len(t) == 0:
+            continue
+        wg, wu = _full(s["q_gu"][e, :I], s["s_gu"][e, 0], B), _full(s["q_gu"][e, I:], s["s_gu"][e, 1], B)
+        wd, xe = _full(s["q_dn"][e], s["s_dn"][e], B), x[t]
+        gt, u = xe @ wg.T, xe @ wu.T
+        n = ((B * 3 + 1) * 2 + 1 + HB + 8) * R32  # up to three terms of each product, as _product_tolerance
+        og, ou = (xe.abs() @ wg.abs().T) * n, (xe.abs() @ wu.abs().T) * n
+        sig = torch.sigmoid(gt)
+        h = gt * sig * u
+        # |d silu| <= 1.1; exp (2 roundings, and its argument's, which 1 + exp divides by), 1 +, the quotient, the product
+        oh = 1.1 * og * (u.abs() + ou) + (gt * sig).abs() * ou + h.abs() * 8 * R32
+        w = gate[t, j, None].to(D)
+        m = ((B * 3 + 1) * 2 + 2 + k * IB + 8) * R32  # the blocks of k experts are added in one sum
+        off[t] += w * (oh @ wd.abs().T + ((h.abs() + oh) @ wd.abs().T) * m)
+        want[t] += w * (h @ wd.T)
+    bad = torch.isnan(want)
+    assert torch.equal(torch.isnan(y), bad)
+    err = (y.to(D) - want).abs()
+    assert bool((err <= off).logical_or(bad).all()), float((err / off).nan_to_num().max())
+    s_exact = x + y.to(D)
+    r = R32 if s["x"].dtype == torch.float32 else RBF
+    assert bool(((x_out.to(D) - s_exact).abs() <= s_exact.abs() * (r + 2 * R32)).logical_or(bad).all())
+
+
+LAYER = [
+    # T, H, I, E, k, act, pad, wide
+    (1, 16, 16, 1, 1, "bf16", 0, True), (1, 16, 16, 1, 1, "f32", 1, True), (3, 144, 48, 5, 5, "bf16", 3, True),
+    (7, 400, 208, 24, 3, "f32", 0, False), (2, 128, 128, 8, 2, "bf16", 0, True), (16, 256, 128, 8, 2, "f32", 1, True),
+    (17, 272, 144, 9, 4, "bf16", 1, False), (33, 1040, 400, 4, 2, "bf16", 0, False), (64, 256, 144, 40, 32, "bf16", 7, True),
+    (64, 144, 272, 3, 1, "f32", 0, True), (48, 2064, 160, 70, 8, "bf16", 0, False), (1, 2048, 768, 128, 8, "bf16", 0, False),
+    (16, 2048, 768, 128, 8, "bf16", 0, False), (5, 7168, 400, 24, 6, "bf16", 0, False), (9, 1024, 2064, 130, 7, "f32", 0, False),
+    (4, 64, 32, 1024, 32, "bf16", 0, True), (64, 32, 16, 1000, 32, "f32", 0, True), (31, 16, 272, 6, 3, "bf16", 0, True),
+    (6, 3216, 2048, 16, 4, "bf16", 0, True), (11, 32, 16384, 4, 2, "bf16", 0, False), (3, 16400, 32, 6, 2, "bf16", 0, False),
+]
+
+
+@pytest.mark.parametrize("T,H,I,E,k,act,pad,wide", LAYER)
+def test_layer(moe, T, H, I, E, k, act, pad, wide):  # noqa: E741
+    _say("layer:", T, H, I, E, k, act, pad, wide)
+    s = _layer_inputs(T, H, I, E, k, act, T * 31 + H + I, wide, pad)
+    o, flat = _outputs(T, H, E, k, ACT[act], pad)
+    moe.fp8_layer(**s, y=o["y"].m, x_out=o["x_out"].m, workspace=_workspace(moe, T, H, I, E, k), **flat)
+    # the sums in fp64 have room for any order; then one rounding
+    want = s["x"].to(D) @ s["router_w"].to(D).T + s["router_b"].to(D)
+    sizes = s["x"].to(D).abs() @ s["router_w"].to(D).abs().T + s["router_b"].to(D).abs()
+    assert bool(((flat["logits"].to(D) - want).abs() <= want.abs() * R32 + sizes * H * 2.0 ** -53).all())
+    _check_layer(s, flat["logits"], o["y"].m, o["x_out"].m, flat["topk_ids"], flat["topk_w"])
+    assert o["y"].untouched() and o["x_out"].untouched()
+    # the other outputs left out, and x's place taken by x_out: the same bits
+    y2, x2 = torch.empty(T, H, device="cuda"), s["x"].clone()
+    moe.fp8_layer(**{**s, "x": x2}, y=y2, x_out=x2, workspace=_workspace(moe, T, H, I, E, k))
+    assert torch.equal(y2, o["y"].m) and torch.equal(x2, o["x_out"].m)
+    y3 = torch.empty(T, H, device="cuda")
+    moe.fp8_layer(**s, y=y3, workspace=_workspace(moe, T, H, I, E, k), logits_in=flat["logits"])
+    assert torch.equal(y3, y2)
+
+
+def test_layer_logits(moe):
+    """Ties, experts that a mask keeps out, tokens that it leaves nothing, NaN and infinities."""
+    T, H, I, E, k = 12, 256, 144, 70, 4  # noqa: E741
+    s = _layer_inputs(T, H, I, E, k, "bf16", 5)
+    inf, nan = float("inf"), float("nan")
+    li = torch.randint(-3, 3, (T, E), device="cuda", generator=_gen(6)).float()  # ties in every row
+    li[1] = 0.0
+    li[1, 1::2] = -0.0
+    li[2] = -inf
+    li[3] = -inf
+    li[3, [64, 9]] = torch.tensor([1.0, 2.0], device="cuda")  # two are left
+    li[4, 30] = nan
+    li[5] = nan
+    li[6, 69] = inf
+    li[7] = torch.finfo(torch.float32).min
+    li[8] = torch.finfo(torch.float32).min
+    li[8, 65] = 3e38
+    li[9] = -inf
+    li[9, 11] = torch.finfo(torch.float32).min
+    li[10, :] = -200.0
+    li[10, 5] = 0.0  # the others' weights underflow
+    o, flat = _outputs(T, H, E, k, torch.bfloat16)
+    moe.fp8_layer(**s, y=o["y"].m, x_out=o["x_out"].m, workspace=_workspace(moe, T, H, I, E, k), logits_in=li, **flat)
+    assert torch.equal(flat["logits"].view(torch.int32), li.view(torch.int32))
+    ids, gate, y = flat["topk_ids"], flat["topk_w"], o["y"].m
+    assert ids[1].tolist() == [0, 1, 2, 3] and ids[2].tolist() == [0, 1, 2, 3] and ids[3].tolist() == [9, 64, 0, 1]
+    assert ids[4, 0] == 30 and ids[5].tolist() == [0, 1, 2, 3] and ids[6, 0] == 69
+    assert ids[7].tolist() == [0, 1, 2, 3] and gate[7].tolist() == [0.25] * 4 and gate[9].tolist() == [1.0, 0, 0, 0]
+    assert bool((gate[2] == 0).all()) and bool((y[2] == 0).all()) and torch.equal(o["x_out"].m[2], s["x"][2])
+    assert gate[3, 2:].tolist() == [0, 0] and gate[10].tolist() == [1.0, 0, 0, 0] and gate[8].tolist() == [1.0, 0, 0, 0]
+    assert all(bool(torch.isnan(y[t]).all()) for t in (4, 5, 6))
+    keep = [t for t in range(T) if t not in (4, 5, 6)]
+    sub = {**s, "x": s["x"][keep].contiguous()}
+    _check_layer(sub, li[keep], y[keep], o["x_out"].m[keep], ids[keep], gate[keep])
+
+
+def test_layer_keeps_tokens_apart(moe):
+    """A token's outputs have the same bits alone, in a batch, and beside tokens that are not
+    finite or whose experts hold NaN."""
+    T, H, I, E, k = 64, 528, 272, 20, 3  # noqa: E741
+    s = _layer_inputs(T, H, I, E, k, "bf16", 11)
+    run = lambda v: moe.fp8_layer(**v, y=torch.empty(v["x"].shape[0], H, device="cuda"),  # noqa: E731
+                                  workspace=_workspace(moe, v["x"].shape[0], H, I, E, k))
+    all_y = run(s)
+    for some in ([0], [63], [5, 40], list(range(16)), list(range(3, 40))):
+        assert torch.equal(run({**s, "x": s["x"][some].contiguous()}), all_y[some])
+    ids = torch.empty(T, k, device="cuda", dtype=torch.int32)
+    moe.fp8_layer(**s, y=torch.empty(T, H, device="cuda"), workspace=_workspace(moe, T, H, I, E, k), topk_ids=ids)
+    x = s["x"].clone()
+    x[10, 3], x[20, 500] = float("nan"), float("inf")
+    q = s["q_dn"].clone()
+    poisoned = int(ids[30, 1])
+    q[poisoned].view(torch.uint8)[:] = 0x7F
+    y = run({**s, "x": x, "q_dn": q})
+    hit = (ids == poisoned).any(1)
+    hit[[10, 20]] = True
+    assert bool(torch.isnan(y[hit]).all()) and torch.equal(y[~hit], all_y[~hit])
+
+
+def test_layer_beyond_32_bits(moe):
+    """Experts whose offsets pass 2^32, the last one among the chosen."""
+    T, H, I, E, k = 3, 7168, 2048, 160, 4  # noqa: E741
+    g = _gen(2)
+    s = _layer_inputs(T, H, 16, 1, 1, "bf16", 3)
+    s["q_gu"], s["q_dn"] = torch.empty(E, 2 * I, H, device="cuda", dtype=F8), torch.empty(E, H, I, device="cuda", dtype=F8)
+    for e in range(E):
+        s["q_gu"][e], s["q_dn"][e] = _normal(g, 2 * I, H), _normal(g, H, I)
+    assert s["q_gu"].numel() > 1 << 32
+    s["s_gu"] = torch.exp(0.5 * _rn(g, E, 2, _up(I), _up(H))) / (100 * H ** 0.5)
+    s["s_dn"] = torch.exp(0.5 * _rn(g, E, _up(H), _up(I))) / (100 * I ** 0.5)
+    s["router_w"], s["router_b"], s["k"] = None, None, k
+    li = _rn(g, T, E)
+    li[:, E - 1] = 9
+    li[1, E - 2] = 10
+    o, flat = _outputs(T, H, E, k, torch.bfloat16)
+    moe.fp8_layer(**s, y=o["y"].m, x_out=o["x_out"].m, workspace=_workspace(moe, T, H, I, E, k), logits_in=li, **flat)
+    _check_layer(s, li, o["y"].m, o["x_out"].m, flat["topk_ids"], flat["topk_w"])
+
+
+# ----------------------------------------------------------------------------- streams, graphs, a run of them
+
+
+def test_other_stream(moe):
+    T, H, I, E, k = 5, 512, 256, 16, 2  # noqa: E741
+    s = _layer_inputs(T, H, I, E, k, "bf16", 1)
+    want = moe.fp8_layer(**s, y=torch.empty(T, H, device="cuda"), workspace=_workspace(moe, T, H, I, E, k)).clone()
+    side, ws, y = torch.cuda.Stream(), _workspace(moe, T, H, I, E, k), torch.empty(T, H, device="cuda")
+    torch.cuda.synchronize()
+    moe.fp8_layer(**s, y=y, workspace=ws, stream=side)
+    side.synchronize()
+    assert torch.equal(y, want)
+    with torch.cuda.stream(side):  # the current stream is the default one
+        y.zero_()
+        moe.fp8_layer(**s, y=y, workspace=ws)
+    side.synchronize()
+    assert torch.equal(y, want)
+
+
+def test_graphs_that_share_a_workspace(moe):
+    """Two captured calls on one workspace, replayed in turn with eager work between."""
+    shapes = [(1, 512, 256, 16, 2), (20, 384, 144, 30, 5)]
+    size = max(moe.fp8_layer_workspace(*n) for n in shapes)
+    ws, graphs = torch.full((size,), 0xFF, device="cuda", dtype=torch.uint8), []
+    for n in shapes:
+        T, H, I, E, k = n  # noqa: E741
+        s = _layer_inputs(T, H, I, E, k, "bf16", T)
+        q, sc, pr = torch.empty(T, H, device="cuda", dtype=F8), torch.empty(T, _up(H), device="cuda"), torch.empty(T, H, device="cuda")
+        y, w, sw = torch.empty(T, H, device="cuda"), _normal(_gen(9), H, H), torch.full((_up(H), _up(H)), 0.01, device="cuda")
+
+        def call(y=y, q=q, sc=sc, pr=pr, s=s, w=w, sw=sw):
+            moe.fp8_quantize(s["x"], q, sc)
+            moe.fp8_matmul(q, sc, w, sw, pr)
+            moe.fp8_layer(**s, y=y, workspace=ws)
+
+        call()
+        torch.cuda.synchronize()
+        want = [t.clone() for t in (y, q.view(torch.uint8), pr)]
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        graphs.append((g, call, (y, q.view(torch.uint8), pr), want))
+    for turn in range(6):
+        g, call, got, want = graphs[turn % 2]
+        for t in got:
+            t.zero_()
+        if turn == 3:
+            ws.fill_(0x5A)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), turn
+        if turn % 3 == 0:
+            call()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want)), turn
+
+
+def test_refusals_by_shape(moe):
+    z = lambda *n, dt=torch.float32: torch.zeros(*n, dtype=dt, device="cuda")  # noqa: E731
+    T, H, N, I, E, k = 4, 144, 136, 32, 3, 2  # noqa: E741
+    bf = torch.bfloat16
+    calls = {
+        moe.fp8_quantize: dict(x=z(T, H, dt=bf), q_out=z(T, H, dt=F8), s_out=z(T, 2)),
+        moe.fp8_matmul: dict(q_x=z(T, H, dt=F8), s_x=z(T, 2), q_w=z(N, H, dt=F8), s_w=z(2, 2), out=z(T, N, dt=bf), bias=z(N),
+                             y_in=z(T, N), res=z(T, N, dt=bf)),
+        moe.fp8_layer: dict(x=z(T, H, dt=bf), router_w=z(E, H, dt=bf), q_gu=z(E, 2 * I, H, dt=F8), s_gu=z(E, 2, 1, 2),
+                            q_dn=z(E, H, I, dt=F8), s_dn=z(E, 2, 1), k=k, y=z(T, H),
+                            workspace=z(moe.fp8_layer_workspace(T, H, I, E, k), dt=torch.uint8), router_b=z(E), logits_in=z(T, E),
+                            x_out=z(T, H, dt=bf), logits=z(T, E), topk_ids=z(T, k, dt=torch.int32), topk_w=z(T, k)),
+    }
+    for fn, sound in calls.items():
+        fn(**sound)
+        torch.cuda.synchronize()
+        for name, m in sound.items():
+            if name in ("x", "q_x", "q_dn", "k", "workspace"):
+                continue
+            with pytest.raises(moe.MoeError, match=name + " has shape"):
+                fn(**{**sound, name: z(*m.shape[:-1], m.shape[-1] + 16, dt=m.dtype)})
+            with pytest.raises(moe.MoeError, match=name + ": "):
+                fn(**{**sound, name: z(*m.shape[:-1], 2 * m.shape[-1], dt=m.dtype)[..., ::2]})
+        for name in [n for n in sound if n in ("workspace",)]:
+            with pytest.raises(moe.MoeError, match="workspace holds"):
+                fn(**{**sound, name: sound[name][:-256]})
+    with pytest.raises(moe.MoeError, match="16"):
+        moe.fp8_matmul(**{**calls[moe.fp8_matmul], "q_x": z(T, H + 8, dt=F8)[:, 8:]})
+
+
+def test_a_run_of_them(moe):
+    """A decode step's path: norm, codes, projection onto the residual stream, norm, the routed layer with
+    the stream's next value. Each step is held to its definition on what the step before it left."""
+    T, H, I, E, k = 6, 1024, 400, 24, 4  # noqa: E741
+    g, bf = _gen(17), torch.bfloat16
+    s = _layer_inputs(T, H, I, E, k, "bf16", 18)
+    w = (_rn(g, H, H) / H ** 0.5).to(bf)
+    qw, sw = torch.empty(H, H, device="cuda", dtype=F8), torch.empty(_up(H), _up(H), device="cuda")
+    moe.fp8_quantize(w, qw, sw, block_rows=128)
+    x, gain = _rn(g, T, H).to(bf), (1 + 0.2 * _rn(g, H)).to(bf)
+    n, q, sc, x1, n1 = torch.empty_like(x), torch.empty(T, H, device="cuda", dtype=F8), torch.empty(T, _up(H), device="cuda"), \
+        torch.empty_like(x), torch.empty_like(x)
+    moe.rms_norm(x, gain, 1e-6, out=n)
+    moe.fp8_quantize(n, q, sc)
+    moe.fp8_matmul(q, sc, qw, sw, x1, res=x)
+    moe.rms_norm(x1, gain, 1e-6, out=n1)
+    o, flat = _outputs(T, H, E, k, bf)
+    layer = {**s, "x": n1}
+    moe.fp8_layer(**layer, y=o["y"].m, x_out=o["x_out"].m, workspace=_workspace(moe, T, H, I, E, k), **flat)
+    x2 = torch.empty_like(x)
+    n2 = torch.empty_like(x)
+    moe.rms_norm(x1, gain, 1e-6, add=o["y"].m, x_out=x2, out=n2)  # the layer's fp32 y onto the stream
+    wq, ws = _want_codes(n.to(D), 1)
+    assert torch.equal(q.to(D), wq) and bool(((sc.to(D) - ws).abs() <= ws * R32).all())
+    # codes hold a value to 2^-4 of itself, or half a step of 2^-9 of the block's scale
+    full = _full(qw, sw, B)
+    assert bool(((full - w.to(D)).abs() <= w.to(D).abs() * 2.0 ** -4 * (1 + R32) + sw.to(D).repeat_interleave(B, 0).repeat_interleave(B, 1) * 2.0 ** -10).all())
+    xs = _full(q, sc)
+    want = xs @ full.T + x.to(D)
+    tol = _product_tolerance(xs, full, sc, sw, H, False) * 1.01 + want.abs() * (RBF + 4 * R32) + x.to(D).abs() * R32
+    assert bool(((x1.to(D) - want).abs() <= tol).all())
+    _check_layer(layer, flat["logits"], o["y"].m, o["x_out"].m, flat["topk_ids"], flat["topk_w"])
+    assert bool(((x2.to(D) - (x1.to(D) + o["y"].m.to(D))).abs() <= (x1.to(D) + o["y"].m.to(D)).abs() * (RBF + 2 * R32)).all())
+
+
+def test_one_shared_expert(moe):
+    """A layer of one expert is the gated block of an expert that every token shares."""
+    T, H, I = 20, 512, 272  # noqa: E741
+    s = _layer_inputs(T, H, I, 1, 1, "bf16", 23)
+    y = moe.fp8_layer(**s, y=torch.empty(T, H, device="cuda"), workspace=_workspace(moe, T, H, I, 1, 1))
+    x = s["x"].to(D)
+    gt, u = x @ _full(s["q_gu"][0, :I], s["s_gu"][0, 0], B).T, x @ _full(s["q_gu"][0, I:], s["s_gu"][0, 1], B).T
+    want = (gt * torch.sigmoid(gt) * u) @ _full(s["q_dn"][0], s["s_dn"][0], B).T
+    assert float((y.to(D) - want).norm() / want.norm()) < 1e-6
