@@ -44,6 +44,18 @@ void launch_fp8_gemm(const Fp8Args& a, bool out_bf16, hipStream_t s);
 
 constexpr int kF8LayerTokens = 64, kF8LayerExperts = 1024, kF8LayerTopK = 32;
 
+// An expert with tokens: its first place among the assignments, grouped by expert in
+// ascending order of experts and tokens, and how many they are.
+struct Fp8Expert {
+  uint16_t expert, at, count, none;
+};
+struct Fp8Tables {
+  Fp8Expert expert[kF8LayerExperts];
+  float gate[kF8LayerTokens * kF8LayerTopK];    // by place
+  uint8_t token[kF8LayerTokens * kF8LayerTopK];
+  int experts;
+};
+
 struct Fp8LayerArgs {
   const void* x;          // [T][H] act
   const void* router_w;   // [E][H] act
@@ -59,7 +71,8 @@ struct Fp8LayerArgs {
   int32_t* ids;           // [T][k] or null
   float* gate;            // [T][k] or null
   uint16_t* h;            // workspace: the intermediate's three bf16 terms, [3][T k][I]
-  unsigned* counters;     // workspace
+  uint16_t* xt;           // workspace: fp32 activations' three bf16 terms, [3][T][H]
+  Fp8Tables* tables;      // workspace
   int64_t ld_x, ld_router, ld_y, ld_x_out;
   int T, H, I, E, k;
 };

@@ -30,12 +30,14 @@ moe_status check_layer_shape(int T, int H, int I, int E, int k) {
   return MOE_OK;
 }
 
-// the layer's workspace: counters | logits [T][E] | the intermediate, three bf16 terms [3][T k][I]
+// the layer's workspace: tables | logits [T][E] | three bf16 terms of fp32 activations [3][T][H] |
+// of the intermediate [3][T k][I]
 struct LayerSpace {
-  size_t counters = 0, logits, h, bytes;
-  LayerSpace(int64_t T, int64_t I, int64_t E, int64_t k) {
-    logits = 256;
-    h = logits + up256(sizeof(float) * T * E);
+  size_t tables = 0, logits, x, h, bytes;
+  LayerSpace(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k) {
+    logits = up256(sizeof(Fp8Tables));
+    x = logits + up256(sizeof(float) * T * E);
+    h = x + up256(3 * sizeof(uint16_t) * T * H);
     bytes = h + up256(3 * sizeof(uint16_t) * T * k * I);
   }
 };
@@ -99,7 +101,7 @@ moe_status moe_fp8_layer_workspace(int32_t T, int32_t H, int32_t I, int32_t E, i
   if (!bytes) return bad("bytes is null");
   *bytes = 0;
   CHECK(check_layer_shape(T, H, I, E, k));
-  *bytes = LayerSpace(T, I, E, k).bytes;
+  *bytes = LayerSpace(T, H, I, E, k).bytes;
   return MOE_OK;
 }
 
@@ -110,7 +112,7 @@ moe_status moe_fp8_layer(const moe_fp8_layer_args* a, moe_stream stream) {
   if (a->T == 0) return MOE_OK;
   const int T = a->T, H = a->H, I = a->I, E = a->E, k = a->k, sz = act_size(a->act_dtype);
   const int HB = f8_blocks(H), IB = f8_blocks(I);
-  const LayerSpace f(T, I, E, k);
+  const LayerSpace f(T, H, I, E, k);
   const auto flat = [](const char* name, const void* p, int64_t n, int size) { return Mat{name, p, 1, n, n, size}; };
   Mat x{"x", a->x, T, H, a->ld_x, sz}, rw{"router_w", a->logits_in ? nullptr : a->router_w, E, H, a->ld_router, sz};
   Mat rb = flat("router_b", a->logits_in ? nullptr : a->router_b, E, 4), li = flat("logits_in", a->logits_in, (int64_t)T * E, 4);
@@ -157,7 +159,8 @@ moe_status moe_fp8_layer(const moe_fp8_layer_args* a, moe_stream stream) {
   g.ids = a->topk_ids;
   g.gate = a->topk_w;
   g.h = reinterpret_cast<uint16_t*>(base + f.h);
-  g.counters = reinterpret_cast<unsigned*>(base + f.counters);
+  g.xt = reinterpret_cast<uint16_t*>(base + f.x);
+  g.tables = reinterpret_cast<Fp8Tables*>(base + f.tables);
   g.ld_x = x.ld;
   g.ld_router = rw.ld;
   g.ld_y = y.ld;

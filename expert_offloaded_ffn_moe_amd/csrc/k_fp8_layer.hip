@@ -24,7 +24,6 @@ namespace moe {
 namespace {
 
 constexpr int kMaxAssign = kF8LayerTokens * kF8LayerTopK;
-constexpr int kTileTokens = 16;  // columns of the MFMA
 
 // ----------------------------------------------------------------------------- router
 
@@ -65,38 +64,72 @@ __device__ __forceinline__ double wave_sum_63(double v) {
   return v;
 }
 
-// An expert's row a workgroup; its waves take eight neighbours a lane in turn. Also clears
-// the counters of the launch that follows.
-constexpr int kRouterWaves = 4;
+// f as three bf16 terms: 8 bits each, the last one exact; an infinity or a NaN stays whole in the first.
+__device__ __forceinline__ void three_terms(float f, uint16_t* t) {
+  typedef OutElem<true> Bf;
+  t[0] = Bf::rounded(f);
+  const bool finite = fabsf(f) < INFINITY;
+  const float r = f - Bf::load(t[0]);
+  t[1] = finite ? Bf::rounded(r) : 0;
+  t[2] = finite ? Bf::rounded(r - Bf::load(t[1])) : 0;
+}
+
+// Workgroups 0 .. E - 1 take a row of the router each, H split over its threads, the others
+// (fp32 activations) a token each, whose terms they write. With logits_in there are T
+// workgroups, which copy a token's logits where they are wanted. Tokens are taken four at a
+// time, their loads ahead of the sums.
+constexpr int kRouterThreads = 256, kRouterTokens = 4;
 template <typename ACT>
-__global__ __launch_bounds__(64 * kRouterWaves) void k_f8_router(Fp8LayerArgs a) {
-  __shared__ double part[kRouterWaves][kF8LayerTokens];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, e = blockIdx.x;
-  if (e == 0 && threadIdx.x < 64) a.counters[threadIdx.x] = 0u;
-  if (a.logits_in) {  // one workgroup for each token then
-    if (a.logits)
-      for (int i = threadIdx.x; i < a.E; i += 64 * kRouterWaves) a.logits[(int64_t)e * a.E + i] = a.logits_in[(int64_t)e * a.E + i];
+__global__ __launch_bounds__(kRouterThreads) void k_f8_router(Fp8LayerArgs a, int rows) {
+  __shared__ double part[kRouterThreads / 64][kF8LayerTokens];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if ((int)blockIdx.x >= rows) {
+    const int t = blockIdx.x - rows;
+    if (a.logits_in && a.logits)
+      for (int i = threadIdx.x; i < a.E; i += kRouterThreads) a.logits[(int64_t)t * a.E + i] = a.logits_in[(int64_t)t * a.E + i];
+    if (sizeof(ACT) == 4) {
+      const float* x = static_cast<const float*>(a.x) + t * a.ld_x;
+      for (int i = threadIdx.x; i < a.H; i += kRouterThreads) {
+        uint16_t v[3];
+        three_terms(x[i], v);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) a.xt[((int64_t)k * a.T + t) * a.H + i] = v[k];
+      }
+    }
     return;
   }
+  const int e = blockIdx.x;
   const ACT* w = static_cast<const ACT*>(a.router_w) + e * a.ld_router;
-  for (int t = 0; t < a.T; ++t) {
-    const ACT* x = static_cast<const ACT*>(a.x) + t * a.ld_x;
-    double sum = 0.0;
-    for (int j = 8 * threadIdx.x; j < a.H; j += 8 * 64 * kRouterWaves) {  // H is a multiple of 16
-      float wv[8], xv[8];
-      values8(w + j, wv);
-      values8(x + j, xv);
+  for (int t0 = 0; t0 < a.T; t0 += kRouterTokens) {
+    const ACT* x[kRouterTokens];
+    double sum[kRouterTokens];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fma((double)wv[i], (double)xv[i], sum);
+    for (int t = 0; t < kRouterTokens; ++t) {
+      x[t] = static_cast<const ACT*>(a.x) + min(t0 + t, a.T - 1) * a.ld_x;
+      sum[t] = 0.0;
     }
-    sum = wave_sum_63(sum);
-    if (lane == 63) part[wave][t] = sum;
+    for (int j = 8 * threadIdx.x; j < a.H; j += 8 * kRouterThreads) {  // H is a multiple of 16
+      float wv[8], xv[kRouterTokens][8];
+      values8(w + j, wv);
+#pragma unroll
+      for (int t = 0; t < kRouterTokens; ++t) values8(x[t] + j, xv[t]);
+#pragma unroll
+      for (int t = 0; t < kRouterTokens; ++t)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[t] = fma((double)wv[i], (double)xv[t][i], sum[t]);
+    }
+#pragma unroll
+    for (int t = 0; t < kRouterTokens; ++t) {
+      if (t0 + t >= a.T) break;
+      sum[t] = wave_sum_63(sum[t]);
+      if (lane == 63) part[wave][t0 + t] = sum[t];
+    }
   }
   __syncthreads();
-  for (int t = threadIdx.x; t < a.T; t += 64 * kRouterWaves) {
+  for (int t = threadIdx.x; t < a.T; t += kRouterThreads) {
     double v = a.router_b ? (double)a.router_b[e] : 0.0;
 #pragma unroll
-    for (int k = 0; k < kRouterWaves; ++k) v += part[k][t];
+    for (int k = 0; k < kRouterThreads / 64; ++k) v += part[k][t];
     a.logits[(int64_t)t * a.E + e] = (float)v;
   }
 }
@@ -110,8 +143,8 @@ struct Route {
   float gate[kMaxAssign];             // weights, in grouped order
   uint16_t at[kF8LayerExperts];       // the expert's first place in that order
   uint16_t expert[kF8LayerExperts];   // experts with tokens
-  uint16_t tile_expert[kMaxAssign];   // tiles of up to 16 tokens of one expert
-  uint8_t tile_first[kMaxAssign];     // the tile's first among its expert's tokens
+  uint16_t tile_expert[kMaxAssign];   // tiles: the expert, and the first of up to `tile` of its tokens
+  uint8_t tile_first[kMaxAssign];
   uint8_t token[kMaxAssign];          // token of a place
   int experts, tiles;
 };
@@ -162,6 +195,8 @@ __device__ __forceinline__ void choose(const float* logits, int E, int k, int& i
   w = sum == 0.f ? 0.f : p / sum;  // every logit -infinity: nothing
 }
 
+// `writes`: one workgroup of the launch, which also leaves the tables for the next launch.
+template <int TILE>
 __device__ __forceinline__ void route(const Fp8LayerArgs& a, Route& r, bool writes) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   const float* logits = a.logits ? a.logits : a.logits_in;
@@ -208,14 +243,14 @@ __device__ __forceinline__ void route(const Fp8LayerArgs& a, Route& r, bool writ
     for (int e0 = 0; e0 < a.E; e0 += 64) {
       const int e = e0 + lane, c = e < a.E ? __popcll(r.mask[e]) : 0;
       const uint64_t some = __ballot(c > 0);
-      const int tc = (c + kTileTokens - 1) / kTileTokens;
+      const int tc = (c + TILE - 1) / TILE;
       const int incl = wave_incl_scan(c), tincl = wave_incl_scan(tc);
       if (c > 0) {
         r.at[e] = (uint16_t)(places + incl - c);
         r.expert[experts + __popcll(some & ((1ull << lane) - 1))] = (uint16_t)e;
         for (int i = 0; i < tc; ++i) {
           r.tile_expert[tiles + tincl - tc + i] = (uint16_t)e;
-          r.tile_first[tiles + tincl - tc + i] = (uint8_t)(kTileTokens * i);
+          r.tile_first[tiles + tincl - tc + i] = (uint8_t)(TILE * i);
         }
       }
       experts += __popcll(some);
@@ -235,209 +270,307 @@ __device__ __forceinline__ void route(const Fp8LayerArgs& a, Route& r, bool writ
     const int p = r.at[id[i]] + __popcll(r.mask[id[i]] & ((1ull << t) - 1));
     r.gate[p] = w[i];
     r.token[p] = (uint8_t)t;
+    if (writes) {
+      a.tables->gate[p] = w[i];
+      a.tables->token[p] = (uint8_t)t;
+    }
+  }
+  if (writes) {
+    for (int i = threadIdx.x; i < r.experts; i += blockDim.x) {
+      const int e = r.expert[i];
+      a.tables->expert[i] = Fp8Expert{(uint16_t)e, r.at[e], (uint16_t)__popcll(r.mask[e]), 0};
+    }
+    if (threadIdx.x == 0) a.tables->experts = r.experts;
   }
   __syncthreads();
 }
 
 // ----------------------------------------------------------------------------- products
 
-// Eight values as NT bf16 terms whose sum they are.
-template <typename ACT>
-struct Terms;
-template <>
-struct Terms<uint16_t> {
-  static constexpr int N = 1;
-  __device__ __forceinline__ static void load(const uint16_t* p, bf16x8v* t) {
-    const Bf16x8u w = *reinterpret_cast<const Bf16x8u*>(p);
-    t[0] = __builtin_bit_cast(bf16x8v, u32x4v{w.v[0], w.v[1], w.v[2], w.v[3]});
-  }
+constexpr int kWaves = 8;  // of a workgroup, taking blocks of 128 of K in turn
+
+// Columns of the MFMA: 16 tokens of one term, or 5 tokens of three (column 3 c + k is token c's
+// term k, the last column none's).
+template <int TERMS>
+struct Columns {
+  static constexpr int kTokens = TERMS == 1 ? 16 : 5;
+  static __device__ __forceinline__ int token(int column) { return TERMS == 1 ? column : column / 3; }
+  static __device__ __forceinline__ int term(int column) { return TERMS == 1 ? 0 : column % 3; }
 };
-__device__ __forceinline__ uint16_t bf16_bits(float f) { return OutElem<true>::rounded(f); }
-// f as three terms: 8 bits each, the last one exact; an infinity or a NaN stays whole in the first
-__device__ __forceinline__ void three_terms(float f, uint16_t* t) {
-  t[0] = bf16_bits(f);
-  const float r = f - OutElem<true>::load(t[0]);
-  t[1] = fabsf(f) < INFINITY ? bf16_bits(r) : 0;
-  t[2] = fabsf(f) < INFINITY ? bf16_bits(r - OutElem<true>::load(t[1])) : 0;
+
+// the other terms' sums, from the two columns on; meant for a token's first column
+__device__ __forceinline__ float add_terms(float v) {
+  constexpr int kShl1 = 0x101, kShl2 = 0x102;  // row_shl: the lane 1 (2) on in the row of 16
+  return v + (dppf<kShl1, 0xF>(0.f, v) + dppf<kShl2, 0xF>(0.f, v));
 }
-template <>
-struct Terms<float> {
-  static constexpr int N = 3;
-  __device__ __forceinline__ static void load(const float* p, bf16x8v* t) {
-    float v[8];
-    values8(p, v);
-    uint32_t w[3][4];
+
+// Bytes 16 p .. of a row of codes, or the last of the row past its end.
+__device__ __forceinline__ f8i4 piece(g_f8i4* row, int p, int pieces) { return row[min(p, pieces - 1)]; }
+// The 16 bf16 at place 16 p of a row, as the two steps of piece p take them.
+__device__ __forceinline__ void values(const uint16_t* row, int p, int pieces, bf16x8v* v) {
+  const uint16_t* at = row + min(p, pieces - 1) * 16;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint16_t a[3], b[3];
-      three_terms(v[2 * i], a);
-      three_terms(v[2 * i + 1], b);
-#pragma unroll
-      for (int k = 0; k < 3; ++k) w[k][i] = (uint32_t)a[k] | (uint32_t)b[k] << 16;
-    }
-#pragma unroll
-    for (int k = 0; k < 3; ++k) t[k] = __builtin_bit_cast(bf16x8v, u32x4v{w[k][0], w[k][1], w[k][2], w[k][3]});
+  for (int c = 0; c < 2; ++c) {
+    const Bf16x8u w = reinterpret_cast<const Bf16x8u*>(at)[c];
+    v[c] = __builtin_bit_cast(bf16x8v, u32x4v{w.v[0], w.v[1], w.v[2], w.v[3]});
   }
-};
+}
 
-constexpr int kWaves = 8;
+__device__ __forceinline__ f32x4 times(const f8i4* w, const bf16x8v* v) {
+  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) sum = mfma_bf16(f8_to_bf16(w[h][2 * c], w[h][2 * c + 1]), v[2 * h + c], sum);
+  return sum;
+}
 
-// One item of the first half: 8 gate rows and their 8 up rows x a tile of up to 16 tokens.
-template <typename ACT>
-__device__ __forceinline__ void gate_up(const Fp8LayerArgs& a, const Route& r, int tile, int rb, f32x4 (*part)[64]) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, q = lane >> 4;
-  const int e = r.tile_expert[tile], first = r.at[e] + r.tile_first[tile];
-  const int tokens = min(kTileTokens, __popcll(r.mask[e]) - r.tile_first[tile]);
-  const int HB = f8_blocks(a.H), IB = f8_blocks(a.I), pieces = a.H / 16;
-  const int row = min(rb * 8 + (i & 7), a.I - 1) + (i >= 8 ? a.I : 0);
-  g_f8i4* w = (g_f8i4*)(a.q_gu + ((int64_t)e * 2 * a.I + row) * a.H);
-  // rows 4q .. of the result: gate's for q < 2, up's else
-  const float* s = a.s_gu + (((int64_t)e * 2 + (q >> 1)) * IB + rb * 8 / kF8Block) * HB;
-  const bool mine = i < tokens;
-  const ACT* x = static_cast<const ACT*>(a.x) + (mine ? r.token[first + i] : 0) * a.ld_x;
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  for (int b = wave; b < HB; b += kWaves) {
-    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-    const float scale = s[b];
+// First half: an item is 16 gate rows and their 16 up rows x a tile of an expert's tokens.
+// A wave's blocks of K over all of the workgroup's items are one sequence, of which it has
+// kAhead under way.
+template <int TERMS>
+__global__ __launch_bounds__(64 * kWaves, 4) void k_f8_gate_up(Fp8LayerArgs a) {
+  typedef Columns<TERMS> Cols;
+  constexpr int kAhead = 2;
+  __shared__ Route r;
+  __shared__ f32x4 part[2][2][kWaves][64];
+  route<Cols::kTokens>(a, r, blockIdx.x == 0);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i = lane & 15, q = lane >> 4;
+  const int HB = f8_blocks(a.H), IB = f8_blocks(a.I), pieces = a.H / 16, per = a.I / 16;
+  const int steps = (HB + kWaves - 1) / kWaves, items = r.tiles * per;
+  const uint16_t* xs = TERMS == 1 ? static_cast<const uint16_t*>(a.x) : a.xt + (int64_t)Cols::term(i) * a.T * a.H;
+  const int64_t ld = TERMS == 1 ? a.ld_x : a.H;
+
+  struct Unit {
+    f8i4 g[2], u[2];
+    bf16x8v x[4];
+    float sg, su;
+  };
+  // what the loads are at
+  int item = blockIdx.x, step = 0;
+  g_f8i4 *wg = nullptr, *wu = nullptr;
+  const uint16_t* x = nullptr;
+  const float* s = nullptr;
+  auto load = [&](Unit& f) {
+    if (item >= items) return;
+    if (step == 0) {
+      const int tile = item / per, rb = item % per, e = r.tile_expert[tile], first = r.tile_first[tile];
+      const int tokens = min(Cols::kTokens, __popcll(r.mask[e]) - first);
+      wg = (g_f8i4*)(a.q_gu + ((int64_t)e * 2 * a.I + rb * 16 + i) * a.H);
+      wu = (g_f8i4*)(a.q_gu + ((int64_t)e * 2 * a.I + a.I + rb * 16 + i) * a.H);
+      s = a.s_gu + ((int64_t)e * 2 * IB + rb * 16 / kF8Block) * HB;
+      // columns past the tile's are the first one's again, and not stored
+      const int c = Cols::token(i);
+      x = xs + r.token[r.at[e] + first + (c < tokens ? c : 0)] * ld;
+    }
+    const int b = min(wave + step * kWaves, HB - 1);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int p = b * 8 + 4 * h + q;
-      f8i4 wv = w[min(p, pieces - 1)];
-      if (p >= pieces) wv = f8i4{0, 0, 0, 0};
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        bf16x8v t[Terms<ACT>::N] = {};
-        if (mine && p < pieces) Terms<ACT>::load(x + p * 16 + 8 * c, t);
-        const bf16x8v wb = f8_to_bf16(wv[2 * c], wv[2 * c + 1]);
-#pragma unroll
-        for (int k = 0; k < Terms<ACT>::N; ++k) sum = mfma_bf16(wb, t[k], sum);
-      }
+      f.g[h] = piece(wg, b * 8 + 4 * h + q, pieces);
+      f.u[h] = piece(wu, b * 8 + 4 * h + q, pieces);
     }
 #pragma unroll
-    for (int v = 0; v < 4; ++v) acc[v] = fmaf(scale, sum[v], acc[v]);
-  }
-  part[wave][lane] = acc;
-  __syncthreads();
-  const int c = threadIdx.x / 8, j = threadIdx.x % 8;
-  if (c < tokens && rb * 8 + j < a.I) {
-    const float* p = reinterpret_cast<const float*>(&part[0][16 * (j / 4) + c]) + j % 4;
-    float g = 0.f, u = 0.f;
-#pragma unroll
-    for (int k = 0; k < kWaves; ++k) {
-      g += p[k * 64 * 4];
-      u += p[k * 64 * 4 + 32 * 4];  // up's rows are 8 on
+    for (int h = 0; h < 2; ++h) values(x, b * 8 + 4 * h + q, pieces, f.x + 2 * h);
+    f.sg = s[b];
+    f.su = s[(int64_t)IB * HB + b];
+    if (++step == steps) {
+      step = 0;
+      item += gridDim.x;
     }
-    uint16_t t[3];
-    three_terms(g / (1.f + expf(-g)) * u, t);
-    const int64_t at = (int64_t)(first + c) * a.I + rb * 8 + j, plane = (int64_t)a.T * a.k * a.I;
+  };
+  // what the sums are at
+  int at = blockIdx.x, done = 0, turn = 0;
+  f32x4 gate = {0.f, 0.f, 0.f, 0.f}, up = gate;
+  auto products = [&](Unit& f) {
+    const int b = wave + done * kWaves;
+    if (b < HB) {
+      if (b * 8 + 8 > pieces) {  // K ends inside the block
 #pragma unroll
-    for (int k = 0; k < 3; ++k) a.h[k * plane + at] = t[k];
-  }
-  __syncthreads();
-}
-
-template <typename ACT>
-__global__ __launch_bounds__(64 * kWaves) void k_f8_gate_up(Fp8LayerArgs a) {
-  __shared__ Route r;
-  __shared__ f32x4 part[kWaves][64];
-  route(a, r, blockIdx.x == 0);
-  const int per = (a.I - 1) / 8 + 1;
-  for (int item = blockIdx.x; item < r.tiles * per; item += gridDim.x) gate_up<ACT>(a, r, item / per, item % per, part);
-}
-
-// One item of the second half: 16 rows of down x every token, over all experts. Column i of
-// group g is token 16 g + i; an expert's products are added with its weight, those of
-// tokens that did not choose it are left out.
-template <typename ACT, int G>
-__device__ __forceinline__ void down(const Fp8LayerArgs& a, const Route& r, int rb, f32x4 (*part)[G][64]) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, q = lane >> 4;
-  const int HB = f8_blocks(a.H), IB = f8_blocks(a.I), pieces = a.I / 16, n0 = rb * 16;
-  const int64_t plane = (int64_t)a.T * a.k * a.I;
-  f32x4 acc[G];
-#pragma unroll
-  for (int g = 0; g < G; ++g) acc[g] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int n = 0; n < r.experts; ++n) {
-    const int e = r.expert[n];
-    const uint64_t mask = r.mask[e];
-    g_f8i4* w = (g_f8i4*)(a.q_dn + ((int64_t)e * a.H + min(n0 + i, a.H - 1)) * a.I);
-    const float* s = a.s_dn + ((int64_t)e * HB + n0 / kF8Block) * IB;
-    for (int b = wave; b < IB; b += kWaves) {
-      f8i4 wv[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int p = b * 8 + 4 * h + q;
-        wv[h] = w[min(p, pieces - 1)];
-        if (p >= pieces) wv[h] = f8i4{0, 0, 0, 0};
-      }
-      const float scale = s[b];
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        if (((mask >> (16 * g)) & 0xFFFF) == 0) continue;
-        const int t = 16 * g + i;
-        const bool mine = (mask >> t) & 1;
-        const int at = mine ? r.at[e] + __popcll(mask & ((1ull << t) - 1)) : 0;
-        const uint16_t* hp = a.h + (int64_t)at * a.I;
-        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int p = b * 8 + 4 * h + q;
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const bf16x8v wb = f8_to_bf16(wv[h][2 * c], wv[h][2 * c + 1]);
-#pragma unroll
-            for (int k = 0; k < 3; ++k) {
-              bf16x8v v = {};
-              if (mine && p < pieces) v = *reinterpret_cast<const bf16x8v*>(hp + k * plane + p * 16 + 8 * c);
-              sum = mfma_bf16(wb, v, sum);
-            }
+        for (int h = 0; h < 2; ++h)
+          if (b * 8 + 4 * h + q >= pieces) {
+            f.g[h] = f.u[h] = f8i4{0, 0, 0, 0};
+            f.x[2 * h] = f.x[2 * h + 1] = bf16x8v{};
           }
-        }
-        const float ws = mine ? r.gate[at] * scale : 0.f;
+      }
+      const f32x4 pg = times(f.g, f.x), pu = times(f.u, f.x);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) acc[g][v] = mine ? fmaf(ws, sum[v], acc[g][v]) : acc[g][v];
+      for (int v = 0; v < 4; ++v) {
+        gate[v] = fmaf(f.sg, pg[v], gate[v]);
+        up[v] = fmaf(f.su, pu[v], up[v]);
+      }
+    }
+    if (++done < steps) return;
+    // the item's sums meet; another buffer each time, so that one barrier does
+    if (TERMS > 1) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        gate[v] = add_terms(gate[v]);
+        up[v] = add_terms(up[v]);
+      }
+    }
+    part[turn][0][wave][lane] = gate;
+    part[turn][1][wave][lane] = up;
+    __syncthreads();
+    const int tile = at / per, rb = at % per, e = r.tile_expert[tile], first = r.tile_first[tile];
+    const int tokens = min(Cols::kTokens, __popcll(r.mask[e]) - first);
+    const int c = threadIdx.x / 16, j = threadIdx.x % 16;
+    if (c < tokens) {
+      const int column = TERMS == 1 ? c : 3 * c;
+      const float* p = reinterpret_cast<const float*>(&part[turn][0][0][16 * (j / 4) + column]) + j % 4;
+      float gs = 0.f, us = 0.f;
+#pragma unroll
+      for (int k = 0; k < kWaves; ++k) {
+        gs += p[k * 64 * 4];
+        us += p[(kWaves + k) * 64 * 4];
+      }
+      uint16_t t[3];
+      three_terms(gs / (1.f + expf(-gs)) * us, t);
+      const int64_t to = (int64_t)(r.at[e] + first + c) * a.I + rb * 16 + j, plane = (int64_t)a.T * a.k * a.I;
+#pragma unroll
+      for (int k = 0; k < 3; ++k) a.h[k * plane + to] = t[k];
+    }
+    gate = up = f32x4{0.f, 0.f, 0.f, 0.f};
+    done = 0;
+    turn ^= 1;
+    at += gridDim.x;
+  };
+  Unit f[kAhead];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) load(f[k]);
+  while (at < items) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (at < items) {
+        products(f[k]);
+        load(f[k]);
       }
     }
   }
+}
+
+// Second half: 16 rows of down x every token, over all experts. A wave's blocks of K over the
+// experts are one sequence, of which it has kAhead under way, with the first tile of the
+// expert's tokens. What a block gives a token is added, with the token's weight for the
+// expert, to the wave's sums in LDS; the waves' sums meet at the end.
+template <typename ACT>
+__global__ __launch_bounds__(64 * kWaves, 4) void k_f8_down(Fp8LayerArgs a) {
+  typedef Columns<3> Cols;
+  constexpr int kAhead = 3;
+  extern __shared__ __attribute__((aligned(16))) float sums[];  // [kWaves][T][16]
+  __shared__ Fp8Expert experts[kF8LayerExperts];
+  __shared__ float gates[kMaxAssign];
+  __shared__ uint8_t tokens[kMaxAssign];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i = lane & 15, q = lane >> 4;
+  const int HB = f8_blocks(a.H), IB = f8_blocks(a.I), pieces = a.I / 16, n0 = blockIdx.x * 16;
+  const int n_experts = a.tables->experts;
+  for (int k = threadIdx.x; k < n_experts; k += 64 * kWaves) experts[k] = a.tables->expert[k];
+  for (int k = threadIdx.x; k < a.T * a.k; k += 64 * kWaves) {
+    gates[k] = a.tables->gate[k];
+    tokens[k] = a.tables->token[k];
+  }
+  for (int k = threadIdx.x; k < kWaves * a.T * 16; k += 64 * kWaves) sums[k] = 0.f;
+  __syncthreads();
+  const int steps = (IB + kWaves - 1) / kWaves;
+  const uint16_t* hs = a.h + (int64_t)Cols::term(i) * a.T * a.k * a.I;
+  const int c = Cols::token(i);
+
+  struct Unit {
+    f8i4 w[2];
+    bf16x8v h[4];
+    float s;
+  };
+  auto load_h = [&](bf16x8v* h, const Fp8Expert& e, int first, int b) {
+    // columns past the tile's are the first one's again, and not used
+    const uint16_t* row = hs + (int64_t)(e.at + first + (first + c < e.count ? c : 0)) * a.I;
 #pragma unroll
-  for (int g = 0; g < G; ++g) part[wave][g][lane] = acc[g];
+    for (int k = 0; k < 2; ++k) values(row, b * 8 + 4 * k + q, pieces, h + 2 * k);
+  };
+  int n = 0, step = 0;
+  auto load = [&](Unit& f) {
+    if (n >= n_experts) return;
+    const Fp8Expert e = experts[n];
+    const int b = min(wave + step * kWaves, IB - 1);
+    g_f8i4* w = (g_f8i4*)(a.q_dn + ((int64_t)e.expert * a.H + n0 + i) * a.I);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) f.w[k] = piece(w, b * 8 + 4 * k + q, pieces);
+    load_h(f.h, e, 0, b);
+    f.s = a.s_dn[((int64_t)e.expert * HB + n0 / kF8Block) * IB + b];
+    if (++step == steps) {
+      step = 0;
+      ++n;
+    }
+  };
+  int at = 0, done = 0;
+  auto products = [&](Unit& f) {
+    const int b = wave + done * kWaves;
+    const Fp8Expert e = experts[at];
+    if (b < IB) {
+      const bool ends = b * 8 + 8 > pieces;  // K ends inside the block
+      if (ends) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (b * 8 + 4 * k + q >= pieces) f.w[k] = f8i4{0, 0, 0, 0};
+      }
+      for (int first = 0; first < e.count; first += Cols::kTokens) {
+        if (first > 0) load_h(f.h, e, first, b);
+        if (ends) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (b * 8 + 4 * k + q >= pieces) f.h[2 * k] = f.h[2 * k + 1] = bf16x8v{};
+        }
+        f32x4 sum = times(f.w, f.h);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) sum[v] = add_terms(sum[v]);
+        if (Cols::term(i) == 0 && first + c < e.count && c < Cols::kTokens) {
+          const float scale = gates[e.at + first + c] * f.s;
+          f32x4* to = reinterpret_cast<f32x4*>(&sums[(wave * a.T + tokens[e.at + first + c]) * 16 + 4 * q]);
+          f32x4 v = *to;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = fmaf(scale, sum[k], v[k]);
+          *to = v;
+        }
+      }
+    }
+    if (++done == steps) {
+      done = 0;
+      ++at;
+    }
+  };
+  Unit f[kAhead];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) load(f[k]);
+  while (at < n_experts) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (at < n_experts) {
+        products(f[k]);
+        load(f[k]);
+      }
+    }
+  }
   __syncthreads();
   for (int o = threadIdx.x; o < 16 * a.T; o += 64 * kWaves) {
-    const int t = o / 16, j = o % 16, n = n0 + j;
-    const float* p = reinterpret_cast<const float*>(&part[0][t / 16][16 * (j / 4) + t % 16]) + j % 4;
+    const int t = o / 16, col = n0 + o % 16;
     float v = 0.f;
 #pragma unroll
-    for (int k = 0; k < kWaves; ++k) v += p[k * G * 64 * 4];
-    if (n >= a.H) continue;
-    a.y[t * a.ld_y + n] = v;
+    for (int k = 0; k < kWaves; ++k) v += sums[k * a.T * 16 + o];
+    a.y[t * a.ld_y + col] = v;
     if (a.x_out) {
       typedef OutElem<sizeof(ACT) == 2> Out;
-      const float s = Out::load(static_cast<const ACT*>(a.x)[t * a.ld_x + n]) + v;
-      static_cast<ACT*>(a.x_out)[t * a.ld_x_out + n] = Out::rounded(s);
+      const float x = Out::load(static_cast<const ACT*>(a.x)[t * a.ld_x + col]) + v;
+      static_cast<ACT*>(a.x_out)[t * a.ld_x_out + col] = Out::rounded(x);
     }
   }
-  __syncthreads();
-}
-
-template <typename ACT, int G>
-__global__ __launch_bounds__(64 * kWaves) void k_f8_down(Fp8LayerArgs a) {
-  __shared__ Route r;
-  __shared__ f32x4 part[kWaves][G][64];
-  route(a, r, false);
-  for (int rb = blockIdx.x; rb < (a.H - 1) / 16 + 1; rb += gridDim.x) down<ACT, G>(a, r, rb, part);
 }
 
 template <typename ACT>
 void layer(const Fp8LayerArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((k_f8_router<ACT>), dim3(a.logits_in ? a.T : a.E), dim3(64 * kRouterWaves), 0, s, a);
-  const int64_t items = (int64_t)a.T * a.k * ((a.I - 1) / 8 + 1);
-  hipLaunchKernelGGL((k_f8_gate_up<ACT>), dim3((unsigned)std::min<int64_t>(items, 1024)), dim3(64 * kWaves), 0, s, a);
-  const int rows = (a.H - 1) / 16 + 1, grid = std::min(rows, 1024);
-  if (a.T <= 16)
-    hipLaunchKernelGGL((k_f8_down<ACT, 1>), dim3(grid), dim3(64 * kWaves), 0, s, a);
-  else if (a.T <= 32)
-    hipLaunchKernelGGL((k_f8_down<ACT, 2>), dim3(grid), dim3(64 * kWaves), 0, s, a);
-  else
-    hipLaunchKernelGGL((k_f8_down<ACT, 4>), dim3(grid), dim3(64 * kWaves), 0, s, a);
+  constexpr int kTerms = sizeof(ACT) == 2 ? 1 : 3;
+  const int rows = a.logits_in ? 0 : a.E, more = a.logits_in || kTerms == 3 ? a.T : 0;
+  hipLaunchKernelGGL((k_f8_router<ACT>), dim3(rows + more), dim3(kRouterThreads), 0, s, a, rows);
+  const int64_t items = (int64_t)a.T * a.k * (a.I / 16);
+  hipLaunchKernelGGL((k_f8_gate_up<kTerms>), dim3((unsigned)std::min<int64_t>(items, 512)), dim3(64 * kWaves), 0, s, a);
+  hipLaunchKernelGGL((k_f8_down<ACT>), dim3(a.H / 16), dim3(64 * kWaves), sizeof(float) * kWaves * 16 * a.T, s, a);
 }
 
 }  // namespace
