@@ -44,17 +44,19 @@ void launch_fp8_gemm(const Fp8Args& a, bool out_bf16, hipStream_t s);
 
 constexpr int kF8LayerTokens = 64, kF8LayerExperts = 1024, kF8LayerTopK = 32;
 
-// An expert with tokens: its first place among the assignments, grouped by expert in
-// ascending order of experts and tokens, and how many they are.
-struct Fp8Expert {
-  uint16_t expert, at, count, none;
+// Up to a few tokens of one expert: the expert, the first one's place among the assignments
+// (grouped by expert, in ascending order of experts and tokens) and how many they are.
+struct Fp8Tile {
+  uint16_t expert, at, tokens, none;
 };
 struct Fp8Tables {
-  Fp8Expert expert[kF8LayerExperts];
-  float gate[kF8LayerTokens * kF8LayerTopK];    // by place
-  uint8_t token[kF8LayerTokens * kF8LayerTopK];
-  int experts;
+  Fp8Tile tile[kF8LayerTokens * kF8LayerTopK];
+  float gate[kF8LayerTokens * kF8LayerTopK];  // by place
+  // [T][k]: a token's places, ascending, each with its tile's first one in the upper half, then kF8NoPlace
+  uint32_t place[kF8LayerTokens * kF8LayerTopK];
+  int tiles, places;
 };
+constexpr uint32_t kF8NoPlace = ~0u;
 
 struct Fp8LayerArgs {
   const void* x;          // [T][H] act
@@ -70,11 +72,12 @@ struct Fp8LayerArgs {
   float* logits;          // [T][E]: the caller's, or the workspace's; null with logits_in alone
   int32_t* ids;           // [T][k] or null
   float* gate;            // [T][k] or null
-  uint16_t* h;            // workspace: the intermediate's three bf16 terms, [3][T k][I]
-  uint16_t* xt;           // workspace: fp32 activations' three bf16 terms, [3][T][H]
+  uint16_t* h;            // workspace: the intermediate's three bf16 terms, [3][T k][Ip]
+  uint16_t* xt;           // workspace: x, or its three bf16 terms, [terms][T][Hp]
   Fp8Tables* tables;      // workspace
   int64_t ld_x, ld_router, ld_y, ld_x_out;
   int T, H, I, E, k;
+  int Hp, Ip;             // H and I up to whole blocks, the rest zeros
 };
 void launch_fp8_layer(const Fp8LayerArgs& a, bool act_bf16, hipStream_t s);
 

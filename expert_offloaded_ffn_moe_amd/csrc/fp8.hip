@@ -30,15 +30,15 @@ moe_status check_layer_shape(int T, int H, int I, int E, int k) {
   return MOE_OK;
 }
 
-// the layer's workspace: tables | logits [T][E] | three bf16 terms of fp32 activations [3][T][H] |
-// of the intermediate [3][T k][I]
+// the layer's workspace: tables | logits [T][E] | bf16 terms of the activations [3][T][H] and of
+// the intermediate [3][T k][I], H and I up to whole blocks
 struct LayerSpace {
   size_t tables = 0, logits, x, h, bytes;
   LayerSpace(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k) {
     logits = up256(sizeof(Fp8Tables));
     x = logits + up256(sizeof(float) * T * E);
-    h = x + up256(3 * sizeof(uint16_t) * T * H);
-    bytes = h + up256(3 * sizeof(uint16_t) * T * k * I);
+    h = x + up256(3 * sizeof(uint16_t) * T * f8_blocks(H) * kF8Block);
+    bytes = h + up256(3 * sizeof(uint16_t) * T * k * f8_blocks(I) * kF8Block);
   }
 };
 
@@ -170,6 +170,8 @@ moe_status moe_fp8_layer(const moe_fp8_layer_args* a, moe_stream stream) {
   g.I = I;
   g.E = E;
   g.k = k;
+  g.Hp = HB * kF8Block;
+  g.Ip = IB * kF8Block;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const OnStreamDevice on(st);
   CHECK(on.ready());

@@ -74,10 +74,10 @@ __device__ __forceinline__ void three_terms(float f, uint16_t* t) {
   t[2] = finite ? Bf::rounded(r - Bf::load(t[1])) : 0;
 }
 
-// Workgroups 0 .. E - 1 take a row of the router each, H split over its threads, the others
-// (fp32 activations) a token each, whose terms they write. With logits_in there are T
-// workgroups, which copy a token's logits where they are wanted. Tokens are taken four at a
-// time, their loads ahead of the sums.
+// The first `rows` workgroups take a row of the router each, H split over their threads, the
+// others a token each, whose values or terms they write where the products read them (and its
+// given logits, where they are wanted). Tokens are taken four at a time, their loads ahead of
+// the sums.
 constexpr int kRouterThreads = 256, kRouterTokens = 4;
 template <typename ACT>
 __global__ __launch_bounds__(kRouterThreads) void k_f8_router(Fp8LayerArgs a, int rows) {
@@ -87,13 +87,15 @@ __global__ __launch_bounds__(kRouterThreads) void k_f8_router(Fp8LayerArgs a, in
     const int t = blockIdx.x - rows;
     if (a.logits_in && a.logits)
       for (int i = threadIdx.x; i < a.E; i += kRouterThreads) a.logits[(int64_t)t * a.E + i] = a.logits_in[(int64_t)t * a.E + i];
-    if (sizeof(ACT) == 4) {
-      const float* x = static_cast<const float*>(a.x) + t * a.ld_x;
-      for (int i = threadIdx.x; i < a.H; i += kRouterThreads) {
+    const ACT* x = static_cast<const ACT*>(a.x) + t * a.ld_x;
+    for (int i = threadIdx.x; i < a.Hp; i += kRouterThreads) {
+      if (sizeof(ACT) == 2) {
+        a.xt[(int64_t)t * a.Hp + i] = i < a.H ? x[i] : 0;
+      } else {
         uint16_t v[3];
-        three_terms(x[i], v);
+        three_terms(i < a.H ? x[i] : 0.f, v);
 #pragma unroll
-        for (int k = 0; k < 3; ++k) a.xt[((int64_t)k * a.T + t) * a.H + i] = v[k];
+        for (int k = 0; k < 3; ++k) a.xt[((int64_t)k * a.T + t) * a.Hp + i] = v[k];
       }
     }
     return;
@@ -139,15 +141,14 @@ __global__ __launch_bounds__(kRouterThreads) void k_f8_router(Fp8LayerArgs a, in
 // Assignments grouped by expert, in ascending order of experts and tokens. Those of weight
 // 0 are left out.
 struct Route {
-  uint64_t mask[kF8LayerExperts];     // the expert's tokens
-  float gate[kMaxAssign];             // weights, in grouped order
-  uint16_t at[kF8LayerExperts];       // the expert's first place in that order
-  uint16_t expert[kF8LayerExperts];   // experts with tokens
-  uint16_t tile_expert[kMaxAssign];   // tiles: the expert, and the first of up to `tile` of its tokens
-  uint8_t tile_first[kMaxAssign];
-  uint8_t token[kMaxAssign];          // token of a place
-  int experts, tiles;
+  uint64_t mask[kF8LayerExperts];  // the expert's tokens
+  Fp8Tile tile[kMaxAssign];
+  float gate[kMaxAssign];          // weights, in grouped order
+  uint16_t at[kF8LayerExperts];    // the expert's first place in that order
+  uint8_t token[kMaxAssign];       // token of a place
+  int tiles;
 };
+constexpr int kDownTokens = 2;  // of a tile of the second half
 
 // Orders as the logits do, with NaN before every number; over 0.
 __device__ __forceinline__ uint32_t logit_key(float f) {
@@ -159,7 +160,7 @@ __device__ __forceinline__ uint32_t logit_key(float f) {
 // The k experts of one token by one wave: k rounds of the wave's maximum and the lowest
 // expert that has it. Lane l holds experts l, l + 64, ...; lane j ends with slot j.
 template <int NV>
-__device__ __forceinline__ void choose(const float* logits, int E, int k, int& id, float& w) {
+__device__ __forceinline__ void choose(const float* logits, int E, int k, int& id, float& w, int& rank) {
   const int lane = threadIdx.x & 63;
   float f[NV];
   uint32_t key[NV];
@@ -193,384 +194,446 @@ __device__ __forceinline__ void choose(const float* logits, int E, int k, int& i
   const float p = lane < k && mine != -INFINITY ? expf(mine - top) : 0.f;
   const float sum = wave_sum(p);
   w = sum == 0.f ? 0.f : p / sum;  // every logit -infinity: nothing
+  rank = 0;  // among the token's experts of any weight
+  for (int j = 0; j < k; ++j) {
+    const int other = __builtin_amdgcn_readlane(id, j);
+    const float wo = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w), j));
+    rank += wo != 0.f && other < id;
+  }
 }
 
-// `writes`: one workgroup of the launch, which also leaves the tables for the next launch.
+// Tiles of up to TILE tokens for this launch; the workgroup that `writes` also leaves the outputs,
+// and the tables for the next launch.
 template <int TILE>
 __device__ __forceinline__ void route(const Fp8LayerArgs& a, Route& r, bool writes) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   const float* logits = a.logits ? a.logits : a.logits_in;
+  uint32_t* slot = reinterpret_cast<uint32_t*>(r.tile);  // id and rank of an assignment, until the tiles are made
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) r.mask[e] = 0;
   __syncthreads();
-  // the slots wait in the tables' arrays, which are filled later: ids in tile_expert, weights in
-  // gate, by assignment
   for (int t = wave; t < a.T; t += waves) {
-    int id;
+    int id, rank;
     float w;
     const float* row = logits + (int64_t)t * a.E;
     const int nv = (a.E + 63) / 64;
     if (nv <= 2)
-      choose<2>(row, a.E, a.k, id, w);
+      choose<2>(row, a.E, a.k, id, w, rank);
     else if (nv <= 6)
-      choose<6>(row, a.E, a.k, id, w);
+      choose<6>(row, a.E, a.k, id, w, rank);
     else
-      choose<16>(row, a.E, a.k, id, w);
+      choose<16>(row, a.E, a.k, id, w, rank);
     if (lane < a.k) {
+      const int s = t * a.k + lane;
       if (w != 0.f) atomicOr(reinterpret_cast<unsigned long long*>(&r.mask[id]), 1ull << t);
-      r.tile_expert[t * a.k + lane] = (uint16_t)id;
-      r.gate[t * a.k + lane] = w;
+      slot[s] = (uint32_t)id | (uint32_t)rank << 16;
+      r.gate[s] = w;
       if (writes) {
-        if (a.ids) a.ids[t * a.k + lane] = id;
-        if (a.gate) a.gate[t * a.k + lane] = w;
+        a.tables->place[s] = kF8NoPlace;
+        if (a.ids) a.ids[s] = id;
+        if (a.gate) a.gate[s] = w;
       }
     }
   }
   __syncthreads();
-  // this thread's assignments, out of the arrays that they wait in
-  constexpr int kMine = kMaxAssign / 256;  // of 256 threads and more
-  int id[kMine];
+  constexpr int kMine = kMaxAssign / 512;  // a thread's assignments
+  uint32_t mine[kMine];
   float w[kMine];
   const int n = a.T * a.k;
 #pragma unroll
   for (int i = 0; i < kMine; ++i) {
-    const int s = threadIdx.x + i * blockDim.x;
-    id[i] = s < n ? r.tile_expert[s] : 0;
+    const int s = threadIdx.x + i * 512;
+    mine[i] = s < n ? slot[s] : 0;
     w[i] = s < n ? r.gate[s] : 0.f;
   }
   __syncthreads();
   if (wave == 0) {
-    int experts = 0, places = 0, tiles = 0;
+    int places = 0, tiles = 0, down = 0;
     for (int e0 = 0; e0 < a.E; e0 += 64) {
       const int e = e0 + lane, c = e < a.E ? __popcll(r.mask[e]) : 0;
-      const uint64_t some = __ballot(c > 0);
-      const int tc = (c + TILE - 1) / TILE;
-      const int incl = wave_incl_scan(c), tincl = wave_incl_scan(tc);
+      if (__ballot(c > 0) == 0) continue;
+      const int tc = (c + TILE - 1) / TILE, dc = (c + kDownTokens - 1) / kDownTokens;
+      const int incl = wave_incl_scan(c), tincl = wave_incl_scan(tc), dincl = wave_incl_scan(dc);
       if (c > 0) {
-        r.at[e] = (uint16_t)(places + incl - c);
-        r.expert[experts + __popcll(some & ((1ull << lane) - 1))] = (uint16_t)e;
-        for (int i = 0; i < tc; ++i) {
-          r.tile_expert[tiles + tincl - tc + i] = (uint16_t)e;
-          r.tile_first[tiles + tincl - tc + i] = (uint8_t)(TILE * i);
-        }
+        const int at = places + incl - c;
+        r.at[e] = (uint16_t)at;
+        for (int i = 0; i < tc; ++i)
+          r.tile[tiles + tincl - tc + i] = Fp8Tile{(uint16_t)e, (uint16_t)(at + TILE * i), (uint16_t)min(TILE, c - TILE * i), 0};
+        if (writes)
+          for (int i = 0; i < dc; ++i)
+            a.tables->tile[down + dincl - dc + i] =
+                Fp8Tile{(uint16_t)e, (uint16_t)(at + kDownTokens * i), (uint16_t)min(kDownTokens, c - kDownTokens * i), 0};
       }
-      experts += __popcll(some);
       places += __builtin_amdgcn_readlane(incl, 63);
       tiles += __builtin_amdgcn_readlane(tincl, 63);
+      down += __builtin_amdgcn_readlane(dincl, 63);
     }
     if (lane == 0) {
-      r.experts = experts;
       r.tiles = tiles;
+      if (writes) {
+        a.tables->tiles = down;
+        a.tables->places = places;
+      }
     }
   }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kMine; ++i) {
     if (w[i] == 0.f) continue;
-    const int t = (threadIdx.x + i * blockDim.x) / a.k;
-    const int p = r.at[id[i]] + __popcll(r.mask[id[i]] & ((1ull << t) - 1));
-    r.gate[p] = w[i];
+    const int t = (threadIdx.x + i * 512) / a.k, id = mine[i] & 0xFFFF;
+    const int within = __popcll(r.mask[id] & ((1ull << t) - 1)), p = r.at[id] + within;
     r.token[p] = (uint8_t)t;
     if (writes) {
       a.tables->gate[p] = w[i];
-      a.tables->token[p] = (uint8_t)t;
+      a.tables->place[t * a.k + (mine[i] >> 16)] = (uint32_t)p | (uint32_t)(p - within % kDownTokens) << 16;  // behind the barriers since its first value
     }
-  }
-  if (writes) {
-    for (int i = threadIdx.x; i < r.experts; i += blockDim.x) {
-      const int e = r.expert[i];
-      a.tables->expert[i] = Fp8Expert{(uint16_t)e, r.at[e], (uint16_t)__popcll(r.mask[e]), 0};
-    }
-    if (threadIdx.x == 0) a.tables->experts = r.experts;
   }
   __syncthreads();
 }
 
 // ----------------------------------------------------------------------------- products
+//
+// A load instruction takes a cycle for each line that each four neighbouring lanes touch, so lanes
+// are given two neighbouring pieces of a row: the MFMA's rows 2 a and 2 a + 1 are both row a of
+// the weights, at a block's even and odd pieces of 16 codes (piece 2 q + (row & 1) for lane quarter
+// q), and its columns 2 v and 2 v + 1 both vector v, at even and odd pieces. Of the products
+// of rows and columns those of like parity are the sums wanted, of 8 rows with 8 vectors; a
+// row's whole sum is that of two neighbouring lanes. (With a row for each of the 16 rows, the
+// lines bounded the 7168-wide layer's first half at 4.9 TB/s and the second at 2.5.)
 
 constexpr int kWaves = 8;  // of a workgroup, taking blocks of 128 of K in turn
+constexpr int kRows = 8;   // of weights in an operand
 
-// Columns of the MFMA: 16 tokens of one term, or 5 tokens of three (column 3 c + k is token c's
-// term k, the last column none's).
+// Vectors: 8 tokens of one term, or 2 tokens of three (vector 3 c + k is token c's term k).
 template <int TERMS>
-struct Columns {
-  static constexpr int kTokens = TERMS == 1 ? 16 : 5;
-  static __device__ __forceinline__ int token(int column) { return TERMS == 1 ? column : column / 3; }
-  static __device__ __forceinline__ int term(int column) { return TERMS == 1 ? 0 : column % 3; }
+struct Vectors {
+  static constexpr int kTokens = TERMS == 1 ? 8 : 2;
+  static __device__ __forceinline__ int token(int v) { return TERMS == 1 ? v : v / 3; }
+  static __device__ __forceinline__ int term(int v) { return TERMS == 1 ? 0 : v % 3; }
+  // the sum over the parities, and over the terms; in the first lane of a token's
+  static __device__ __forceinline__ float whole(float v) {
+    constexpr int kShl2 = 0x102, kShl4 = 0x104;  // row_shl: the lane 2 (4) on in the row of 16
+    v += dppf<kDppXor1, 0xF>(0.f, v);
+    return TERMS == 1 ? v : v + (dppf<kShl2, 0xF>(0.f, v) + dppf<kShl4, 0xF>(0.f, v));
+  }
+  static __device__ __forceinline__ int lane_of(int token) { return TERMS == 1 ? 2 * token : 6 * token; }
+  static __device__ __forceinline__ bool is_first(int column) { return TERMS == 1 ? column % 2 == 0 : column == 0 || column == 6; }
 };
 
-// the other terms' sums, from the two columns on; meant for a token's first column
-__device__ __forceinline__ float add_terms(float v) {
-  constexpr int kShl1 = 0x101, kShl2 = 0x102;  // row_shl: the lane 1 (2) on in the row of 16
-  return v + (dppf<kShl1, 0xF>(0.f, v) + dppf<kShl2, 0xF>(0.f, v));
+// 0 that the compiler takes for a lane's own: a load with it in its address is a vector load, which is
+// waited for in the order of the vector loads. (A scalar load is waited for with every LDS read.)
+__device__ __forceinline__ int lane_zero() {
+  int z;
+  asm volatile("v_mov_b32 %0, 0" : "=v"(z));
+  return z;
 }
 
-// Bytes 16 p .. of a row of codes, or the last of the row past its end.
-__device__ __forceinline__ f8i4 piece(g_f8i4* row, int p, int pieces) { return row[min(p, pieces - 1)]; }
-// The 16 bf16 at place 16 p of a row, as the two steps of piece p take them.
-__device__ __forceinline__ void values(const uint16_t* row, int p, int pieces, bf16x8v* v) {
-  const uint16_t* at = row + min(p, pieces - 1) * 16;
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    const Bf16x8u w = reinterpret_cast<const Bf16x8u*>(at)[c];
-    v[c] = __builtin_bit_cast(bf16x8v, u32x4v{w.v[0], w.v[1], w.v[2], w.v[3]});
-  }
+// A lane's 16 values of a vector, as two steps of the MFMA take them.
+struct Values {
+  bf16x8v v[2];
+};
+__device__ __forceinline__ Values load_values(const uint16_t* at) {
+  typedef __attribute__((address_space(1))) const bf16x8v g_bf16x8;
+  return Values{{((g_bf16x8*)at)[0], ((g_bf16x8*)at)[1]}};
 }
 
-__device__ __forceinline__ f32x4 times(const f8i4* w, const bf16x8v* v) {
-  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+// The sums of 8 rows with a block's values, all parities: added, scaled, to s.
+__device__ __forceinline__ void add_products(const f8i4& w, const Values& x, float scale, f32x4& s) {
+  f32x4 p = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+  for (int c = 0; c < 2; ++c) p = mfma_bf16(f8_to_bf16(w[2 * c], w[2 * c + 1]), x.v[c], p);
 #pragma unroll
-    for (int c = 0; c < 2; ++c) sum = mfma_bf16(f8_to_bf16(w[h][2 * c], w[h][2 * c + 1]), v[2 * h + c], sum);
-  return sum;
+  for (int v = 0; v < 4; ++v) s[v] = fmaf(scale, p[v], s[v]);
+}
+__device__ __forceinline__ float of_parity(float even, float odd) { return threadIdx.x & 1 ? odd : even; }
+
+__device__ __forceinline__ Fp8Tile uniform(const Fp8Tile* tile) {
+  const uint64_t u = *reinterpret_cast<const uint64_t*>(tile);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)u), hi = __builtin_amdgcn_readfirstlane((uint32_t)(u >> 32));
+  return Fp8Tile{(uint16_t)lo, (uint16_t)(lo >> 16), (uint16_t)hi, 0};
 }
 
-// First half: an item is 16 gate rows and their 16 up rows x a tile of an expert's tokens.
-// A wave's blocks of K over all of the workgroup's items are one sequence, of which it has
-// kAhead under way.
+// Every wave's LDS accesses are done; loads from memory stay under way.
+__device__ __forceinline__ void meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// First half: an item is 16 gate rows and their 16 up rows x a tile of an expert's tokens. A
+// workgroup keeps to its rows and takes every gridDim.y'th tile. A wave's blocks of K over all of
+// its items are one sequence, of which it has kAhead under way. Every turn loads, past the
+// end the last tile's again: a load that a branch leaves out would make every wait one for
+// all loads.
 template <int TERMS>
 __global__ __launch_bounds__(64 * kWaves, 4) void k_f8_gate_up(Fp8LayerArgs a) {
-  typedef Columns<TERMS> Cols;
-  constexpr int kAhead = 2;
+  typedef Vectors<TERMS> Vec;
+  constexpr int kAhead = 3;
   __shared__ Route r;
-  __shared__ f32x4 part[2][2][kWaves][64];
-  route<Cols::kTokens>(a, r, blockIdx.x == 0);
+  __shared__ float part[2][kWaves][4][2][64];  // [turn][wave][operand][row of the lane's two][lane]
+  route<Vec::kTokens>(a, r, blockIdx.x + blockIdx.y == 0);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i = lane & 15, q = lane >> 4;
-  const int HB = f8_blocks(a.H), IB = f8_blocks(a.I), pieces = a.H / 16, per = a.I / 16;
-  const int steps = (HB + kWaves - 1) / kWaves, items = r.tiles * per;
-  const uint16_t* xs = TERMS == 1 ? static_cast<const uint16_t*>(a.x) : a.xt + (int64_t)Cols::term(i) * a.T * a.H;
-  const int64_t ld = TERMS == 1 ? a.ld_x : a.H;
+  const int HB = f8_blocks(a.H), IB = f8_blocks(a.I), pieces = a.H / 16, rb = blockIdx.x;
+  const int steps = (HB + kWaves - 1) / kWaves, own = 2 * q + (i & 1);  // own: piece of a block
+  const int tiles = r.tiles, zero = lane_zero();
+  if ((int)blockIdx.y >= tiles) return;
+  const uint16_t* xs = a.xt + (int64_t)Vec::term(i / 2) * a.T * a.Hp + own * 16;
+  const int row = (i / 2) * a.H, eight = kRows * a.H;  // within the item's 16 rows
+  const int c = Vec::token(i / 2);
 
   struct Unit {
-    f8i4 g[2], u[2];
-    bf16x8v x[4];
+    f8i4 w[4];  // gate's rows 0 - 7 and 8 - 15, up's
+    Values x;
     float sg, su;
   };
   // what the loads are at
-  int item = blockIdx.x, step = 0;
-  g_f8i4 *wg = nullptr, *wu = nullptr;
+  int tile = blockIdx.y, step = 0;
+  const uint8_t *wg = nullptr, *wu = nullptr;
   const uint16_t* x = nullptr;
   const float* s = nullptr;
   auto load = [&](Unit& f) {
-    if (item >= items) return;
     if (step == 0) {
-      const int tile = item / per, rb = item % per, e = r.tile_expert[tile], first = r.tile_first[tile];
-      const int tokens = min(Cols::kTokens, __popcll(r.mask[e]) - first);
-      wg = (g_f8i4*)(a.q_gu + ((int64_t)e * 2 * a.I + rb * 16 + i) * a.H);
-      wu = (g_f8i4*)(a.q_gu + ((int64_t)e * 2 * a.I + a.I + rb * 16 + i) * a.H);
-      s = a.s_gu + ((int64_t)e * 2 * IB + rb * 16 / kF8Block) * HB;
-      // columns past the tile's are the first one's again, and not stored
-      const int c = Cols::token(i);
-      x = xs + r.token[r.at[e] + first + (c < tokens ? c : 0)] * ld;
+      const Fp8Tile t = uniform(&r.tile[min(tile, tiles - 1)]);
+      wg = a.q_gu + ((int64_t)t.expert * 2 * a.I + rb * 16) * a.H;
+      wu = wg + (int64_t)a.I * a.H;
+      s = a.s_gu + ((int64_t)t.expert * 2 * IB + rb * 16 / kF8Block) * HB;
+      // vectors past the tile's are the first one's again, and not stored
+      x = xs + r.token[t.at + (c < t.tokens ? c : 0)] * a.Hp;
     }
-    const int b = min(wave + step * kWaves, HB - 1);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      f.g[h] = piece(wg, b * 8 + 4 * h + q, pieces);
-      f.u[h] = piece(wu, b * 8 + 4 * h + q, pieces);
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) values(x, b * 8 + 4 * h + q, pieces, f.x + 2 * h);
-    f.sg = s[b];
-    f.su = s[(int64_t)IB * HB + b];
+    const int b = min(wave + step * kWaves, HB - 1), at = row + 16 * min(b * 8 + own, pieces - 1);
+    f.w[0] = *(g_f8i4*)(wg + at);
+    f.w[1] = *(g_f8i4*)(wg + at + eight);
+    f.w[2] = *(g_f8i4*)(wu + at);
+    f.w[3] = *(g_f8i4*)(wu + at + eight);
+    f.x = load_values(x + b * kF8Block);
+    f.sg = s[b + zero];
+    f.su = s[IB * HB + b + zero];
     if (++step == steps) {
       step = 0;
-      item += gridDim.x;
+      tile += gridDim.y;
     }
   };
   // what the sums are at
-  int at = blockIdx.x, done = 0, turn = 0;
-  f32x4 gate = {0.f, 0.f, 0.f, 0.f}, up = gate;
-  auto products = [&](Unit& f) {
-    const int b = wave + done * kWaves;
-    if (b < HB) {
-      if (b * 8 + 8 > pieces) {  // K ends inside the block
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (b * 8 + 4 * h + q >= pieces) {
-            f.g[h] = f.u[h] = f8i4{0, 0, 0, 0};
-            f.x[2 * h] = f.x[2 * h + 1] = bf16x8v{};
-          }
-      }
-      const f32x4 pg = times(f.g, f.x), pu = times(f.u, f.x);
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        gate[v] = fmaf(f.sg, pg[v], gate[v]);
-        up[v] = fmaf(f.su, pu[v], up[v]);
-      }
+  int at = blockIdx.y, done = 0, turn = 0;
+  f32x4 sum[4] = {};
+  auto products = [&](const Unit& f) {
+    if (wave + done * kWaves < HB) {
+      add_products(f.w[0], f.x, f.sg, sum[0]);
+      add_products(f.w[1], f.x, f.sg, sum[1]);
+      add_products(f.w[2], f.x, f.su, sum[2]);
+      add_products(f.w[3], f.x, f.su, sum[3]);
     }
     if (++done < steps) return;
+    done = 0;
+    if (at >= tiles) return;
     // the item's sums meet; another buffer each time, so that one barrier does
-    if (TERMS > 1) {
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        gate[v] = add_terms(gate[v]);
-        up[v] = add_terms(up[v]);
-      }
+    for (int k = 0; k < 4; ++k) {
+      part[turn][wave][k][0][lane] = Vec::whole(of_parity(sum[k][0], sum[k][1]));
+      part[turn][wave][k][1][lane] = Vec::whole(of_parity(sum[k][2], sum[k][3]));
+      sum[k] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
-    part[turn][0][wave][lane] = gate;
-    part[turn][1][wave][lane] = up;
-    __syncthreads();
-    const int tile = at / per, rb = at % per, e = r.tile_expert[tile], first = r.tile_first[tile];
-    const int tokens = min(Cols::kTokens, __popcll(r.mask[e]) - first);
-    const int c = threadIdx.x / 16, j = threadIdx.x % 16;
-    if (c < tokens) {
-      const int column = TERMS == 1 ? c : 3 * c;
-      const float* p = reinterpret_cast<const float*>(&part[turn][0][0][16 * (j / 4) + column]) + j % 4;
-      float gs = 0.f, us = 0.f;
+    meet();
+    const Fp8Tile t = uniform(&r.tile[at]);
+    const int ct = threadIdx.x / 16, j = threadIdx.x % 16;
+    if (ct < t.tokens) {
+      const float* from = &part[turn][0][j / 8][j % 2][16 * (j % 8 / 2) + Vec::lane_of(ct)];
+      float g = 0.f, u = 0.f;
 #pragma unroll
       for (int k = 0; k < kWaves; ++k) {
-        gs += p[k * 64 * 4];
-        us += p[(kWaves + k) * 64 * 4];
+        g += from[k * 4 * 2 * 64];
+        u += from[k * 4 * 2 * 64 + 2 * 2 * 64];
       }
-      uint16_t t[3];
-      three_terms(gs / (1.f + expf(-gs)) * us, t);
-      const int64_t to = (int64_t)(r.at[e] + first + c) * a.I + rb * 16 + j, plane = (int64_t)a.T * a.k * a.I;
+      uint16_t v[3];
+      three_terms(g / (1.f + expf(-g)) * u, v);
+      uint16_t* to = a.h + (int64_t)(t.at + ct) * a.Ip + rb * 16 + j;
+      const int64_t plane = (int64_t)a.T * a.k * a.Ip;
 #pragma unroll
-      for (int k = 0; k < 3; ++k) a.h[k * plane + to] = t[k];
+      for (int k = 0; k < 3; ++k) to[k * plane] = v[k];
+      if (rb == (int)gridDim.x - 1)
+        for (int z = 16; rb * 16 + z < a.Ip; z += 16)
+#pragma unroll
+          for (int k = 0; k < 3; ++k) to[k * plane + z] = 0;
     }
-    gate = up = f32x4{0.f, 0.f, 0.f, 0.f};
-    done = 0;
     turn ^= 1;
-    at += gridDim.x;
+    at += gridDim.y;
   };
   Unit f[kAhead];
 #pragma unroll
   for (int k = 0; k < kAhead; ++k) load(f[k]);
-  while (at < items) {
+  while (at < tiles) {
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      if (at < items) {
-        products(f[k]);
-        load(f[k]);
-      }
+      products(f[k]);
+      load(f[k]);
     }
   }
 }
 
-// Second half: 16 rows of down x every token, over all experts. A wave's blocks of K over the
-// experts are one sequence, of which it has kAhead under way, with the first tile of the
-// expert's tokens. What a block gives a token is added, with the token's weight for the
-// expert, to the wave's sums in LDS; the waves' sums meet at the end.
-template <typename ACT>
-__global__ __launch_bounds__(64 * kWaves, 4) void k_f8_down(Fp8LayerArgs a) {
-  typedef Columns<3> Cols;
-  constexpr int kAhead = 3;
-  extern __shared__ __attribute__((aligned(16))) float sums[];  // [kWaves][T][16]
-  __shared__ Fp8Expert experts[kF8LayerExperts];
-  __shared__ float gates[kMaxAssign];
-  __shared__ uint8_t tokens[kMaxAssign];
+// Second half: 16 rows of down x every token, over all tiles. Waves are KS x NG: wave (s, g)
+// takes the blocks s, s + KS, ... of K of the tiles g, g + NG, ..., one sequence of which it has
+// kAhead under way. What they give an assignment goes to LDS, one place for each assignment
+// and s, and is added there with the assignments' weights in the order of the experts: so a
+// token's sums do not turn on which others there are. Where LDS does not hold all places, they
+// go in windows of `window`, which the last tile of one may run over.
+struct DownShape {
+  int ks, slots, window;
+};
+
+template <typename ACT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 4) void k_f8_down(Fp8LayerArgs a, DownShape d) {
+  typedef Vectors<3> Vec;
+  static_assert(Vec::kTokens == kDownTokens, "the tables' tiles");
+  constexpr int kAhead = 4, kOut = kF8LayerTokens * 16 / (64 * WAVES);  // kOut: outputs of a thread
+  extern __shared__ __attribute__((aligned(16))) float acc[];  // [ks][slots][16]
+  const int n = a.T * a.k;
+  Fp8Tile* tile = reinterpret_cast<Fp8Tile*>(acc + d.ks * d.slots * 16);
+  float* gates = reinterpret_cast<float*>(tile + n);
+  uint32_t* place = reinterpret_cast<uint32_t*>(gates + n);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i = lane & 15, q = lane >> 4;
   const int HB = f8_blocks(a.H), IB = f8_blocks(a.I), pieces = a.I / 16, n0 = blockIdx.x * 16;
-  const int n_experts = a.tables->experts;
-  for (int k = threadIdx.x; k < n_experts; k += 64 * kWaves) experts[k] = a.tables->expert[k];
-  for (int k = threadIdx.x; k < a.T * a.k; k += 64 * kWaves) {
+  for (int k = threadIdx.x; k < n; k += 64 * WAVES) {
+    tile[k] = a.tables->tile[k];
     gates[k] = a.tables->gate[k];
-    tokens[k] = a.tables->token[k];
+    place[k] = a.tables->place[k];
   }
-  for (int k = threadIdx.x; k < kWaves * a.T * 16; k += 64 * kWaves) sums[k] = 0.f;
+  const int tiles = __builtin_amdgcn_readfirstlane(a.tables->tiles), places = __builtin_amdgcn_readfirstlane(a.tables->places);
   __syncthreads();
-  const int steps = (IB + kWaves - 1) / kWaves;
-  const uint16_t* hs = a.h + (int64_t)Cols::term(i) * a.T * a.k * a.I;
-  const int c = Cols::token(i);
+  const int ks = wave % d.ks, g = wave / d.ks, groups = WAVES / d.ks, steps = (IB + d.ks - 1) / d.ks;
+  const int own = 2 * q + (i & 1), c = Vec::token(i / 2), zero = lane_zero();  // own: piece of a block
+  const uint16_t* hs = a.h + (int64_t)Vec::term(i / 2) * n * a.Ip + own * 16;
+  const int row = (i / 2) * a.I, eight = kRows * a.I;  // within the 16 rows
 
   struct Unit {
     f8i4 w[2];
-    bf16x8v h[4];
+    Values h;
     float s;
   };
-  auto load_h = [&](bf16x8v* h, const Fp8Expert& e, int first, int b) {
-    // columns past the tile's are the first one's again, and not used
-    const uint16_t* row = hs + (int64_t)(e.at + first + (first + c < e.count ? c : 0)) * a.I;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) values(row, b * 8 + 4 * k + q, pieces, h + 2 * k);
-  };
-  int n = 0, step = 0;
-  auto load = [&](Unit& f) {
-    if (n >= n_experts) return;
-    const Fp8Expert e = experts[n];
-    const int b = min(wave + step * kWaves, IB - 1);
-    g_f8i4* w = (g_f8i4*)(a.q_dn + ((int64_t)e.expert * a.H + n0 + i) * a.I);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) f.w[k] = piece(w, b * 8 + 4 * k + q, pieces);
-    load_h(f.h, e, 0, b);
-    f.s = a.s_dn[((int64_t)e.expert * HB + n0 / kF8Block) * IB + b];
-    if (++step == steps) {
-      step = 0;
-      ++n;
-    }
-  };
-  int at = 0, done = 0;
-  auto products = [&](Unit& f) {
-    const int b = wave + done * kWaves;
-    const Fp8Expert e = experts[at];
-    if (b < IB) {
-      const bool ends = b * 8 + 8 > pieces;  // K ends inside the block
-      if (ends) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          if (b * 8 + 4 * k + q >= pieces) f.w[k] = f8i4{0, 0, 0, 0};
+  float y[kOut] = {};
+  int end = 0;
+  for (int base = 0; base < places; base += d.window) {
+    const int begin = end;  // the window's tiles
+    end = tiles;
+    if (base + d.window < places) {
+      int lo = begin;
+      while (lo < end) {  // the first tile past the window
+        const int mid = (lo + end) / 2;
+        if (tile[mid].at < base + d.window)
+          lo = mid + 1;
+        else
+          end = mid;
       }
-      for (int first = 0; first < e.count; first += Cols::kTokens) {
-        if (first > 0) load_h(f.h, e, first, b);
-        if (ends) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            if (b * 8 + 4 * k + q >= pieces) f.h[2 * k] = f.h[2 * k + 1] = bf16x8v{};
-        }
-        f32x4 sum = times(f.w, f.h);
-#pragma unroll
-        for (int v = 0; v < 4; ++v) sum[v] = add_terms(sum[v]);
-        if (Cols::term(i) == 0 && first + c < e.count && c < Cols::kTokens) {
-          const float scale = gates[e.at + first + c] * f.s;
-          f32x4* to = reinterpret_cast<f32x4*>(&sums[(wave * a.T + tokens[e.at + first + c]) * 16 + 4 * q]);
-          f32x4 v = *to;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] = fmaf(scale, sum[k], v[k]);
-          *to = v;
-        }
-      }
+      end = __builtin_amdgcn_readfirstlane(end);
     }
-    if (++done == steps) {
+    int next = begin + g, step = 0;  // what the loads are at
+    const uint8_t* w = nullptr;
+    const uint16_t* h = nullptr;
+    const float* s = nullptr;
+    auto load = [&](Unit& f) {
+      if (step == 0) {
+        const Fp8Tile t = uniform(&tile[min(next, tiles - 1)]);
+        w = a.q_dn + ((int64_t)t.expert * a.H + n0) * a.I;
+        s = a.s_dn + ((int64_t)t.expert * HB + n0 / kF8Block) * IB;
+        // vectors past the tile's are the first one's again, and not used
+        h = hs + (t.at + (c < t.tokens ? c : 0)) * (int64_t)a.Ip;
+      }
+      const int b = min(ks + step * d.ks, IB - 1), at = row + 16 * min(b * 8 + own, pieces - 1);
+      f.w[0] = *(g_f8i4*)(w + at);
+      f.w[1] = *(g_f8i4*)(w + at + eight);
+      f.h = load_values(h + b * kF8Block);
+      f.s = s[b + zero];
+      if (++step == steps) {
+        step = 0;
+        next += groups;
+      }
+    };
+    int at = begin + g, done = 0;  // what the sums are at
+    f32x4 sum[2] = {};             // rows 2 q, 2 q + 1 of the first eight, of the others
+    auto products = [&](const Unit& f) {
+      if (ks + done * d.ks < IB) {
+        add_products(f.w[0], f.h, f.s, sum[0]);
+        add_products(f.w[1], f.h, f.s, sum[1]);
+      }
+      if (++done < steps) return;
       done = 0;
-      ++at;
-    }
-  };
-  Unit f[kAhead];
+      if (at >= end) return;
+      const Fp8Tile t = uniform(&tile[at]);
+      float v[4];
 #pragma unroll
-  for (int k = 0; k < kAhead; ++k) load(f[k]);
-  while (at < n_experts) {
+      for (int k = 0; k < 2; ++k) {
+        v[2 * k] = Vec::whole(of_parity(sum[k][0], sum[k][1]));
+        v[2 * k + 1] = Vec::whole(of_parity(sum[k][2], sum[k][3]));
+        sum[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+      if (Vec::is_first(i) && c < t.tokens) {
+        float* to = &acc[(ks * d.slots + t.at + c - base) * 16 + 2 * q];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      if (at < n_experts) {
+        for (int k = 0; k < 4; ++k) to[k % 2 + k / 2 * 8] = v[k];
+      }
+      at += groups;
+    };
+    Unit f[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) load(f[k]);
+    while (at < end) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
         products(f[k]);
         load(f[k]);
       }
     }
-  }
-  __syncthreads();
-  for (int o = threadIdx.x; o < 16 * a.T; o += 64 * kWaves) {
-    const int t = o / 16, col = n0 + o % 16;
-    float v = 0.f;
+    meet();
 #pragma unroll
-    for (int k = 0; k < kWaves; ++k) v += sums[k * a.T * 16 + o];
-    a.y[t * a.ld_y + col] = v;
+    for (int o = 0; o < kOut; ++o) {
+      const int out = threadIdx.x + o * 64 * WAVES, t = out / 16, r = out % 16;
+      if (t >= a.T) break;
+      for (int j = 0; j < a.k; ++j) {
+        const int p = place[t * a.k + j] & 0xFFFF, first = place[t * a.k + j] >> 16;
+        if (first < base || first >= base + d.window) continue;
+        float v = 0.f;
+        for (int k = 0; k < d.ks; ++k) v += acc[(k * d.slots + p - base) * 16 + r];
+        y[o] = fmaf(gates[p], v, y[o]);
+      }
+    }
+    meet();
+  }
+#pragma unroll
+  for (int o = 0; o < kOut; ++o) {
+    const int out = threadIdx.x + o * 64 * WAVES, t = out / 16, col = n0 + out % 16;
+    if (t >= a.T) break;
+    a.y[t * a.ld_y + col] = y[o];
     if (a.x_out) {
       typedef OutElem<sizeof(ACT) == 2> Out;
-      const float x = Out::load(static_cast<const ACT*>(a.x)[t * a.ld_x + col]) + v;
+      const float x = Out::load(static_cast<const ACT*>(a.x)[t * a.ld_x + col]) + y[o];
       static_cast<ACT*>(a.x_out)[t * a.ld_x_out + col] = Out::rounded(x);
     }
   }
 }
 
+template <typename ACT, int WAVES>
+void down(const Fp8LayerArgs& a, hipStream_t s) {
+  const int IB = f8_blocks(a.I), n = a.T * a.k;
+  // as many parts of K as divide its blocks with little left over: the fewer tiles have to be at
+  // hand for every wave to have work
+  int ks = 1;
+  for (int p = 2; p <= WAVES && p <= IB; p *= 2)
+    if ((IB + p - 1) / p * p * 7 <= IB * 8) ks = p;
+  constexpr int kRoom = WAVES == 8 ? 48 << 10 : 96 << 10;  // LDS for the sums: two workgroups a CU, or one
+  const int room = kRoom / (ks * 16 * (int)sizeof(float));
+  DownShape d;
+  d.ks = ks;
+  d.slots = std::min(n, room);
+  d.window = n <= room ? n : room - (kDownTokens - 1);
+  const size_t lds = sizeof(float) * 16 * ks * d.slots + (sizeof(Fp8Tile) + sizeof(float) + sizeof(uint32_t)) * n;
+  hipLaunchKernelGGL((k_f8_down<ACT, WAVES>), dim3(a.H / 16), dim3(64 * WAVES), lds, s, a, d);
+}
+
 template <typename ACT>
 void layer(const Fp8LayerArgs& a, hipStream_t s) {
   constexpr int kTerms = sizeof(ACT) == 2 ? 1 : 3;
-  const int rows = a.logits_in ? 0 : a.E, more = a.logits_in || kTerms == 3 ? a.T : 0;
-  hipLaunchKernelGGL((k_f8_router<ACT>), dim3(rows + more), dim3(kRouterThreads), 0, s, a, rows);
-  const int64_t items = (int64_t)a.T * a.k * (a.I / 16);
-  hipLaunchKernelGGL((k_f8_gate_up<kTerms>), dim3((unsigned)std::min<int64_t>(items, 512)), dim3(64 * kWaves), 0, s, a);
-  hipLaunchKernelGGL((k_f8_down<ACT>), dim3(a.H / 16), dim3(64 * kWaves), sizeof(float) * kWaves * 16 * a.T, s, a);
+  const int rows = a.logits_in ? 0 : a.E;
+  hipLaunchKernelGGL((k_f8_router<ACT>), dim3(rows + a.T), dim3(kRouterThreads), 0, s, a, rows);
+  const int per = a.I / 16, most = a.T * a.k;  // blocks of rows; tiles
+  hipLaunchKernelGGL((k_f8_gate_up<kTerms>), dim3(per, std::min(most, std::max(1, 512 / per))), dim3(64 * kWaves), 0, s, a);
+  if (a.H / 16 <= 256)
+    down<ACT, 16>(a, s);
+  else
+    down<ACT, 8>(a, s);
 }
 
 }  // namespace
