@@ -157,49 +157,57 @@ __device__ __forceinline__ uint32_t logit_key(float f) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+__device__ __forceinline__ float logit_of(uint32_t key) {
+  if (key == ~0u) return __uint_as_float(0x7FC00000u);
+  return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
+}
+
 // The k experts of one token by one wave: k rounds of the wave's maximum and the lowest
-// expert that has it. Lane l holds experts l, l + 64, ...; lane j ends with slot j.
+// expert that has it. Lane l holds experts l, l + 64, ...; lane j ends with slot j, and its
+// rank among the token's experts of any weight.
 template <int NV>
-__device__ __forceinline__ void choose(const float* logits, int E, int k, int& id, float& w, int& rank) {
+__device__ __forceinline__ void choose_of(const float* logits, int E, int k, int& id, float& w, int& rank) {
   const int lane = threadIdx.x & 63;
-  float f[NV];
   uint32_t key[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    f[i] = logits[min(lane + 64 * i, E - 1)];
-    key[i] = lane + 64 * i < E ? logit_key(f[i]) : 0u;
+    const float f = logits[min(lane + 64 * i, E - 1)];
+    key[i] = lane + 64 * i < E ? logit_key(f) : 0u;
   }
-  float mine = 0.f;
+  uint32_t mine = 0u;
   id = 0;
   for (int j = 0; j < k; ++j) {
     uint32_t m = key[0];
 #pragma unroll
     for (int i = 1; i < NV; ++i) m = max(m, key[i]);
     m = wave_max_u(m);
-    int win = -1;
-    float v = 0.f;
+    int win = 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
+    for (int i = NV - 1; i >= 0; --i) {
       const unsigned long long b = __ballot(key[i] == m);
-      if (win < 0 && b != 0ull) {
-        win = 64 * i + (int)__builtin_ctzll(b);
-        v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(f[i]), win & 63));
-        if ((win & 63) == lane) key[i] = 0u;
-      }
+      win = b != 0ull ? 64 * i + (int)__builtin_ctzll(b) : win;
     }
-    mine = lane == j ? v : mine;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) key[i] = lane + 64 * i == win ? 0u : key[i];
+    mine = lane == j ? m : mine;
     id = lane == j ? win : id;
   }
-  const float top = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine), 0));
-  const float p = lane < k && mine != -INFINITY ? expf(mine - top) : 0.f;
+  const float v = logit_of(mine), top = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 0));
+  const float p = lane < k && v != -INFINITY ? expf(v - top) : 0.f;
   const float sum = wave_sum(p);
   w = sum == 0.f ? 0.f : p / sum;  // every logit -infinity: nothing
-  rank = 0;  // among the token's experts of any weight
-  for (int j = 0; j < k; ++j) {
-    const int other = __builtin_amdgcn_readlane(id, j);
-    const float wo = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w), j));
-    rank += wo != 0.f && other < id;
-  }
+  const uint64_t some = __ballot(w != 0.f);
+  rank = 0;
+  for (int j = 0; j < k; ++j) rank += (some >> j & 1) && __builtin_amdgcn_readlane(id, j) < id;
+}
+__device__ __forceinline__ void choose(const float* logits, int E, int k, int& id, float& w, int& rank) {
+  const int nv = (E + 63) / 64;
+  if (nv <= 2)
+    choose_of<2>(logits, E, k, id, w, rank);
+  else if (nv <= 6)
+    choose_of<6>(logits, E, k, id, w, rank);
+  else
+    choose_of<16>(logits, E, k, id, w, rank);
 }
 
 // Tiles of up to TILE tokens for this launch; the workgroup that `writes` also leaves the outputs,
@@ -208,20 +216,41 @@ template <int TILE>
 __device__ __forceinline__ void route(const Fp8LayerArgs& a, Route& r, bool writes) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   const float* logits = a.logits ? a.logits : a.logits_in;
+  if (a.T == 1) {  // a token's experts are its tiles: no grouping (route of 2048 / 128 / 8: 2.5 us, 3.8 with it)
+    if (wave == 0) {
+      int id, rank;
+      float w;
+      choose(logits, a.E, a.k, id, w, rank);
+      const bool is = lane < a.k && w != 0.f;
+      const int n = __popcll(__ballot(is));
+      if (is) {
+        r.tile[rank] = Fp8Tile{(uint16_t)id, (uint16_t)rank, 1, 0};
+        r.token[rank] = 0;
+      }
+      if (lane == 0) r.tiles = n;
+      if (writes) {
+        if (is) {
+          a.tables->tile[rank] = Fp8Tile{(uint16_t)id, (uint16_t)rank, 1, 0};
+          a.tables->gate[rank] = w;
+        }
+        if (lane < a.k) {
+          a.tables->place[lane] = lane < n ? (uint32_t)lane | (uint32_t)lane << 16 : kF8NoPlace;
+          if (a.ids) a.ids[lane] = id;
+          if (a.gate) a.gate[lane] = w;
+        }
+        if (lane == 0) a.tables->tiles = a.tables->places = n;
+      }
+    }
+    __syncthreads();
+    return;
+  }
   uint32_t* slot = reinterpret_cast<uint32_t*>(r.tile);  // id and rank of an assignment, until the tiles are made
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) r.mask[e] = 0;
   __syncthreads();
   for (int t = wave; t < a.T; t += waves) {
     int id, rank;
     float w;
-    const float* row = logits + (int64_t)t * a.E;
-    const int nv = (a.E + 63) / 64;
-    if (nv <= 2)
-      choose<2>(row, a.E, a.k, id, w, rank);
-    else if (nv <= 6)
-      choose<6>(row, a.E, a.k, id, w, rank);
-    else
-      choose<16>(row, a.E, a.k, id, w, rank);
+    choose(logits + (int64_t)t * a.E, a.E, a.k, id, w, rank);
     if (lane < a.k) {
       const int s = t * a.k + lane;
       if (w != 0.f) atomicOr(reinterpret_cast<unsigned long long*>(&r.mask[id]), 1ull << t);
@@ -331,10 +360,18 @@ __device__ __forceinline__ int lane_zero() {
 struct Values {
   bf16x8v v[2];
 };
-__device__ __forceinline__ Values load_values(const uint16_t* at) {
-  typedef __attribute__((address_space(1))) const bf16x8v g_bf16x8;
-  return Values{{((g_bf16x8*)at)[0], ((g_bf16x8*)at)[1]}};
+__device__ __forceinline__ Values load_values(__amdgpu_buffer_rsrc_t from, uint32_t at) {
+  return Values{{__builtin_bit_cast(bf16x8v, __builtin_amdgcn_raw_buffer_load_b128(from, at, 0, 0)),
+                 __builtin_bit_cast(bf16x8v, __builtin_amdgcn_raw_buffer_load_b128(from, at + 16, 0, 0))}};
 }
+// The workspace's bf16 values as a buffer of under 2^30 bytes: a lane whose vector is none reads past its
+// end, which gives zeros and asks no memory for anything. (Vectors that repeat another's instead
+// take as much of the CU's room for loads under way as the weights do: 128 CUs then stream
+// 2.8 TB/s of weights, and 5.5 without vectors.)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t values_buffer(const uint16_t* p, int64_t n) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p), 0, (uint32_t)(2 * n), 0x00020000);
+}
+constexpr uint32_t kNoVector = 1u << 30;
 
 // The sums of 8 rows with a block's values, all parities: added, scaled, to s.
 __device__ __forceinline__ void add_products(const f8i4& w, const Values& x, float scale, f32x4& s) {
@@ -360,10 +397,9 @@ __device__ __forceinline__ void meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts
 // its items are one sequence, of which it has kAhead under way. Every turn loads, past the
 // end the last tile's again: a load that a branch leaves out would make every wait one for
 // all loads.
-template <int TERMS>
+template <int TERMS, int kAhead>
 __global__ __launch_bounds__(64 * kWaves, 4) void k_f8_gate_up(Fp8LayerArgs a) {
   typedef Vectors<TERMS> Vec;
-  constexpr int kAhead = 3;
   __shared__ Route r;
   __shared__ float part[2][kWaves][4][2][64];  // [turn][wave][operand][row of the lane's two][lane]
   route<Vec::kTokens>(a, r, blockIdx.x + blockIdx.y == 0);
@@ -372,7 +408,8 @@ __global__ __launch_bounds__(64 * kWaves, 4) void k_f8_gate_up(Fp8LayerArgs a) {
   const int steps = (HB + kWaves - 1) / kWaves, own = 2 * q + (i & 1);  // own: piece of a block
   const int tiles = r.tiles, zero = lane_zero();
   if ((int)blockIdx.y >= tiles) return;
-  const uint16_t* xs = a.xt + (int64_t)Vec::term(i / 2) * a.T * a.Hp + own * 16;
+  const __amdgpu_buffer_rsrc_t xs = values_buffer(a.xt, (int64_t)TERMS * a.T * a.Hp);
+  const uint32_t own_x = 2 * (Vec::term(i / 2) * a.T * a.Hp + own * 16);
   const int row = (i / 2) * a.H, eight = kRows * a.H;  // within the item's 16 rows
   const int c = Vec::token(i / 2);
 
@@ -384,7 +421,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void k_f8_gate_up(Fp8LayerArgs a) {
   // what the loads are at
   int tile = blockIdx.y, step = 0;
   const uint8_t *wg = nullptr, *wu = nullptr;
-  const uint16_t* x = nullptr;
+  uint32_t x = 0;
   const float* s = nullptr;
   auto load = [&](Unit& f) {
     if (step == 0) {
@@ -392,15 +429,14 @@ __global__ __launch_bounds__(64 * kWaves, 4) void k_f8_gate_up(Fp8LayerArgs a) {
       wg = a.q_gu + ((int64_t)t.expert * 2 * a.I + rb * 16) * a.H;
       wu = wg + (int64_t)a.I * a.H;
       s = a.s_gu + ((int64_t)t.expert * 2 * IB + rb * 16 / kF8Block) * HB;
-      // vectors past the tile's are the first one's again, and not stored
-      x = xs + r.token[t.at + (c < t.tokens ? c : 0)] * a.Hp;
+      x = c < t.tokens ? own_x + 2 * r.token[t.at + c] * a.Hp : kNoVector;
     }
     const int b = min(wave + step * kWaves, HB - 1), at = row + 16 * min(b * 8 + own, pieces - 1);
     f.w[0] = *(g_f8i4*)(wg + at);
     f.w[1] = *(g_f8i4*)(wg + at + eight);
     f.w[2] = *(g_f8i4*)(wu + at);
     f.w[3] = *(g_f8i4*)(wu + at + eight);
-    f.x = load_values(x + b * kF8Block);
+    f.x = load_values(xs, x + 2 * b * kF8Block);
     f.sg = s[b + zero];
     f.su = s[IB * HB + b + zero];
     if (++step == steps) {
@@ -465,7 +501,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void k_f8_gate_up(Fp8LayerArgs a) {
   }
 }
 
-// Second half: 16 rows of down x every token, over all tiles. Waves are KS x NG: wave (s, g)
+// Second half: 8 OPS rows of down x every token, over all tiles. Waves are KS x NG: wave (s, g)
 // takes the blocks s, s + KS, ... of K of the tiles g, g + NG, ..., one sequence of which it has
 // kAhead under way. What they give an assignment goes to LDS, one place for each assignment
 // and s, and is added there with the assignments' weights in the order of the experts: so a
@@ -475,18 +511,19 @@ struct DownShape {
   int ks, slots, window;
 };
 
-template <typename ACT, int WAVES>
+template <typename ACT, int WAVES, int OPS, int kAhead>
 __global__ __launch_bounds__(64 * WAVES, 4) void k_f8_down(Fp8LayerArgs a, DownShape d) {
   typedef Vectors<3> Vec;
   static_assert(Vec::kTokens == kDownTokens, "the tables' tiles");
-  constexpr int kAhead = 4, kOut = kF8LayerTokens * 16 / (64 * WAVES);  // kOut: outputs of a thread
-  extern __shared__ __attribute__((aligned(16))) float acc[];  // [ks][slots][16]
+  constexpr int kOf = kRows * OPS;                                     // rows of the workgroup
+  constexpr int kOut = (kF8LayerTokens * kOf - 1) / (64 * WAVES) + 1;  // outputs of a thread
+  extern __shared__ __attribute__((aligned(16))) float acc[];  // [ks][slots][kOf]
   const int n = a.T * a.k;
-  Fp8Tile* tile = reinterpret_cast<Fp8Tile*>(acc + d.ks * d.slots * 16);
+  Fp8Tile* tile = reinterpret_cast<Fp8Tile*>(acc + d.ks * d.slots * kOf);
   float* gates = reinterpret_cast<float*>(tile + n);
   uint32_t* place = reinterpret_cast<uint32_t*>(gates + n);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i = lane & 15, q = lane >> 4;
-  const int HB = f8_blocks(a.H), IB = f8_blocks(a.I), pieces = a.I / 16, n0 = blockIdx.x * 16;
+  const int HB = f8_blocks(a.H), IB = f8_blocks(a.I), pieces = a.I / 16, n0 = blockIdx.x * kOf;
   for (int k = threadIdx.x; k < n; k += 64 * WAVES) {
     tile[k] = a.tables->tile[k];
     gates[k] = a.tables->gate[k];
@@ -496,11 +533,12 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_f8_down(Fp8LayerArgs a, DownS
   __syncthreads();
   const int ks = wave % d.ks, g = wave / d.ks, groups = WAVES / d.ks, steps = (IB + d.ks - 1) / d.ks;
   const int own = 2 * q + (i & 1), c = Vec::token(i / 2), zero = lane_zero();  // own: piece of a block
-  const uint16_t* hs = a.h + (int64_t)Vec::term(i / 2) * n * a.Ip + own * 16;
-  const int row = (i / 2) * a.I, eight = kRows * a.I;  // within the 16 rows
+  const __amdgpu_buffer_rsrc_t hs = values_buffer(a.h, (int64_t)3 * n * a.Ip);
+  const uint32_t own_h = 2 * (Vec::term(i / 2) * n * a.Ip + own * 16);
+  const int row = (i / 2) * a.I;  // within eight rows
 
   struct Unit {
-    f8i4 w[2];
+    f8i4 w[OPS];
     Values h;
     float s;
   };
@@ -522,20 +560,19 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_f8_down(Fp8LayerArgs a, DownS
     }
     int next = begin + g, step = 0;  // what the loads are at
     const uint8_t* w = nullptr;
-    const uint16_t* h = nullptr;
+    uint32_t h = 0;
     const float* s = nullptr;
     auto load = [&](Unit& f) {
       if (step == 0) {
         const Fp8Tile t = uniform(&tile[min(next, tiles - 1)]);
         w = a.q_dn + ((int64_t)t.expert * a.H + n0) * a.I;
         s = a.s_dn + ((int64_t)t.expert * HB + n0 / kF8Block) * IB;
-        // vectors past the tile's are the first one's again, and not used
-        h = hs + (t.at + (c < t.tokens ? c : 0)) * (int64_t)a.Ip;
+        h = c < t.tokens ? own_h + 2 * (t.at + c) * a.Ip : kNoVector;
       }
       const int b = min(ks + step * d.ks, IB - 1), at = row + 16 * min(b * 8 + own, pieces - 1);
-      f.w[0] = *(g_f8i4*)(w + at);
-      f.w[1] = *(g_f8i4*)(w + at + eight);
-      f.h = load_values(h + b * kF8Block);
+#pragma unroll
+      for (int k = 0; k < OPS; ++k) f.w[k] = *(g_f8i4*)(w + at + k * kRows * a.I);
+      f.h = load_values(hs, h + 2 * b * kF8Block);
       f.s = s[b + zero];
       if (++step == steps) {
         step = 0;
@@ -543,27 +580,25 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_f8_down(Fp8LayerArgs a, DownS
       }
     };
     int at = begin + g, done = 0;  // what the sums are at
-    f32x4 sum[2] = {};             // rows 2 q, 2 q + 1 of the first eight, of the others
+    f32x4 sum[OPS] = {};           // rows 2 q and 2 q + 1 of each eight
     auto products = [&](const Unit& f) {
       if (ks + done * d.ks < IB) {
-        add_products(f.w[0], f.h, f.s, sum[0]);
-        add_products(f.w[1], f.h, f.s, sum[1]);
+#pragma unroll
+        for (int k = 0; k < OPS; ++k) add_products(f.w[k], f.h, f.s, sum[k]);
       }
       if (++done < steps) return;
       done = 0;
       if (at >= end) return;
       const Fp8Tile t = uniform(&tile[at]);
-      float v[4];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        v[2 * k] = Vec::whole(of_parity(sum[k][0], sum[k][1]));
-        v[2 * k + 1] = Vec::whole(of_parity(sum[k][2], sum[k][3]));
+      for (int k = 0; k < OPS; ++k) {
+        const float v0 = Vec::whole(of_parity(sum[k][0], sum[k][1])), v1 = Vec::whole(of_parity(sum[k][2], sum[k][3]));
         sum[k] = f32x4{0.f, 0.f, 0.f, 0.f};
-      }
-      if (Vec::is_first(i) && c < t.tokens) {
-        float* to = &acc[(ks * d.slots + t.at + c - base) * 16 + 2 * q];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) to[k % 2 + k / 2 * 8] = v[k];
+        if (Vec::is_first(i) && c < t.tokens) {
+          float* to = &acc[(ks * d.slots + t.at + c - base) * kOf + 8 * k + 2 * q];
+          to[0] = v0;
+          to[1] = v1;
+        }
       }
       at += groups;
     };
@@ -580,21 +615,34 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_f8_down(Fp8LayerArgs a, DownS
     meet();
 #pragma unroll
     for (int o = 0; o < kOut; ++o) {
-      const int out = threadIdx.x + o * 64 * WAVES, t = out / 16, r = out % 16;
+      const int out = threadIdx.x + o * 64 * WAVES, t = out / kOf, r = out % kOf;
       if (t >= a.T) break;
-      for (int j = 0; j < a.k; ++j) {
-        const int p = place[t * a.k + j] & 0xFFFF, first = place[t * a.k + j] >> 16;
-        if (first < base || first >= base + d.window) continue;
-        float v = 0.f;
-        for (int k = 0; k < d.ks; ++k) v += acc[(k * d.slots + p - base) * 16 + r];
-        y[o] = fmaf(gates[p], v, y[o]);
+      constexpr int kAt = 4;  // assignments at once
+      for (int j = 0; j < a.k; j += kAt) {
+        const float* from[kAt];
+        float gate[kAt], v[kAt];
+        bool is[kAt];
+#pragma unroll
+        for (int u = 0; u < kAt; ++u) {
+          const uint32_t at = place[t * a.k + min(j + u, a.k - 1)];
+          const int p = at & 0xFFFF, first = at >> 16;
+          is[u] = j + u < a.k && first >= base && first < base + d.window;
+          from[u] = acc + (is[u] ? p - base : 0) * kOf + r;
+          gate[u] = gates[is[u] ? p : 0];
+          v[u] = 0.f;
+        }
+        for (int k = 0; k < d.ks; ++k)
+#pragma unroll
+          for (int u = 0; u < kAt; ++u) v[u] += from[u][k * d.slots * kOf];
+#pragma unroll
+        for (int u = 0; u < kAt; ++u) y[o] = is[u] ? fmaf(gate[u], v[u], y[o]) : y[o];
       }
     }
     meet();
   }
 #pragma unroll
   for (int o = 0; o < kOut; ++o) {
-    const int out = threadIdx.x + o * 64 * WAVES, t = out / 16, col = n0 + out % 16;
+    const int out = threadIdx.x + o * 64 * WAVES, t = out / kOf, col = n0 + out % kOf;
     if (t >= a.T) break;
     a.y[t * a.ld_y + col] = y[o];
     if (a.x_out) {
@@ -605,7 +653,7 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_f8_down(Fp8LayerArgs a, DownS
   }
 }
 
-template <typename ACT, int WAVES>
+template <typename ACT, int WAVES, int OPS>
 void down(const Fp8LayerArgs& a, hipStream_t s) {
   const int IB = f8_blocks(a.I), n = a.T * a.k;
   // as many parts of K as divide its blocks with little left over: the fewer tiles have to be at
@@ -614,13 +662,20 @@ void down(const Fp8LayerArgs& a, hipStream_t s) {
   for (int p = 2; p <= WAVES && p <= IB; p *= 2)
     if ((IB + p - 1) / p * p * 7 <= IB * 8) ks = p;
   constexpr int kRoom = WAVES == 8 ? 48 << 10 : 96 << 10;  // LDS for the sums: two workgroups a CU, or one
-  const int room = kRoom / (ks * 16 * (int)sizeof(float));
+  const int place = kRows * OPS * (int)sizeof(float), room = kRoom / (ks * place);
   DownShape d;
   d.ks = ks;
   d.slots = std::min(n, room);
   d.window = n <= room ? n : room - (kDownTokens - 1);
-  const size_t lds = sizeof(float) * 16 * ks * d.slots + (sizeof(Fp8Tile) + sizeof(float) + sizeof(uint32_t)) * n;
-  hipLaunchKernelGGL((k_f8_down<ACT, WAVES>), dim3(a.H / 16), dim3(64 * WAVES), lds, s, a, d);
+  const size_t lds = (size_t)ks * d.slots * place + (sizeof(Fp8Tile) + sizeof(float) + sizeof(uint32_t)) * n;
+  const int groups = WAVES / ks, most = ((n - 1) / groups + 1) * ((IB - 1) / ks + 1);  // blocks of K of a wave
+#define DOWN(AHEAD) \
+  hipLaunchKernelGGL((k_f8_down<ACT, WAVES, OPS, AHEAD>), dim3(a.H / (kRows * OPS)), dim3(64 * WAVES), lds, s, a, d)
+  if (most <= 3)
+    DOWN(3);
+  else
+    DOWN(OPS == 1 ? 6 : 4);
+#undef DOWN
 }
 
 template <typename ACT>
@@ -629,11 +684,15 @@ void layer(const Fp8LayerArgs& a, hipStream_t s) {
   const int rows = a.logits_in ? 0 : a.E;
   hipLaunchKernelGGL((k_f8_router<ACT>), dim3(rows + a.T), dim3(kRouterThreads), 0, s, a, rows);
   const int per = a.I / 16, most = a.T * a.k;  // blocks of rows; tiles
-  hipLaunchKernelGGL((k_f8_gate_up<kTerms>), dim3(per, std::min(most, std::max(1, 512 / per))), dim3(64 * kWaves), 0, s, a);
-  if (a.H / 16 <= 256)
-    down<ACT, 16>(a, s);
+  const dim3 grid(per, std::min(most, std::max(1, 512 / per)));
+  if (f8_blocks(a.H) <= 2 * kWaves && (int)grid.y == most)  // two blocks of K a wave at most
+    hipLaunchKernelGGL((k_f8_gate_up<kTerms, 2>), grid, dim3(64 * kWaves), 0, s, a);
   else
-    down<ACT, 8>(a, s);
+    hipLaunchKernelGGL((k_f8_gate_up<kTerms, 3>), grid, dim3(64 * kWaves), 0, s, a);
+  if (a.H / 16 <= 256)
+    down<ACT, 16, 1>(a, s);
+  else
+    down<ACT, 8, 2>(a, s);
 }
 
 }  // namespace
