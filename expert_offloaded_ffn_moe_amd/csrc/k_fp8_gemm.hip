@@ -1,5 +1,26 @@
-// Product of e4m3 codes with a scale for each block of 128, for many tokens: tiles of
-// 64 x 64, a wave 32 x 32 of them, through one pair of LDS buffers a block of 128 of K.
+// Product of e4m3 codes with a scale for each block of 128, for many tokens: tiles of tokens x
+// channels through a ring of LDS buffers, a block of 128 of K a step.
+//
+//   out[t][n] = sum_b (sx[t][b] sw[n / 128][b]) sum_{k in b} x[t][k] w[n][k] + ...
+//
+// Tokens are the row operand and channels the column operand of a 16 x 16 MFMA, so a lane
+// receives the sums of column l % 16 and rows 4 (l / 16) .. + 3. A block's sum starts from zero and
+// is added to the tile's with its scales, 4 multiply-adds for each 16 x 16 x 128 product, beside
+// which the matrix pipe goes on.
+//
+// bf16 outputs take v_mfma_f32_16x16x128_f8f6f4 on the codes themselves, 32 of a row a lane. It
+// adds eight neighbouring products at a time, each cut to 2^-13 of the binade of the largest
+// (measured with one large product beside small ones; 1.5e-5 of the sum on normal codes, 2^-13 of
+// the sum of sizes on codes of every size alike), and those sums in fp32. The output's own
+// rounding of 2^-8 covers it; the bf16 MFMA, on which the products are exact, has half of its
+// rate and its operands have to be converted first. fp32 outputs take that one, four steps of
+// 32 a block.
+//
+// LDS holds rows of 128 bytes, whose 16-byte pieces stand at places piece ^ (row / 2 % 8), so that
+// the lanes that a read serves at once use every bank once; loads go from memory to LDS
+// directly, in lane order, so that each lane fetches the piece that belongs at its place. Lane
+// quarter q reads pieces q and 4 + q of both operands. Pieces past K come from a line of
+// zeros. A step's scales follow the same way: a wave's part of the rows' and its channels' one.
 #include <hip/hip_runtime.h>
 
 #include "f8_dev.h"
@@ -9,71 +30,359 @@
 namespace moe {
 namespace {
 
-constexpr int kTile = 64;
+typedef __attribute__((address_space(3))) void lvoid;
+typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 
-template <bool BF16>
-__global__ __launch_bounds__(256) void k_fp8_gemm(Fp8Args a, int mtiles) {
-  typedef typename OutElem<BF16>::T E;
-  __shared__ f8i4 sh[2][kTile][9];  // rows 16 bytes longer than a block
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, q = lane >> 4;
-  const int m0 = blockIdx.x % mtiles * kTile, n0 = blockIdx.x / mtiles * kTile;
-  const int wm = wave / 2 * 32, wn = wave % 2 * 32, pieces = a.K / 16, blocks = f8_blocks(a.K);
-  f32x4 acc[2][2];
-  for (int i = 0; i < 2; ++i)
-    for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int b = 0; b < blocks; ++b) {
-    __syncthreads();
-    for (int o = threadIdx.x; o < 2 * kTile * 8; o += 256) {
-      const int side = o / (kTile * 8), r = o / 8 % kTile, p = o % 8;
-      const uint8_t* row = side == 0 ? a.x + (int64_t)min(m0 + r, a.T - 1) * a.ld_x : a.w + (int64_t)min(n0 + r, a.N - 1) * a.ld_w;
-      sh[side][r][p] = b * 8 + p < pieces ? ((g_f8i4*)row)[b * 8 + p] : f8i4{0, 0, 0, 0};
-    }
-    __syncthreads();
-    const float sw = a.sw[(int64_t)(n0 / kF8Block) * a.ld_sw + b];
+constexpr int kBK = kF8Block;  // bytes of a row in a step
+
+__device__ __forceinline__ int swizzle(int r) { return (r >> 1) & 7; }
+
+__device__ const f8i4 zero_codes = {0, 0, 0, 0};
+
+// Workgroups are dealt to the 8 XCDs round-robin; each XCD gets one contiguous range of
+// the tiles, so that the tiles of its L2 share rows and channels.
+__device__ __forceinline__ int xcd_order(int b, int nb) {
+  constexpr int kXcd = 8;
+  const int per = nb / kXcd, rem = nb % kXcd, x = b % kXcd, i = b / kXcd;
+  return x < rem ? x * (per + 1) + i : rem * (per + 1) + (x - rem) * per + i;
+}
+
+// All but the newest N of this wave's loads are in, every LDS read too, and so it is for every
+// wave of the workgroup. One block: what follows reads LDS that other waves' loads wrote.
+template <int N>
+__device__ __forceinline__ void meet_with_loads_but() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// 16 (4) bytes from each lane's address to LDS at `to` + 16 (4) lane; the compiler adds no wait
+// for them, meet_with_loads_but counts them. (A write of M0 is followed by one wait state.)
+__device__ __forceinline__ void load_to_lds(const void* from, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory", "m0");
+}
+__device__ __forceinline__ void load_one_to_lds(const void* from, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(to), "v"(from) : "memory", "m0");
+}
+
+// A row's (column's) 32 codes of a lane, and as four operands of the bf16 MFMA.
+struct Codes {
+  i32x8 v;
+};
+struct Converted {
+  bf16x8v v[4];
+};
+template <bool EXACT>
+struct Operand {
+  typedef Codes T;
+  static __device__ __forceinline__ T of(const Codes& c) { return c; }
+};
+template <>
+struct Operand<true> {
+  typedef Converted T;
+  static __device__ __forceinline__ T of(const Codes& c) {
+    T t;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float s[4];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) s[v] = a.sx[(int64_t)min(m0 + wm + 16 * i + 4 * q + v, a.T - 1) * a.ld_sx + b] * sw;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const f8i4 x = sh[0][wm + 16 * i + l16][4 * h + q], w = sh[1][wn + 16 * j + l16][4 * h + q];
-#pragma unroll
-          for (int e = 0; e < 4; e += 2) sum = mfma_bf16(f8_to_bf16(x[e], x[e + 1]), f8_to_bf16(w[e], w[e + 1]), sum);
-        }
-#pragma unroll
-        for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(s[v], sum[v], acc[i][j][v]);
-      }
-    }
+    for (int i = 0; i < 4; ++i) t.v[i] = f8_to_bf16(c.v[2 * i], c.v[2 * i + 1]);
+    return t;
   }
+};
+__device__ __forceinline__ f32x4 block_product(const Codes& x, const Codes& w) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x.v, w.v, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 block_product(const Converted& x, const Converted& w) {
+  f32x4 p = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < 4; ++i) p = mfma_bf16(x.v[i], w.v[i], p);
+  return p;
+}
+
+// Four neighbouring channels of PASSES rows, ROWS apart, from their sums in LDS (of PARTS parts,
+// PART floats apart). WHOLE: every row and channel is one of the matrix's, and what the rows
+// need is loaded for all of them before it is used.
+template <bool BF16, int PASSES, int ROWS, int LDROW, int PARTS, int PART, bool WHOLE>
+__device__ __forceinline__ void store_rows(const Fp8Args& a, int64_t t0, int n, const float* from, const float* bias) {
+  typedef typename OutElem<BF16>::T E;
+  constexpr int kAt = PASSES < 4 ? PASSES : 4;  // rows at once
+  const int left = WHOLE ? 4 : a.N - n;
+  if (!WHOLE && left <= 0) return;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+  for (int p0 = 0; p0 < PASSES; p0 += kAt) {
+    float v[kAt][4], more[kAt][4];
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int64_t t = m0 + wm + 16 * i + 4 * q + v;
-        const int n = n0 + wn + 16 * j + l16;
-        if (t >= a.T || n >= a.N) continue;
-        float o = acc[i][j][v];
-        if (a.o.bias) o += a.o.bias[n];
-        if (a.o.y) o += a.o.y[t * a.o.ld_y + n];
-        if (a.o.res) o += OutElem<BF16>::load(static_cast<const E*>(a.o.res)[t * a.o.ld_res + n]);
-        static_cast<E*>(a.o.out)[t * a.o.ld_out + n] = OutElem<BF16>::rounded(o);
+    for (int p = 0; p < kAt; ++p) {
+      const int r = (p0 + p) * ROWS;
+      f32x4 s = *reinterpret_cast<const f32x4*>(from + r * LDROW);
+#pragma unroll
+      for (int k = 1; k < PARTS; ++k) s += *reinterpret_cast<const f32x4*>(from + k * PART + r * LDROW);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[p][e] = s[e] + bias[e];
+    }
+    if (a.o.y) {
+#pragma unroll
+      for (int p = 0; p < kAt; ++p)
+        if (WHOLE || t0 + (p0 + p) * ROWS < a.T) load4(a.o.y + (t0 + (p0 + p) * ROWS) * a.o.ld_y + n, left, more[p]);
+#pragma unroll
+      for (int p = 0; p < kAt; ++p)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[p][e] += more[p][e];
+    }
+    if (a.o.res) {
+#pragma unroll
+      for (int p = 0; p < kAt; ++p)
+        if (WHOLE || t0 + (p0 + p) * ROWS < a.T)
+          load4(static_cast<const E*>(a.o.res) + (t0 + (p0 + p) * ROWS) * a.o.ld_res + n, left, more[p]);
+#pragma unroll
+      for (int p = 0; p < kAt; ++p)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[p][e] += more[p][e];
+    }
+#pragma unroll
+    for (int p = 0; p < kAt; ++p)
+      if (WHOLE || t0 + (p0 + p) * ROWS < a.T)
+        store4(static_cast<E*>(a.o.out) + (t0 + (p0 + p) * ROWS) * a.o.ld_out + n, left, v[p]);
+  }
+}
+
+// WM x WN waves, each 32 TM x 32 TN; RING buffers. KG such groups of waves take the blocks of K in
+// turn, each with buffers of its own, and add their sums at the end.
+//
+// A step's columns and two blocks of 16 rows are in registers at its start. Each block of rows,
+// after its products, makes room for the next but one. When a step's last two are left, every wave
+// has read the buffer: it is filled anew, and the next one, which is full, is read.
+template <int WM, int WN, int TM, int TN, int RING, int KG, bool BF16>
+__global__ __launch_bounds__(64 * WM* WN* KG) void k_fp8_gemm(Fp8Args a, int mtiles) {
+  typedef Operand<!BF16> Make;
+  typedef typename Make::T Op;
+  constexpr int kWaves = WM * WN, BM = 32 * TM * WM, BN = 32 * TN * WN;
+  constexpr int kLoadsA = BM / 8 / kWaves, kLoadsB = BN / 8 / kWaves, kLoads = kLoadsA + kLoadsB;  // of a wave per step, of 8 rows
+  static_assert(kLoadsA * 8 * kWaves == BM && kLoadsB * 8 * kWaves == BN, "rows divide among the waves");
+  constexpr int kOwnRows = BM / kWaves, kOwn = kOwnRows + 4;  // rows whose scales a wave loads; its floats in LDS
+  static_assert(kOwnRows % 4 == 0 && kOwnRows < 64, "a lane for each row and one for the channels");
+  constexpr int kData = (BM + BN) * kBK, kBuffer = kData + kWaves * kOwn * 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t all[KG][RING][(kBuffer + 1023) / 1024 * 1024];
+  const int lane = threadIdx.x & 63, wave_id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = KG == 1 ? 0 : wave_id / kWaves, wave = KG == 1 ? wave_id : wave_id % kWaves;
+  auto& sh = all[group];
+  const int tile = xcd_order(blockIdx.x, gridDim.x);
+  const int m0 = tile % mtiles * BM, n0 = tile / mtiles * BN;
+  const int wm = wave / WN, wn = wave % WN, l16 = lane & 15, quarter = lane >> 4;
+  const int blocks = f8_blocks(a.K);
+
+  // this lane's piece of each row that it fetches; rows past the last are read as the last,
+  // and not stored
+  const uint8_t* p[kLoads];
+  int at[kLoads];  // its offset in K
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const bool in_a = i < kLoadsA;
+    const int r = (in_a ? wave * kLoadsA + i : wave * kLoadsB + i - kLoadsA) * 8 + lane / 8;
+    const int64_t row = in_a ? min(m0 + r, a.T - 1) : min(n0 + r, a.N - 1);
+    at[i] = ((lane % 8) ^ swizzle(r)) * 16;
+    p[i] = (in_a ? a.x + row * a.ld_x : a.w + row * a.ld_w) + group * kBK + at[i];
+  }
+  const float* scales = lane < kOwnRows ? a.sx + (int64_t)min(m0 + wave * kOwnRows + lane, a.T - 1) * a.ld_sx
+                                        : a.sw + (int64_t)(min(n0 + wn * 32 * TN, a.N - 1) / kF8Block) * a.ld_sw;
+  const uint8_t* zeros = reinterpret_cast<const uint8_t*>(&zero_codes);
+  const uint32_t ring = (uint32_t)(uintptr_t)(lvoid*)&sh[0][0];
+  int kat = group;  // the next block to load
+  // the part'th of `parts` parts of the next step's loads, into buffer `buf` (past the last block:
+  // zeros, and scales of 0)
+  auto stage = [&](int buf, int part, int parts) {
+    const uint32_t to = ring + buf * (uint32_t)sizeof(sh[0]);
+    if (part == 0) {
+      if ((kat + 1) * kBK > a.K) {  // the last of K is in it, or nothing
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+          if (kat * kBK + at[i] >= a.K) p[i] = zeros;
       }
+      const void* scale = kat < blocks ? (const void*)(scales + kat) : zeros;
+      if (lane <= kOwnRows) load_one_to_lds(scale, to + kData + wave * kOwn * 4);
+      kat += KG;
+    }
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      if (i < kLoads * part / parts || i >= kLoads * (part + 1) / parts) continue;
+      load_to_lds(p[i], to + (i < kLoadsA ? (wave * kLoadsA + i) * 1024 : BM * kBK + (wave * kLoadsB + i - kLoadsA) * 1024));
+      p[i] += KG * kBK;
+    }
+  };
+
+  constexpr int kMB = 2 * TM, kNB = 2 * TN;  // blocks of 16 rows and columns
+  f32x4 acc[kMB][kNB];
+#pragma unroll
+  for (int i = 0; i < kMB; ++i)
+#pragma unroll
+    for (int j = 0; j < kNB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  struct Rows {
+    Codes v;
+    f32x4 s;
+  };
+  struct Cols {
+    Codes v[kNB];
+    float s;
+  };
+  auto codes = [&](const uint8_t* rows) {  // of row l16
+    const f8i4 lo = *reinterpret_cast<const f8i4*>(rows + l16 * kBK + ((quarter ^ swizzle(l16)) << 4));
+    const f8i4 hi = *reinterpret_cast<const f8i4*>(rows + l16 * kBK + (((4 + quarter) ^ swizzle(l16)) << 4));
+    return Codes{i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]}};
+  };
+  auto fetch_rows = [&](Rows& f, int buf, int i) {
+    const int r = wm * 32 * TM + i * 16, mine = r + 4 * quarter;
+    f.v = codes(&sh[buf][r * kBK]);
+    f.s = *reinterpret_cast<const f32x4*>(&sh[buf][kData + (mine / kOwnRows * kOwn + mine % kOwnRows) * 4]);
+  };
+  auto fetch_cols = [&](Cols& f, int buf) {
+#pragma unroll
+    for (int j = 0; j < kNB; ++j) f.v[j] = codes(&sh[buf][(BM + wn * 32 * TN + 16 * j) * kBK]);
+    f.s = *reinterpret_cast<const float*>(&sh[buf][kData + (wave * kOwn + kOwnRows) * 4]);
+  };
+  auto products = [&](const Rows& r, const Op* c, float sw, int i) {
+    const Op x = Make::of(r.v);
+    f32x4 b[kNB], s;
+#pragma unroll
+    for (int j = 0; j < kNB; ++j) b[j] = block_product(x, c[j]);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) s[v] = r.s[v] * sw;
+    __builtin_amdgcn_sched_barrier(0);  // every product is under way before the first is waited for
+#pragma unroll
+    for (int j = 0; j < kNB; ++j)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(s[v], b[j][v], acc[i][j][v]);
+    // the sums are formed here: put off to the step's end they kept every product in registers
+#pragma unroll
+    for (int j = 0; j < kNB; ++j) asm volatile("" : "+v"(acc[i][j]));
+  };
+  static_assert(RING > 1, "a buffer is filled while another is read");
+  constexpr int kStepLoads = kLoads + 1;
+  Rows rows[2];
+  Cols c0, c1;
+  int buf = 0;
+  auto step = [&](const Cols& now, Cols& next) {
+    Op c[kNB];
+#pragma unroll
+    for (int j = 0; j < kNB; ++j) c[j] = Make::of(now.v[j]);
+    // reads follow the products of what was read before: the compiler waits for all reads at once
+    int done = 0;
+#pragma unroll
+    for (int i = 0; i < kMB; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (i == kMB - 2) {
+        done = buf;  // every wave has all of it in registers at the barrier
+        buf = buf + 1 == RING ? 0 : buf + 1;
+        meet_with_loads_but<(RING - 2) * kStepLoads>();  // the next buffer is in
+      }
+      products(rows[i % 2], c, now.s, i);
+      __builtin_amdgcn_sched_barrier(0);
+      if (i == kMB - 2) fetch_cols(next, buf);
+      fetch_rows(rows[i % 2], buf, i < kMB - 2 ? i + 2 : i - (kMB - 2));
+      if (i >= kMB - 2) stage(done, i - (kMB - 2), 2);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+#pragma unroll
+  for (int r = 0; r < RING; ++r) stage(r, 0, 1);
+  meet_with_loads_but<(RING - 1) * kStepLoads>();
+  fetch_rows(rows[0], 0, 0);
+  fetch_rows(rows[1], 0, 1);
+  fetch_cols(c0, 0);
+  for (int b = 0; b < blocks; b += 2 * KG) {  // two steps a turn, so that each set of columns has its registers
+    step(c0, c1);
+    step(c1, c0);
+  }
+
+  // Each wave turns its sums in LDS, a block of 32 rows at a time (rows 16 bytes longer, so that
+  // the four rows of a write use different banks), and reads four neighbouring channels of a
+  // row a lane: whole lines are read and written from there on.
+  meet_with_loads_but<0>();
+  constexpr int kCols = 32 * TN, kRow = kCols + 4, kLanes = kCols / 4, kRows = 64 / kLanes;  // lanes of a row, rows a pass
+  constexpr int kTurn = 32 * kRow;  // floats of a wave's block
+  static_assert(sizeof(all) >= KG * kWaves * kTurn * 4, "the waves' blocks fit the buffers");
+  float* turns = reinterpret_cast<float*>(&all[0][0][0]);
+  float* turn = turns + wave_id * kTurn;
+  const int c = lane % kLanes * 4, n = n0 + wn * kCols + c;
+  float bias[4] = {0.f, 0.f, 0.f, 0.f};
+  if (a.o.bias) load4(a.o.bias + n, a.N - n, bias);
+  const bool whole = n0 + BN <= a.N;  // every channel of the tile is one
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int j = 0; j < kNB; ++j)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) turn[(16 * b + 4 * quarter + v) * kRow + 16 * j + l16] = acc[2 * i + b][j][v];
+    if (KG > 1) __syncthreads();
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    // each group stores a part of the rows, as long as there are any
+    constexpr int kPasses = 32 / kRows >= KG ? 32 / kRows / KG : 1;
+    const int rb = group * kPasses * kRows + lane / kLanes;
+    const bool stores = group * kPasses * kRows < 32;
+    const int row = (wm * TM + i) * 32 + rb;  // this lane's first row in the tile
+    const float* from = turns + wave * kTurn + rb * kRow + c;
+    if (!stores) {
+    } else if (whole && m0 + (wm * TM + i + 1) * 32 <= a.T)
+      store_rows<BF16, kPasses, kRows, kRow, KG, kWaves * kTurn, true>(a, m0 + row, n, from, bias);
+    else
+      store_rows<BF16, kPasses, kRows, kRow, KG, kWaves * kTurn, false>(a, m0 + row, n, from, bias);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (KG > 1 && i + 1 < TM) __syncthreads();
+  }
 }
 
 }  // namespace
 
+// The tiles, and what a block of K costs a CU in each (us); the tile whose rounds over the 256 CUs
+// cost least is taken.
+struct Tile {
+  int tokens, channels;
+  float cost;
+};
+constexpr int kCus = 256;
+constexpr Tile kTiles[] = {{128, 256, 0.95f}, {128, 128, 0.58f}, {64, 128, 0.38f}, {64, 64, 0.27f}, {64, 32, 0.21f}, {32, 32, 0.17f}};
+constexpr int kTileCount = sizeof(kTiles) / sizeof(kTiles[0]);
+
+static int choose_tile(int64_t T, int64_t N, int first) {
+  int best = first;
+  float least = 0.f;
+  for (int i = first; i < kTileCount; ++i) {
+    const int64_t n = ((T - 1) / kTiles[i].tokens + 1) * ((N - 1) / kTiles[i].channels + 1);
+    const float cost = (float)((n - 1) / kCus + 1) * kTiles[i].cost;
+    if (i == first || cost < least) {
+      best = i;
+      least = cost;
+    }
+  }
+  return best;
+}
+
+template <bool BF16, int WM, int WN, int TM, int TN, int RING, int KG>
+static void gemm_tile(const Fp8Args& a, hipStream_t s) {
+  const int mt = (a.T - 1) / (32 * TM * WM) + 1, nt = (a.N - 1) / (32 * TN * WN) + 1;
+  hipLaunchKernelGGL((k_fp8_gemm<WM, WN, TM, TN, RING, KG, BF16>), dim3(mt * nt), dim3(64 * WM * WN * KG), 0, s, a, mt);
+}
+
+#ifndef FORCE_TILE
+#define FORCE_TILE(x) (x)
+#endif
+template <bool BF16>
+static void gemm(const Fp8Args& a, hipStream_t s) {
+  switch (FORCE_TILE(choose_tile(a.T, a.N, BF16 ? 0 : 1))) {
+    case 0:
+      if constexpr (BF16) return gemm_tile<BF16, 2, 4, 2, 2, 3, 1>(a, s);
+    case 1: return gemm_tile<BF16, 2, 4, 2, 1, 4, 1>(a, s);
+    case 2: return gemm_tile<BF16, 2, 4, 1, 1, 4, 1>(a, s);
+    case 3: return gemm_tile<BF16, 2, 2, 1, 1, 4, 2>(a, s);
+    case 4: return gemm_tile<BF16, 2, 1, 1, 1, 3, 4>(a, s);
+    default: return gemm_tile<BF16, 1, 1, 1, 1, 4, 4>(a, s);
+  }
+}
+
 void launch_fp8_gemm(const Fp8Args& a, bool out_bf16, hipStream_t s) {
-  const int mt = (a.T - 1) / kTile + 1, nt = (a.N - 1) / kTile + 1;
   if (out_bf16)
-    hipLaunchKernelGGL((k_fp8_gemm<true>), dim3(mt * nt), dim3(256), 0, s, a, mt);
+    gemm<true>(a, s);
   else
-    hipLaunchKernelGGL((k_fp8_gemm<false>), dim3(mt * nt), dim3(256), 0, s, a, mt);
+    gemm<false>(a, s);
 }
 
 }  // namespace moe
