@@ -235,18 +235,24 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_fp8_gemm(Fp8Args a, int mti
     for (int j = 0; j < kNB; ++j) f.v[j] = codes(&sh[buf][(BM + wn * 32 * TN + 16 * j) * kBK]);
     f.s = *reinterpret_cast<const float*>(&sh[buf][kData + (wave * kOwn + kOwnRows) * 4]);
   };
+  // A block of rows' products are under way while those of the block before are added.
+  f32x4 part[2][kNB], scale[2];
+#pragma unroll
+  for (int j = 0; j < kNB; ++j) part[1][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  scale[1] = f32x4{0.f, 0.f, 0.f, 0.f};
   auto products = [&](const Rows& r, const Op* c, float sw, int i) {
     const Op x = Make::of(r.v);
-    f32x4 b[kNB], s;
 #pragma unroll
-    for (int j = 0; j < kNB; ++j) b[j] = block_product(x, c[j]);
+    for (int j = 0; j < kNB; ++j) part[i % 2][j] = block_product(x, c[j]);
 #pragma unroll
-    for (int v = 0; v < 4; ++v) s[v] = r.s[v] * sw;
-    __builtin_amdgcn_sched_barrier(0);  // every product is under way before the first is waited for
+    for (int v = 0; v < 4; ++v) scale[i % 2][v] = r.s[v] * sw;
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto add = [&](int i) {
 #pragma unroll
     for (int j = 0; j < kNB; ++j)
 #pragma unroll
-      for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(s[v], b[j][v], acc[i][j][v]);
+      for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(scale[i % 2][v], part[i % 2][j][v], acc[i][j][v]);
     // the sums are formed here: put off to the step's end they kept every product in registers
 #pragma unroll
     for (int j = 0; j < kNB; ++j) asm volatile("" : "+v"(acc[i][j]));
@@ -271,6 +277,7 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_fp8_gemm(Fp8Args a, int mti
         meet_with_loads_but<(RING - 2) * kStepLoads>();  // the next buffer is in
       }
       products(rows[i % 2], c, now.s, i);
+      add((i + kMB - 1) % kMB);
       __builtin_amdgcn_sched_barrier(0);
       if (i == kMB - 2) fetch_cols(next, buf);
       fetch_rows(rows[i % 2], buf, i < kMB - 2 ? i + 2 : i - (kMB - 2));
@@ -288,6 +295,7 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_fp8_gemm(Fp8Args a, int mti
     step(c0, c1);
     step(c1, c0);
   }
+  add(kMB - 1);
 
   // Each wave turns its sums in LDS, a block of 32 rows at a time (rows 16 bytes longer, so that
   // the four rows of a write use different banks), and reads four neighbouring channels of a
