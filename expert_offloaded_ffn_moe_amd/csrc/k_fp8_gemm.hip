@@ -220,20 +220,37 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_fp8_gemm(Fp8Args a, int mti
     Codes v[kNB];
     float s;
   };
-  auto codes = [&](const uint8_t* rows) {  // of row l16
-    const f8i4 lo = *reinterpret_cast<const f8i4*>(rows + l16 * kBK + ((quarter ^ swizzle(l16)) << 4));
-    const f8i4 hi = *reinterpret_cast<const f8i4*>(rows + l16 * kBK + (((4 + quarter) ^ swizzle(l16)) << 4));
-    return Codes{i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]}};
+  // what this lane reads of a buffer: its places in the wave's first row and column, the two pieces
+  // apart, and its rows' scales
+  typedef __attribute__((address_space(3))) const uint8_t l_u8;
+  typedef __attribute__((address_space(3))) const f8i4 l_f8i4;
+  const int at_lo = l16 * kBK + ((quarter ^ swizzle(l16)) << 4), at_hi = l16 * kBK + (((4 + quarter) ^ swizzle(l16)) << 4);
+  const int row0 = wm * 32 * TM * kBK, col0 = (BM + wn * 32 * TN) * kBK;
+  l_u8* lds = (l_u8*)&sh[0][0];
+  auto codes = [&](l_u8* lo, l_u8* hi, int block) {
+    const f8i4 a = *(l_f8i4*)(lo + block * 16 * kBK), b = *(l_f8i4*)(hi + block * 16 * kBK);
+    return Codes{i32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
   };
-  auto fetch_rows = [&](Rows& f, int buf, int i) {
-    const int r = wm * 32 * TM + i * 16, mine = r + 4 * quarter;
-    f.v = codes(&sh[buf][r * kBK]);
-    f.s = *reinterpret_cast<const f32x4*>(&sh[buf][kData + (mine / kOwnRows * kOwn + mine % kOwnRows) * 4]);
+  struct Reader {
+    l_u8 *row_lo, *row_hi, *col_lo, *col_hi, *scale, *own;
   };
-  auto fetch_cols = [&](Cols& f, int buf) {
+  auto reader = [&](int buf) {
+    l_u8* b = lds + buf * (int)sizeof(sh[0]);
+    const int mine = wm * 32 * TM + 4 * quarter;
+    return Reader{b + row0 + at_lo, b + row0 + at_hi, b + col0 + at_lo, b + col0 + at_hi,
+                  b + kData + (mine / kOwnRows * kOwn + mine % kOwnRows) * 4, b + kData + (wave * kOwn + kOwnRows) * 4};
+  };
+  auto fetch_rows = [&](Rows& f, const Reader& from, int i) {
+    f.v = codes(from.row_lo, from.row_hi, i);
+    // 16 rows on: in the same wave's part or a whole number of them on
+    constexpr int kPer = kOwnRows < 16 ? 16 / kOwnRows * kOwn : kOwn;
+    const int next = kOwnRows <= 16 ? i * kPer : i * 16 / kOwnRows * kOwn + i * 16 % kOwnRows;
+    f.s = *(__attribute__((address_space(3))) const f32x4*)(from.scale + next * 4);
+  };
+  auto fetch_cols = [&](Cols& f, const Reader& from) {
 #pragma unroll
-    for (int j = 0; j < kNB; ++j) f.v[j] = codes(&sh[buf][(BM + wn * 32 * TN + 16 * j) * kBK]);
-    f.s = *reinterpret_cast<const float*>(&sh[buf][kData + (wave * kOwn + kOwnRows) * 4]);
+    for (int j = 0; j < kNB; ++j) f.v[j] = codes(from.col_lo, from.col_hi, j);
+    f.s = *(__attribute__((address_space(3))) const float*)from.own;
   };
   // A block of rows' products are under way while those of the block before are added.
   f32x4 part[2][kNB], scale[2];
@@ -242,26 +259,24 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_fp8_gemm(Fp8Args a, int mti
   scale[1] = f32x4{0.f, 0.f, 0.f, 0.f};
   auto products = [&](const Rows& r, const Op* c, float sw, int i) {
     const Op x = Make::of(r.v);
+    const int before = (i + kMB - 1) % kMB;
 #pragma unroll
-    for (int j = 0; j < kNB; ++j) part[i % 2][j] = block_product(x, c[j]);
+    for (int j = 0; j < kNB; ++j) {
+      part[i % 2][j] = block_product(x, c[j]);
+      scale[i % 2][j] = r.s[j] * sw;
+      if (kNB == 2) scale[i % 2][2 + j] = r.s[2 + j] * sw;
 #pragma unroll
-    for (int v = 0; v < 4; ++v) scale[i % 2][v] = r.s[v] * sw;
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  auto add = [&](int i) {
-#pragma unroll
-    for (int j = 0; j < kNB; ++j)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(scale[i % 2][v], part[i % 2][j][v], acc[i][j][v]);
-    // the sums are formed here: put off to the step's end they kept every product in registers
-#pragma unroll
-    for (int j = 0; j < kNB; ++j) asm volatile("" : "+v"(acc[i][j]));
+      for (int v = 0; v < 4; ++v) acc[before][j][v] = fmaf(scale[before % 2][v], part[before % 2][j][v], acc[before][j][v]);
+      asm volatile("" : "+v"(acc[before][j]));  // formed here: put off to the step's end, sums kept every product in registers
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
   static_assert(RING > 1, "a buffer is filled while another is read");
   constexpr int kStepLoads = kLoads + 1;
   Rows rows[2];
   Cols c0, c1;
   int buf = 0;
+  Reader from = reader(0);
   auto step = [&](const Cols& now, Cols& next) {
     Op c[kNB];
 #pragma unroll
@@ -277,10 +292,11 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_fp8_gemm(Fp8Args a, int mti
         meet_with_loads_but<(RING - 2) * kStepLoads>();  // the next buffer is in
       }
       products(rows[i % 2], c, now.s, i);
-      add((i + kMB - 1) % kMB);
-      __builtin_amdgcn_sched_barrier(0);
-      if (i == kMB - 2) fetch_cols(next, buf);
-      fetch_rows(rows[i % 2], buf, i < kMB - 2 ? i + 2 : i - (kMB - 2));
+      if (i == kMB - 2) {
+        from = reader(buf);
+        fetch_cols(next, from);
+      }
+      fetch_rows(rows[i % 2], from, i < kMB - 2 ? i + 2 : i - (kMB - 2));
       if (i >= kMB - 2) stage(done, i - (kMB - 2), 2);
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -288,14 +304,17 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_fp8_gemm(Fp8Args a, int mti
 #pragma unroll
   for (int r = 0; r < RING; ++r) stage(r, 0, 1);
   meet_with_loads_but<(RING - 1) * kStepLoads>();
-  fetch_rows(rows[0], 0, 0);
-  fetch_rows(rows[1], 0, 1);
-  fetch_cols(c0, 0);
+  fetch_rows(rows[0], from, 0);
+  fetch_rows(rows[1], from, 1);
+  fetch_cols(c0, from);
   for (int b = 0; b < blocks; b += 2 * KG) {  // two steps a turn, so that each set of columns has its registers
     step(c0, c1);
     step(c1, c0);
   }
-  add(kMB - 1);
+#pragma unroll
+  for (int j = 0; j < kNB; ++j)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) acc[kMB - 1][j][v] = fmaf(scale[1][v], part[1][j][v], acc[kMB - 1][j][v]);
 
   // Each wave turns its sums in LDS, a block of 32 rows at a time (rows 16 bytes longer, so that
   // the four rows of a write use different banks), and reads four neighbouring channels of a
