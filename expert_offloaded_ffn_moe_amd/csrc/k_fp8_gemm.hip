@@ -20,8 +20,11 @@
 // the lanes that a read serves at once use every bank once; loads go from memory to LDS
 // directly, in lane order, so that each lane fetches the piece that belongs at its place. Lane
 // quarter q reads pieces q and 4 + q of both operands. Pieces past K come from a line of
-// zeros. A step's scales follow the same way: a wave's part of the rows' and its channels' one.
+// zeros. Scales follow the same way, a wave's part of the rows' and its channels' one, those of
+// four steps at once: a row's scales are neighbours, and their line comes from L2 once for them.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "f8_dev.h"
 #include "fp8.h"
@@ -157,8 +160,9 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_fp8_gemm(Fp8Args a, int mti
   static_assert(kLoadsA * 8 * kWaves == BM && kLoadsB * 8 * kWaves == BN, "rows divide among the waves");
   constexpr int kOwnRows = BM / kWaves, kOwn = kOwnRows + 4;  // rows whose scales a wave loads; its floats in LDS
   static_assert(kOwnRows % 4 == 0 && kOwnRows < 64, "a lane for each row and one for the channels");
-  constexpr int kData = (BM + BN) * kBK, kBuffer = kData + kWaves * kOwn * 4;
-  __shared__ __attribute__((aligned(1024))) uint8_t all[KG][RING][(kBuffer + 1023) / 1024 * 1024];
+  constexpr int kSteps = 4;  // whose scales are loaded together
+  __shared__ __attribute__((aligned(1024))) uint8_t all[KG][RING][(BM + BN) * kBK];
+  __shared__ __attribute__((aligned(16))) float all_scales[KG][2][kSteps][kWaves * kOwn];
   const int lane = threadIdx.x & 63, wave_id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = KG == 1 ? 0 : wave_id / kWaves, wave = KG == 1 ? wave_id : wave_id % kWaves;
   auto& sh = all[group];
@@ -182,11 +186,18 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_fp8_gemm(Fp8Args a, int mti
   const float* scales = lane < kOwnRows ? a.sx + (int64_t)min(m0 + wave * kOwnRows + lane, a.T - 1) * a.ld_sx
                                         : a.sw + (int64_t)(min(n0 + wn * 32 * TN, a.N - 1) / kF8Block) * a.ld_sw;
   const uint8_t* zeros = reinterpret_cast<const uint8_t*>(&zero_codes);
-  const uint32_t ring = (uint32_t)(uintptr_t)(lvoid*)&sh[0][0];
+  const uint32_t ring = (uint32_t)(uintptr_t)(lvoid*)&sh[0][0], scale_sets = (uint32_t)(uintptr_t)(lvoid*)&all_scales[group][0][0][0];
   int kat = group;  // the next block to load
-  // the part'th of `parts` parts of the next step's loads, into buffer `buf` (past the last block:
-  // zeros, and scales of 0)
-  auto stage = [&](int buf, int part, int parts) {
+  // the scales of the next kSteps steps into set `set`, past the last block 0
+  auto stage_scales = [&](int set) {
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      const void* scale = kat + k * KG < blocks ? (const void*)(scales + kat + k * KG) : zeros;
+      if (lane <= kOwnRows) load_one_to_lds(scale, scale_sets + ((set * kSteps + k) * kWaves + wave) * kOwn * 4);
+    }
+  };
+  // the part'th of two parts of the next step's loads, into buffer `buf` (past the last block: zeros)
+  auto stage = [&](int buf, int part) {
     const uint32_t to = ring + buf * (uint32_t)sizeof(sh[0]);
     if (part == 0) {
       if ((kat + 1) * kBK > a.K) {  // the last of K is in it, or nothing
@@ -194,13 +205,11 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_fp8_gemm(Fp8Args a, int mti
         for (int i = 0; i < kLoads; ++i)
           if (kat * kBK + at[i] >= a.K) p[i] = zeros;
       }
-      const void* scale = kat < blocks ? (const void*)(scales + kat) : zeros;
-      if (lane <= kOwnRows) load_one_to_lds(scale, to + kData + wave * kOwn * 4);
       kat += KG;
     }
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      if (i < kLoads * part / parts || i >= kLoads * (part + 1) / parts) continue;
+      if (i < kLoads * part / 2 || i >= kLoads * (part + 1) / 2) continue;
       load_to_lds(p[i], to + (i < kLoadsA ? (wave * kLoadsA + i) * 1024 : BM * kBK + (wave * kLoadsB + i - kLoadsA) * 1024));
       p[i] += KG * kBK;
     }
@@ -231,26 +240,30 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_fp8_gemm(Fp8Args a, int mti
     const f8i4 a = *(l_f8i4*)(lo + block * 16 * kBK), b = *(l_f8i4*)(hi + block * 16 * kBK);
     return Codes{i32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
   };
+  typedef __attribute__((address_space(3))) const float l_f32;
+  typedef __attribute__((address_space(3))) const f32x4 l_f32x4;
+  const int first = wm * 32 * TM + 4 * quarter;  // this lane's first row
+  l_f32* row_scales = (l_f32*)&all_scales[group][0][0][first / kOwnRows * kOwn + first % kOwnRows];
+  l_f32* col_scale = (l_f32*)&all_scales[group][0][0][wave * kOwn + kOwnRows];
   struct Reader {
-    l_u8 *row_lo, *row_hi, *col_lo, *col_hi, *scale, *own;
+    l_u8 *row_lo, *row_hi, *col_lo, *col_hi;
+    int scales;  // the step's, in floats
   };
-  auto reader = [&](int buf) {
+  auto reader = [&](int buf, int set, int step) {
     l_u8* b = lds + buf * (int)sizeof(sh[0]);
-    const int mine = wm * 32 * TM + 4 * quarter;
-    return Reader{b + row0 + at_lo, b + row0 + at_hi, b + col0 + at_lo, b + col0 + at_hi,
-                  b + kData + (mine / kOwnRows * kOwn + mine % kOwnRows) * 4, b + kData + (wave * kOwn + kOwnRows) * 4};
+    return Reader{b + row0 + at_lo, b + row0 + at_hi, b + col0 + at_lo, b + col0 + at_hi, (set * kSteps + step) * kWaves * kOwn};
   };
   auto fetch_rows = [&](Rows& f, const Reader& from, int i) {
     f.v = codes(from.row_lo, from.row_hi, i);
     // 16 rows on: in the same wave's part or a whole number of them on
     constexpr int kPer = kOwnRows < 16 ? 16 / kOwnRows * kOwn : kOwn;
     const int next = kOwnRows <= 16 ? i * kPer : i * 16 / kOwnRows * kOwn + i * 16 % kOwnRows;
-    f.s = *(__attribute__((address_space(3))) const f32x4*)(from.scale + next * 4);
+    f.s = *(l_f32x4*)(row_scales + from.scales + next);
   };
   auto fetch_cols = [&](Cols& f, const Reader& from) {
 #pragma unroll
     for (int j = 0; j < kNB; ++j) f.v[j] = codes(from.col_lo, from.col_hi, j);
-    f.s = *(__attribute__((address_space(3))) const float*)from.own;
+    f.s = col_scale[from.scales];
   };
   // A block of rows' products are under way while those of the block before are added.
   f32x4 part[2][kNB], scale[2];
@@ -271,13 +284,17 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_fp8_gemm(Fp8Args a, int mti
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  static_assert(RING > 1, "a buffer is filled while another is read");
-  constexpr int kStepLoads = kLoads + 1;
+  static_assert(RING > 1 && RING <= kSteps, "a buffer is filled while another is read; the scales' sets are two");
   Rows rows[2];
   Cols c0, c1;
-  int buf = 0;
-  Reader from = reader(0);
-  auto step = [&](const Cols& now, Cols& next) {
+  int buf = 0, set = 0;
+  Reader from = reader(0, 0, 0);
+  // step S of kSteps; one RING steps on is loaded in it
+  auto step = [&](auto number, const Cols& now, Cols& next) {
+    constexpr int S = decltype(number)::value;
+    // of the steps S + 2 .. S + RING - 1, whose loads may be under way when the next one's are in, one
+    // may have come with scales
+    constexpr bool kScales = (S + RING - 1) / kSteps > (S + 1) / kSteps;
     Op c[kNB];
 #pragma unroll
     for (int j = 0; j < kNB; ++j) c[j] = Make::of(now.v[j]);
@@ -289,27 +306,39 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_fp8_gemm(Fp8Args a, int mti
       if (i == kMB - 2) {
         done = buf;  // every wave has all of it in registers at the barrier
         buf = buf + 1 == RING ? 0 : buf + 1;
-        meet_with_loads_but<(RING - 2) * kStepLoads>();  // the next buffer is in
+        meet_with_loads_but<(RING - 2) * kLoads + (kScales ? kSteps : 0)>();  // the next buffer is in
       }
       products(rows[i % 2], c, now.s, i);
       if (i == kMB - 2) {
-        from = reader(buf);
+        from = reader(buf, S == kSteps - 1 ? set ^ 1 : set, (S + 1) % kSteps);
         fetch_cols(next, from);
       }
       fetch_rows(rows[i % 2], from, i < kMB - 2 ? i + 2 : i - (kMB - 2));
-      if (i >= kMB - 2) stage(done, i - (kMB - 2), 2);
+      if (i == kMB - 2 && S + RING == kSteps) stage_scales(set ^ 1);
+      if (i >= kMB - 2) stage(done, i - (kMB - 2));
     }
     __builtin_amdgcn_sched_barrier(0);
   };
+  stage_scales(0);
 #pragma unroll
-  for (int r = 0; r < RING; ++r) stage(r, 0, 1);
-  meet_with_loads_but<(RING - 1) * kStepLoads>();
+  for (int r = 0; r < RING; ++r) {
+    stage(r, 0);
+    stage(r, 1);
+  }
+  meet_with_loads_but<(RING - 1) * kLoads>();
   fetch_rows(rows[0], from, 0);
   fetch_rows(rows[1], from, 1);
   fetch_cols(c0, from);
-  for (int b = 0; b < blocks; b += 2 * KG) {  // two steps a turn, so that each set of columns has its registers
-    step(c0, c1);
-    step(c1, c0);
+  for (int left = (blocks - 1) / KG + 1;;) {  // two sets of columns in turn, so that each has its registers
+    step(std::integral_constant<int, 0>(), c0, c1);
+    if (--left == 0) break;
+    step(std::integral_constant<int, 1>(), c1, c0);
+    if (--left == 0) break;
+    step(std::integral_constant<int, 2>(), c0, c1);
+    if (--left == 0) break;
+    step(std::integral_constant<int, 3>(), c1, c0);
+    if (--left == 0) break;
+    set ^= 1;
   }
 #pragma unroll
   for (int j = 0; j < kNB; ++j)
