@@ -148,9 +148,11 @@ __device__ __forceinline__ void store_rows(const Fp8Args& a, int64_t t0, int n, 
 // WM x WN waves, each 32 TM x 32 TN; RING buffers. KG such groups of waves take the blocks of K in
 // turn, each with buffers of its own, and add their sums at the end.
 //
-// A step's columns and two blocks of 16 rows are in registers at its start. Each block of rows,
-// after its products, makes room for the next but one. When a step's last two are left, every wave
-// has read the buffer: it is filled anew, and the next one, which is full, is read.
+// A step's rows and columns are in registers when it starts. Early in it (when its last reads are
+// sure to be in) the waves meet: the buffer that they were read from is filled anew, and the next
+// one, which is full, is read, into the registers of each block of rows after its products and a
+// second set of columns. Both are spread over the rest of the step, since all waves' reads
+// together take LDS as long as the products take.
 template <int WM, int WN, int TM, int TN, int RING, int KG, bool BF16>
 __global__ __launch_bounds__(64 * WM* WN* KG) void k_fp8_gemm(Fp8Args a, int mtiles) {
   typedef Operand<!BF16> Make;
@@ -196,8 +198,8 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_fp8_gemm(Fp8Args a, int mti
       if (lane <= kOwnRows) load_one_to_lds(scale, scale_sets + ((set * kSteps + k) * kWaves + wave) * kOwn * 4);
     }
   };
-  // the part'th of two parts of the next step's loads, into buffer `buf` (past the last block: zeros)
-  auto stage = [&](int buf, int part) {
+  // the part'th of `parts` parts of the next step's loads, into buffer `buf` (past the last block: zeros)
+  auto stage = [&](int buf, int part, int parts) {
     const uint32_t to = ring + buf * (uint32_t)sizeof(sh[0]);
     if (part == 0) {
       if ((kat + 1) * kBK > a.K) {  // the last of K is in it, or nothing
@@ -209,7 +211,7 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_fp8_gemm(Fp8Args a, int mti
     }
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      if (i < kLoads * part / 2 || i >= kLoads * (part + 1) / 2) continue;
+      if (i < kLoads * part / parts || i >= kLoads * (part + 1) / parts) continue;
       load_to_lds(p[i], to + (i < kLoadsA ? (wave * kLoadsA + i) * 1024 : BM * kBK + (wave * kLoadsB + i - kLoadsA) * 1024));
       p[i] += KG * kBK;
     }
@@ -260,10 +262,11 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_fp8_gemm(Fp8Args a, int mti
     const int next = kOwnRows <= 16 ? i * kPer : i * 16 / kOwnRows * kOwn + i * 16 % kOwnRows;
     f.s = *(l_f32x4*)(row_scales + from.scales + next);
   };
-  auto fetch_cols = [&](Cols& f, const Reader& from) {
+  auto fetch_cols = [&](Cols& f, const Reader& from, int part, int parts) {
 #pragma unroll
-    for (int j = 0; j < kNB; ++j) f.v[j] = codes(from.col_lo, from.col_hi, j);
-    f.s = col_scale[from.scales];
+    for (int j = 0; j < kNB; ++j)
+      if (j >= kNB * part / parts && j < kNB * (part + 1) / parts) f.v[j] = codes(from.col_lo, from.col_hi, j);
+    if (part == 0) f.s = col_scale[from.scales];
   };
   // A block of rows' products are under way while those of the block before are added.
   f32x4 part[2][kNB], scale[2];
@@ -285,7 +288,7 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_fp8_gemm(Fp8Args a, int mti
     }
   };
   static_assert(RING > 1 && RING <= kSteps, "a buffer is filled while another is read; the scales' sets are two");
-  Rows rows[2];
+  Rows rows[kMB];
   Cols c0, c1;
   int buf = 0, set = 0;
   Reader from = reader(0, 0, 0);
@@ -299,36 +302,38 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_fp8_gemm(Fp8Args a, int mti
 #pragma unroll
     for (int j = 0; j < kNB; ++j) c[j] = Make::of(now.v[j]);
     // reads follow the products of what was read before: the compiler waits for all reads at once
+    constexpr int kMeet = kMB / 2 - 1, kParts = kMB - kMeet;  // in which slot; those from it on
     int done = 0;
 #pragma unroll
     for (int i = 0; i < kMB; ++i) {
       __builtin_amdgcn_sched_barrier(0);
-      if (i == kMB - 2) {
-        done = buf;  // every wave has all of it in registers at the barrier
+      if (i == kMeet) {
+        done = buf;
         buf = buf + 1 == RING ? 0 : buf + 1;
         meet_with_loads_but<(RING - 2) * kLoads + (kScales ? kSteps : 0)>();  // the next buffer is in
-      }
-      products(rows[i % 2], c, now.s, i);
-      if (i == kMB - 2) {
         from = reader(buf, S == kSteps - 1 ? set ^ 1 : set, (S + 1) % kSteps);
-        fetch_cols(next, from);
       }
-      fetch_rows(rows[i % 2], from, i < kMB - 2 ? i + 2 : i - (kMB - 2));
-      if (i == kMB - 2 && S + RING == kSteps) stage_scales(set ^ 1);
-      if (i >= kMB - 2) stage(done, i - (kMB - 2));
+      products(rows[i], c, now.s, i);
+      if (i < kMeet) continue;
+      if (i == kMeet)
+#pragma unroll
+        for (int k = 0; k < kMeet; ++k) fetch_rows(rows[k], from, k);
+      fetch_rows(rows[i], from, i);
+      if (i - kMeet < 2) fetch_cols(next, from, i - kMeet, 2);
+      if (i == kMeet && S + RING == kSteps) stage_scales(set ^ 1);
+      stage(done, i - kMeet, kParts);
     }
     __builtin_amdgcn_sched_barrier(0);
   };
   stage_scales(0);
 #pragma unroll
   for (int r = 0; r < RING; ++r) {
-    stage(r, 0);
-    stage(r, 1);
+    stage(r, 0, 1);
   }
   meet_with_loads_but<(RING - 1) * kLoads>();
-  fetch_rows(rows[0], from, 0);
-  fetch_rows(rows[1], from, 1);
-  fetch_cols(c0, from);
+#pragma unroll
+  for (int i = 0; i < kMB; ++i) fetch_rows(rows[i], from, i);
+  fetch_cols(c0, from, 0, 1);
   for (int left = (blocks - 1) / KG + 1;;) {  // two sets of columns in turn, so that each has its registers
     step(std::integral_constant<int, 0>(), c0, c1);
     if (--left == 0) break;
