@@ -321,13 +321,7 @@ __device__ __forceinline__ void route(const Fp8LayerArgs& a, Route& r, bool writ
 
 // ----------------------------------------------------------------------------- products
 //
-// A load instruction takes a cycle for each line that each four neighbouring lanes touch, so lanes
-// are given two neighbouring pieces of a row: the MFMA's rows 2 a and 2 a + 1 are both row a of
-// the weights, at a block's even and odd pieces of 16 codes (piece 2 q + (row & 1) for lane quarter
-// q), and its columns 2 v and 2 v + 1 both vector v, at even and odd pieces. Of the products
-// of rows and columns those of like parity are the sums wanted, of 8 rows with 8 vectors; a
-// row's whole sum is that of two neighbouring lanes. (With a row for each of the 16 rows, the
-// lines bounded the 7168-wide layer's first half at 4.9 TB/s and the second at 2.5.)
+// Operands are of 8 rows and 8 vectors, at two parities of the pieces of K (f8_dev.h).
 
 constexpr int kWaves = 8;  // of a workgroup, taking blocks of 128 of K in turn
 constexpr int kRows = 8;   // of weights in an operand
@@ -347,14 +341,6 @@ struct Vectors {
   static __device__ __forceinline__ int lane_of(int token) { return TERMS == 1 ? 2 * token : 6 * token; }
   static __device__ __forceinline__ bool is_first(int column) { return TERMS == 1 ? column % 2 == 0 : column == 0 || column == 6; }
 };
-
-// 0 that the compiler takes for a lane's own: a load with it in its address is a vector load, which is
-// waited for in the order of the vector loads. (A scalar load is waited for with every LDS read.)
-__device__ __forceinline__ int lane_zero() {
-  int z;
-  asm volatile("v_mov_b32 %0, 0" : "=v"(z));
-  return z;
-}
 
 // A lane's 16 values of a vector, as two steps of the MFMA take them.
 struct Values {
@@ -381,7 +367,6 @@ __device__ __forceinline__ void add_products(const f8i4& w, const Values& x, flo
 #pragma unroll
   for (int v = 0; v < 4; ++v) s[v] = fmaf(scale, p[v], s[v]);
 }
-__device__ __forceinline__ float of_parity(float even, float odd) { return threadIdx.x & 1 ? odd : even; }
 
 __device__ __forceinline__ Fp8Tile uniform(const Fp8Tile* tile) {
   const uint64_t u = *reinterpret_cast<const uint64_t*>(tile);
@@ -389,14 +374,11 @@ __device__ __forceinline__ Fp8Tile uniform(const Fp8Tile* tile) {
   return Fp8Tile{(uint16_t)lo, (uint16_t)(lo >> 16), (uint16_t)hi, 0};
 }
 
-// Every wave's LDS accesses are done; loads from memory stay under way.
-__device__ __forceinline__ void meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
-
 // First half: an item is 16 gate rows and their 16 up rows x a tile of an expert's tokens. A
 // workgroup keeps to its rows and takes every gridDim.y'th tile. A wave's blocks of K over all of
-// its items are one sequence, of which it has kAhead under way. Every turn loads, past the
-// end the last tile's again: a load that a branch leaves out would make every wait one for
-// all loads.
+// its items are one sequence, of which it has kAhead under way. A turn but the last loads as
+// many, past the end the last tile's again: a load that a branch leaves out would make every
+// wait one for all loads.
 template <int TERMS, int kAhead>
 __global__ __launch_bounds__(64 * kWaves, 4) void k_f8_gate_up(Fp8LayerArgs a) {
   typedef Vectors<TERMS> Vec;
@@ -456,7 +438,6 @@ __global__ __launch_bounds__(64 * kWaves, 4) void k_f8_gate_up(Fp8LayerArgs a) {
     }
     if (++done < steps) return;
     done = 0;
-    if (at >= tiles) return;
     // the item's sums meet; another buffer each time, so that one barrier does
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -492,13 +473,17 @@ __global__ __launch_bounds__(64 * kWaves, 4) void k_f8_gate_up(Fp8LayerArgs a) {
   Unit f[kAhead];
 #pragma unroll
   for (int k = 0; k < kAhead; ++k) load(f[k]);
-  while (at < tiles) {
+  int left = ((tiles - 1 - (int)blockIdx.y) / (int)gridDim.y + 1) * steps;  // blocks of K
+  for (; left > kAhead; left -= kAhead) {
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       products(f[k]);
       load(f[k]);
     }
   }
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k)
+    if (k < left) products(f[k]);
 }
 
 // Second half: 8 OPS rows of down x every token, over all tiles. Waves are KS x NG: wave (s, g)
@@ -588,7 +573,6 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_f8_down(Fp8LayerArgs a, DownS
       }
       if (++done < steps) return;
       done = 0;
-      if (at >= end) return;
       const Fp8Tile t = uniform(&tile[at]);
 #pragma unroll
       for (int k = 0; k < OPS; ++k) {
@@ -605,13 +589,17 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_f8_down(Fp8LayerArgs a, DownS
     Unit f[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) load(f[k]);
-    while (at < end) {
+    int left = at < end ? ((end - 1 - at) / groups + 1) * steps : 0;  // blocks of K
+    for (; left > kAhead; left -= kAhead) {
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         products(f[k]);
         load(f[k]);
       }
     }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (k < left) products(f[k]);
     meet();
 #pragma unroll
     for (int o = 0; o < kOut; ++o) {
