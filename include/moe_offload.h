@@ -590,10 +590,10 @@ moe_status moe_fp8_quantize(const moe_fp8_quantize_args* args, moe_stream stream
 /* Product of such codes:
  *   out[t][n] = act( sum_b s_x[t][b] s_w[n/128][b] sum_{k in block b} q_x[t][k] q_w[n][k]
  *                    + bias[n] + y_in[t][n] + res[t][n] )
- * summed in fp32, rounded once. For bf16 outputs of more than 16 tokens a block's inner sum
- * comes from the 8-bit matrix instruction, which cuts each of eight neighbouring products to
+ * summed in fp32, rounded once. For bf16 outputs of more than 4 tokens a block's inner sum may
+ * come from the 8-bit matrix instruction, which cuts each of eight neighbouring products to
  * 2^-13 of the largest one's binade (1.5e-5 of the sum on normal codes, where the output's own
- * rounding is 2^-8); fp32 outputs, and up to 16 tokens, are summed from exact products. A block's
+ * rounding is 2^-8); fp32 outputs, and up to 4 tokens, are summed from exact products. A block's
  * scales are multiplied with each other first. y_in, res and in-place outputs as in
  * moe_int8_matmul. */
 typedef struct {

@@ -178,6 +178,10 @@ def test_codes_of_many_rows(moe):
 
 PRODUCT = [
     # T, N, K, out, bias, y, res, pad, wide codes
+    (4, 6200, 400, "bf16", False, True, True, 16, True), (5, 6200, 400, "bf16", True, False, True, 16, True), (8, 100, 144, "bf16", True, True, True, 16, True),
+    (9, 100, 144, "bf16", False, True, False, 0, True), (8, 6150, 2064, "f32", True, False, True, 16, False), (3, 33, 8208, "bf16", False, False, True, 0, True),
+    (7, 50, 131056, "f32", False, False, False, 0, False), (40, 33, 131056, "bf16", False, False, False, 0, False),
+    (64, 200, 384, "bf16", False, False, False, 0, True), (48, 72, 512, "f32", True, False, False, 0, True), (256, 300, 640, "bf16", True, True, False, 16, True),
     (1, 1, 16, "f32", False, False, False, 0, True), (1, 16, 128, "bf16", True, False, True, 0, True),
     (2, 17, 144, "f32", True, True, True, 16, True), (5, 130, 2064, "bf16", False, True, False, 32, False),
     (16, 300, 1024, "f32", False, False, True, 0, True), (1, 7168, 7168, "bf16", False, False, True, 0, False),
@@ -216,7 +220,7 @@ def test_product(moe, T, N, K, out, bias, y, res, pad, wide):
     o = Padded(T, N, N + 2 * pad, dt)
     moe.fp8_matmul(qx.m, sx.m, qw.m, sw.m, o.m, bias=b, y_in=ym.m if y else None, res=rm.m if res else None)
     x, w = _full(qx.m, sx.m), _full(qw.m, sw.m, B)
-    want, tol = x @ w.T, _product_tolerance(x, w, out == "f32" or T <= 16)
+    want, tol = x @ w.T, _product_tolerance(x, w, out == "f32" or T <= 4)
     for more in (b, ym.m if y else None, rm.m if res else None):
         if more is not None:
             want = want + more.to(D)
@@ -332,6 +336,8 @@ LAYER = [
     (64, 144, 272, 3, 1, "f32", 0, True), (48, 2064, 160, 70, 8, "bf16", 0, False), (1, 2048, 768, 128, 8, "bf16", 0, False),
     (16, 2048, 768, 128, 8, "bf16", 0, False), (5, 7168, 400, 24, 6, "bf16", 0, False), (9, 1024, 2064, 130, 7, "f32", 0, False),
     (4, 64, 32, 1024, 32, "bf16", 0, True), (64, 32, 16, 1000, 32, "f32", 0, True), (31, 16, 272, 6, 3, "bf16", 0, True),
+    # more assignments than LDS has places for: windows of them
+    (64, 4112, 272, 40, 32, "bf16", 0, True), (64, 5136, 2048, 8, 8, "bf16", 0, False), (40, 2064, 1040, 33, 32, "f32", 0, False),
     (6, 3216, 2048, 16, 4, "bf16", 0, True), (11, 32, 16384, 4, 2, "bf16", 0, False), (3, 16400, 32, 6, 2, "bf16", 0, False),
 ]
 
@@ -436,7 +442,77 @@ def test_layer_beyond_32_bits(moe):
     _check_layer(s, li, o["y"].m, o["x_out"].m, flat["topk_ids"], flat["topk_w"])
 
 
+def test_beyond_32_bits(moe):
+    """Matrices of more than 2^32 elements: their last rows and channels, and rows behind the last."""
+    g, K, N = _gen(7), 8208, (1 << 19) + 1040
+    w = torch.empty(N, K, device="cuda", dtype=F8)
+    for i in range(0, N, 1 << 16):
+        w[i:i + (1 << 16)] = _normal(g, min(1 << 16, N - i), K)
+    assert w.numel() > 1 << 32
+    sw = torch.exp(_rn(g, _up(N), _up(K))) / 1e4
+    for T in (2, 40):
+        x, sx = _normal(g, T, K), torch.exp(_rn(g, T, _up(K)))
+        out = torch.empty(T, N, device="cuda")
+        moe.fp8_matmul(x, sx, w, sw, out)
+        lo = (N - 700) // B * B
+        xs, ws = _full(x, sx), _full(w[lo:], sw[lo // B:], B)
+        assert bool(((out[:, lo:].to(D) - xs @ ws.T).abs() <= _product_tolerance(xs, ws, True) + (xs @ ws.T).abs() * R32).all())
+    # as many tokens, the weights being few
+    x, sx, few, sf = w, torch.exp(_rn(g, N, _up(K))), _normal(g, 24, K), torch.exp(_rn(g, 1, _up(K))) / 1e4
+    out = torch.empty(N, 24, device="cuda")
+    moe.fp8_matmul(x, sx, few, sf, out)
+    xs, ws = _full(x[-300:], sx[-300:]), _full(few, sf, B)
+    assert bool(((out[-300:].to(D) - xs @ ws.T).abs() <= _product_tolerance(xs, ws, True) + (xs @ ws.T).abs() * R32).all())
+    del w, x, out
+    T, H = 1 << 20, 4104
+    v = torch.empty(T, H, device="cuda", dtype=torch.bfloat16)
+    for i in range(0, T, 1 << 17):
+        v[i:i + (1 << 17)] = _rn(g, 1 << 17, H).to(torch.bfloat16)
+    for rows in (1, 128):
+        q, s = torch.empty(T, H, device="cuda", dtype=F8), torch.empty(-(-T // rows), _up(H), device="cuda")
+        moe.fp8_quantize(v, q, s, block_rows=rows)
+        wq, ws = _want_codes(v[-128:].to(D), rows)
+        assert torch.equal(q[-128:].to(D), wq) and bool(((s[-128 // rows:].to(D) - ws).abs() <= ws * R32).all())
+
+
 # ----------------------------------------------------------------------------- streams, graphs, a run of them
+
+
+def test_two_threads(moe):
+    """Calls from two threads on streams of their own overlap, each with its own workspace."""
+    import threading
+    jobs, bad = [], []
+    for n in ((1, 1024, 400, 32, 4), (30, 512, 272, 20, 3)):
+        T, H, I, E, k = n  # noqa: E741
+        s = _layer_inputs(T, H, I, E, k, "bf16", T)
+        want = moe.fp8_layer(**s, y=torch.empty(T, H, device="cuda"), workspace=_workspace(moe, *n)).clone()
+        w, sw, q, sc = _normal(_gen(1), H, H), torch.full((_up(H), _up(H)), 0.01, device="cuda"), torch.empty(T, H, device="cuda", dtype=F8), \
+            torch.empty(T, _up(H), device="cuda")
+        p = torch.empty(T, H, device="cuda")
+        moe.fp8_quantize(s["x"], q, sc)
+        moe.fp8_matmul(q, sc, w, sw, p)
+        jobs.append((n, s, want, w, sw, p.clone()))
+    torch.cuda.synchronize()
+
+    def work(n, s, want, w, sw, prod):
+        T, H = n[:2]
+        stream, ws, y = torch.cuda.Stream(), _workspace(moe, *n), torch.empty(T, H, device="cuda")
+        q, sc, p = torch.empty(T, H, device="cuda", dtype=F8), torch.empty(T, _up(H), device="cuda"), torch.empty(T, H, device="cuda")
+        torch.cuda.synchronize()
+        for _ in range(50):
+            moe.fp8_layer(**s, y=y, workspace=ws, stream=stream)
+            moe.fp8_quantize(s["x"], q, sc, stream=stream)
+            moe.fp8_matmul(q, sc, w, sw, p, stream=stream)
+        stream.synchronize()
+        if not (torch.equal(y, want) and torch.equal(p, prod)):
+            bad.append(n)
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
 
 
 def test_other_stream(moe):
@@ -552,7 +628,7 @@ def test_a_run_of_them(moe):
     assert bool(((full - w.to(D)).abs() <= w.to(D).abs() * 2.0 ** -4 * (1 + R32) + sw.to(D).repeat_interleave(B, 0).repeat_interleave(B, 1) * 2.0 ** -10).all())
     xs = _full(q, sc)
     want = xs @ full.T + x.to(D)
-    tol = _product_tolerance(xs, full, True) * 1.01 + want.abs() * (RBF + 4 * R32) + x.to(D).abs() * R32
+    tol = _product_tolerance(xs, full, False) * 1.01 + want.abs() * (RBF + 4 * R32) + x.to(D).abs() * R32
     assert bool(((x1.to(D) - want).abs() <= tol).all())
     _check_layer(layer, flat["logits"], o["y"].m, o["x_out"].m, flat["topk_ids"], flat["topk_w"])
     assert bool(((x2.to(D) - (x1.to(D) + o["y"].m.to(D))).abs() <= (x1.to(D) + o["y"].m.to(D)).abs() * (RBF + 2 * R32)).all())
