@@ -23,7 +23,6 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t f8i4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8v __attribute__((ext_vector_type(8)));
-typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(1))) const f8i4 g_f8i4;
 
 // Eight codes as bf16 (every e4m3 number is one; a NaN stays one).

@@ -427,12 +427,9 @@ static void gemm_tile(const Fp8Args& a, hipStream_t s) {
   hipLaunchKernelGGL((k_fp8_gemm<WM, WN, TM, TN, RING, KG, BF16>), dim3(mt * nt), dim3(64 * WM * WN * KG), 0, s, a, mt);
 }
 
-#ifndef FORCE_TILE
-#define FORCE_TILE(x) (x)
-#endif
 template <bool BF16>
 static void gemm(const Fp8Args& a, hipStream_t s) {
-  switch (FORCE_TILE(choose_tile(a.T, a.N, BF16 ? 0 : 1))) {
+  switch (choose_tile(a.T, a.N, BF16 ? 0 : 1)) {
     case 0:
       if constexpr (BF16) return gemm_tile<BF16, 2, 4, 2, 2, 3, 1>(a, s);
     case 1: return gemm_tile<BF16, 2, 4, 2, 1, 4, 1>(a, s);
