@@ -9,8 +9,14 @@
 // is the exact sum of three bf16 terms (8 bits of its mantissa each), so that fp32
 // activations and the intermediate h, which stays in fp32, take three products.
 //
-// Every workgroup forms the routing's tables by itself, in LDS: a launch of its own would
-// cost more.
+// Three launches: the router (which also lays out x as the products read it), the first half, the
+// second half. Every workgroup of the first half forms the routing's tables by itself, in LDS
+// (2.5 us for one token), instead of a launch of its own; one leaves them for the second half.
+//
+// What bounds it: a token on 6 experts of 7168 / 2048 (264 MB) takes 61 us, of which gate and up
+// 31 (5.7 TB/s), down 18.5 (4.8), the router 6; a token on 8 of 2048 / 768 (38 MB) 18 us, of which
+// 3 + 10 + 6: there the starts of three short bursts count, not the bytes (7.5 us).
+// 16 tokens take 72 us on 2048 / 768 and 346 to 384 on 7168 / 2048 (4.2 to 5.2 TB/s).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -496,10 +502,11 @@ struct DownShape {
   int ks, slots, window;
 };
 
-template <typename ACT, int WAVES, int OPS, int kAhead>
+template <typename ACT, int WAVES, int OPS>
 __global__ __launch_bounds__(64 * WAVES, 4) void k_f8_down(Fp8LayerArgs a, DownShape d) {
   typedef Vectors<3> Vec;
   static_assert(Vec::kTokens == kDownTokens, "the tables' tiles");
+  constexpr int kAhead = 3;  // six or four: a token on 2048 / 768 20.1 us (18.8), the others the same
   constexpr int kOf = kRows * OPS;                                     // rows of the workgroup
   constexpr int kOut = (kF8LayerTokens * kOf - 1) / (64 * WAVES) + 1;  // outputs of a thread
   extern __shared__ __attribute__((aligned(16))) float acc[];  // [ks][slots][kOf]
@@ -656,14 +663,7 @@ void down(const Fp8LayerArgs& a, hipStream_t s) {
   d.slots = std::min(n, room);
   d.window = n <= room ? n : room - (kDownTokens - 1);
   const size_t lds = (size_t)ks * d.slots * place + (sizeof(Fp8Tile) + sizeof(float) + sizeof(uint32_t)) * n;
-  const int groups = WAVES / ks, most = ((n - 1) / groups + 1) * ((IB - 1) / ks + 1);  // blocks of K of a wave
-#define DOWN(AHEAD) \
-  hipLaunchKernelGGL((k_f8_down<ACT, WAVES, OPS, AHEAD>), dim3(a.H / (kRows * OPS)), dim3(64 * WAVES), lds, s, a, d)
-  if (most <= 3)
-    DOWN(3);
-  else
-    DOWN(OPS == 1 ? 6 : 4);
-#undef DOWN
+  hipLaunchKernelGGL((k_f8_down<ACT, WAVES, OPS>), dim3(a.H / (kRows * OPS)), dim3(64 * WAVES), lds, s, a, d);
 }
 
 template <typename ACT>
@@ -673,10 +673,15 @@ void layer(const Fp8LayerArgs& a, hipStream_t s) {
   hipLaunchKernelGGL((k_f8_router<ACT>), dim3(rows + a.T), dim3(kRouterThreads), 0, s, a, rows);
   const int per = a.I / 16, most = a.T * a.k;  // blocks of rows; tiles
   const dim3 grid(per, std::min(most, std::max(1, 512 / per)));
-  if (f8_blocks(a.H) <= 2 * kWaves && (int)grid.y == most)  // two blocks of K a wave at most
+  // Where no wave has more than two blocks of K, two under way: the third would be loaded for nothing (a token
+  // on 2048 / 768 18.8 us, 19.8 with three; 7 tokens on 400 / 208 15.7, 16.1).
+  if (f8_blocks(a.H) <= 2 * kWaves && (int)grid.y == most)
     hipLaunchKernelGGL((k_f8_gate_up<kTerms, 2>), grid, dim3(64 * kWaves), 0, s, a);
   else
     hipLaunchKernelGGL((k_f8_gate_up<kTerms, 3>), grid, dim3(64 * kWaves), 0, s, a);
+  // Workgroups of 16 rows leave CUs idle while there are at most 256 of them; 8 rows and twice the waves then
+  // take 18.8 us for a token on 2048 / 768 (16 rows: 20.4), 72 for 16 tokens (80). Above, 16 rows read each
+  // vector half as often: a token on 7168 / 2048 61 us (8 rows: 80), 16 tokens 385 (461).
   if (a.H / 16 <= 256)
     down<ACT, 16, 1>(a, s);
   else
