@@ -14,8 +14,8 @@
 // (2.5 us for one token), instead of a launch of its own; one leaves them for the second half.
 //
 // What bounds it: a token on 6 experts of 7168 / 2048 (264 MB) takes 61 us, of which gate and up
-// 31 (5.7 TB/s), down 18.5 (4.8), the router 6; a token on 8 of 2048 / 768 (38 MB) 18 us, of which
-// 3 + 10 + 6: there the starts of three short bursts count, not the bytes (7.5 us).
+// 31 (5.7 TB/s), down 18.7 (4.7), the router 6; a token on 8 of 2048 / 768 (38 MB) 18 us, of which
+// 3 + 9 + 6: there the starts of three short bursts count, not the bytes (7.5 us).
 // 16 tokens take 72 us on 2048 / 768 and 346 to 384 on 7168 / 2048 (4.2 to 5.2 TB/s).
 #include <hip/hip_runtime.h>
 
