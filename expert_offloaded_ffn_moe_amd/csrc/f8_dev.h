@@ -25,10 +25,11 @@ typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8v __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(1))) const f8i4 g_f8i4;
 
-// Eight codes as bf16 (every e4m3 number is one; a NaN stays one).
-__device__ __forceinline__ bf16x8v f8_to_bf16(int lo, int hi) {
-  const bf16x2v a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true);
-  const bf16x2v c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true);
+// Eight codes as bf16 (every e4m3 number is one, and so is its product with a power of two from
+// 2^-100 to 2^100; a NaN stays one).
+__device__ __forceinline__ bf16x8v f8_to_bf16(int lo, int hi, float power = 1.f) {
+  const bf16x2v a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, power, false), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, power, true);
+  const bf16x2v c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, power, false), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, power, true);
   return bf16x8v{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 

@@ -365,13 +365,27 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t values_buffer(const uint16_t* 
 }
 constexpr uint32_t kNoVector = 1u << 30;
 
+// A block's scale as a power of two from 2^-100 to 2^100, which the codes' conversion takes, and
+// the rest, of size 1 to 2 where the scale is in that range. So what is summed has the size of the
+// weights, not of their codes, and leaves fp32 only where the weights' own sum does; no bit of
+// a sum that stays inside changes.
+struct BlockScale {
+  float power, rest;
+  __device__ __forceinline__ explicit BlockScale(float s) {
+    constexpr uint32_t kLeast = (127u - 100) << 23, kMost = (127u + 100) << 23;
+    const uint32_t e = min(max(__float_as_uint(s) & 0x7F800000u, kLeast), kMost);
+    power = __uint_as_float(e);
+    rest = s * __uint_as_float((254u << 23) - e);
+  }
+};
+
 // The sums of 8 rows with a block's values, all parities: added, scaled, to s.
-__device__ __forceinline__ void add_products(const f8i4& w, const Values& x, float scale, f32x4& s) {
+__device__ __forceinline__ void add_products(const f8i4& w, const Values& x, const BlockScale& scale, f32x4& s) {
   f32x4 p = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int c = 0; c < 2; ++c) p = mfma_bf16(f8_to_bf16(w[2 * c], w[2 * c + 1]), x.v[c], p);
+  for (int c = 0; c < 2; ++c) p = mfma_bf16(f8_to_bf16(w[2 * c], w[2 * c + 1], scale.power), x.v[c], p);
 #pragma unroll
-  for (int v = 0; v < 4; ++v) s[v] = fmaf(scale, p[v], s[v]);
+  for (int v = 0; v < 4; ++v) s[v] = fmaf(scale.rest, p[v], s[v]);
 }
 
 __device__ __forceinline__ Fp8Tile uniform(const Fp8Tile* tile) {
@@ -437,10 +451,11 @@ __global__ __launch_bounds__(64 * kWaves, 4) void k_f8_gate_up(Fp8LayerArgs a) {
   f32x4 sum[4] = {};
   auto products = [&](const Unit& f) {
     if (wave + done * kWaves < HB) {
-      add_products(f.w[0], f.x, f.sg, sum[0]);
-      add_products(f.w[1], f.x, f.sg, sum[1]);
-      add_products(f.w[2], f.x, f.su, sum[2]);
-      add_products(f.w[3], f.x, f.su, sum[3]);
+      const BlockScale sg(f.sg), su(f.su);
+      add_products(f.w[0], f.x, sg, sum[0]);
+      add_products(f.w[1], f.x, sg, sum[1]);
+      add_products(f.w[2], f.x, su, sum[2]);
+      add_products(f.w[3], f.x, su, sum[3]);
     }
     if (++done < steps) return;
     done = 0;
@@ -575,8 +590,9 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_f8_down(Fp8LayerArgs a, DownS
     f32x4 sum[OPS] = {};           // rows 2 q and 2 q + 1 of each eight
     auto products = [&](const Unit& f) {
       if (ks + done * d.ks < IB) {
+        const BlockScale scale(f.s);
 #pragma unroll
-        for (int k = 0; k < OPS; ++k) add_products(f.w[k], f.h, f.s, sum[k]);
+        for (int k = 0; k < OPS; ++k) add_products(f.w[k], f.h, scale, sum[k]);
       }
       if (++done < steps) return;
       done = 0;
