@@ -6,8 +6,8 @@
 //
 // The router's sums are in fp64, so that which experts a token takes does not turn on the
 // order of the sums. A bf16 x fp8 product is exact in the bf16 MFMA (f8_dev.h); an fp32 value
-// is the exact sum of three bf16 terms (8 bits of its mantissa each), so that fp32
-// activations and the intermediate h, which stays in fp32, take three products.
+// is the exact sum of three bf16 terms (8 bits of its mantissa each) with powers of two, so that
+// fp32 activations and the intermediate h, which stays in fp32, take three products.
 //
 // Three launches: the router (which also lays out x as the products read it), the first half, the
 // second half. Every workgroup of the first half forms the routing's tables by itself, in LDS
@@ -70,14 +70,19 @@ __device__ __forceinline__ double wave_sum_63(double v) {
   return v;
 }
 
-// f as three bf16 terms: 8 bits each, the last one exact; an infinity or a NaN stays whole in the first.
+// f as three bf16 terms, f = t0 + 2^-7 t1 + 2^-16 t2 for every finite f: its first 8 bits, cut; what that
+// leaves, under 2^-7 of f's binade and held 2^7 fold, rounded; what that leaves, held 2^9 fold again. So
+// none is larger than f (than 2^-125, of the smallest f, whose terms are bf16 numbers too), and the
+// sums of none leave fp32 where f's own do not. An infinity or a NaN stays whole in the first.
+constexpr float kSecond = 0x1p-7f, kThird = 0x1p-9f;  // the second to the first, the third to the second
 __device__ __forceinline__ void three_terms(float f, uint16_t* t) {
   typedef OutElem<true> Bf;
-  t[0] = Bf::rounded(f);
   const bool finite = fabsf(f) < INFINITY;
-  const float r = f - Bf::load(t[0]);
-  t[1] = finite ? Bf::rounded(r) : 0;
-  t[2] = finite ? Bf::rounded(r - Bf::load(t[1])) : 0;
+  const uint32_t u = __float_as_uint(f);
+  const float r = finite ? (f - __uint_as_float(u & 0xFFFF0000u)) * (1.f / kSecond) : 0.f;
+  t[0] = finite ? (uint16_t)(u >> 16) : Bf::rounded(f);
+  t[1] = Bf::rounded(r);
+  t[2] = (uint16_t)(__float_as_uint((r - Bf::load(t[1])) * (1.f / kThird)) >> 16);
 }
 
 // The first `rows` workgroups take a row of the router each, H split over their threads, the
@@ -338,11 +343,11 @@ struct Vectors {
   static constexpr int kTokens = TERMS == 1 ? 8 : 2;
   static __device__ __forceinline__ int token(int v) { return TERMS == 1 ? v : v / 3; }
   static __device__ __forceinline__ int term(int v) { return TERMS == 1 ? 0 : v % 3; }
-  // the sum over the parities, and over the terms; in the first lane of a token's
+  // the sum over the parities, and over the terms with their sizes; in the first lane of a token's
   static __device__ __forceinline__ float whole(float v) {
     constexpr int kShl2 = 0x102, kShl4 = 0x104;  // row_shl: the lane 2 (4) on in the row of 16
     v += dppf<kDppXor1, 0xF>(0.f, v);
-    return TERMS == 1 ? v : v + (dppf<kShl2, 0xF>(0.f, v) + dppf<kShl4, 0xF>(0.f, v));
+    return TERMS == 1 ? v : fmaf(fmaf(dppf<kShl4, 0xF>(0.f, v), kThird, dppf<kShl2, 0xF>(0.f, v)), kSecond, v);
   }
   static __device__ __forceinline__ int lane_of(int token) { return TERMS == 1 ? 2 * token : 6 * token; }
   static __device__ __forceinline__ bool is_first(int column) { return TERMS == 1 ? column % 2 == 0 : column == 0 || column == 6; }

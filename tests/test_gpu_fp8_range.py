@@ -12,8 +12,79 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
 
+TOP = torch.finfo(torch.float32).max
+BF_TOP = 255.0 * 2.0 ** 120  # bfloat16's largest; from half a step above it on, rounding gives infinity
+
+
+@pytest.mark.parametrize("value", [TOP, -TOP, BF_TOP + 2.0 ** 119, -BF_TOP - 2.0 ** 119, BF_TOP + 2.0 ** 119 - 2.0 ** 104, BF_TOP,
+                                   1.0 + 2.0 ** -23, -1.7182819, 2.0 ** -100 * (2 - 2.0 ** -23), 2.0 ** -112 * 1.2345678,
+                                   -(2.0 ** -118) * (1 + 2.0 ** -23), 2.0 ** -126, 2.0 ** -126 * (2 - 2.0 ** -23), 2.0 ** -130 * 1.171875,
+                                   2.0 ** -149])
+def test_any_size_of_activation_and_intermediate(moe, value):
+    """One activation of that size, one intermediate of 64 (or 1) times it, and an output of that
+    times a code and a scale. The other products are of zeros."""
+    _say("size:", value)
+    v = torch.tensor(value, device="cuda").item()
+    H, I = 288, 144  # noqa: E741
+    s = dict(x=torch.zeros(1, H, device="cuda"), router_w=None, k=1)
+    s["q_gu"], s["q_dn"] = torch.zeros(1, 2 * I, H, device="cuda"), torch.zeros(1, H, I, device="cuda")
+    s["s_gu"], s["s_dn"] = torch.ones(1, 2, _up(I), _up(H), device="cuda"), torch.ones(1, _up(H), _up(I), device="cuda")
+    # gate of the intermediate's element 130: 64 from x's element 0, whose silu is 64 in fp32; up: v from element 200
+    s["x"][0, 0], s["x"][0, 200] = 1.0, v
+    s["q_gu"][0, 130, 0], s["q_gu"][0, I + 130, 200] = 64.0, 1.0
+    large = abs(v) > 1
+    if large:
+        s["s_gu"][0, 1, 1, 1] = 2.0 ** -6
+    codes = torch.arange(H, device="cuda") % 15 - 7.0
+    s["q_dn"][0, :, 130] = codes
+    s["s_dn"][:] = 2.0 ** (-100 if large else 100)
+    s["q_gu"], s["q_dn"] = s["q_gu"].to(F8), s["q_dn"].to(F8)
+    y = moe.fp8_layer(**s, y=torch.empty(1, H, device="cuda"), workspace=_workspace(moe, 1, H, I, 1, 1),
+                      logits_in=torch.zeros(1, 1, device="cuda"))
+    h = v if large else 64.0 * v
+    want = codes.to(D) * h * (2.0 ** -100 if large else 2.0 ** 100)
+    # u and h are exact; a code times h in three parts: two additions that may cut (2^-23 each)
+    err = (y[0].to(D) - want).abs()
+    assert bool((err <= want.abs() * 4 * R32).all()), (v, y[0, :15].tolist(), want[:15].tolist())
+    # x of that size where every weight is 0: as if it were not there
+    codes = torch.zeros(1, 2 * I, H, device="cuda")
+    codes[0, 130, 0], codes[0, I + 130, 0] = 64.0, 1.0
+    s["q_gu"] = codes.to(F8)
+    ys = []
+    for at in (v, 0.0):
+        s["x"][0, 200] = at
+        ys.append(moe.fp8_layer(**s, y=torch.empty(1, H, device="cuda"), workspace=_workspace(moe, 1, H, I, 1, 1),
+                                logits_in=torch.zeros(1, 1, device="cuda")))
+    assert bool(torch.isfinite(ys[0]).all()) and torch.equal(*ys)
+
+
+@pytest.mark.parametrize("low", [2.0 ** -7 - 2.0 ** -23, 2.0 ** -8 - 2.0 ** -23, 2.0 ** -8, 2.0 ** -9 + 2.0 ** -17])
+def test_sums_next_to_the_range_s_end(moe, low):
+    """1.5 times a value of fp32's last binade, as the up product and as an output: finite, whatever
+    parts the value goes in."""
+    v = torch.tensor(2.0 ** 127 * (1.3125 + low), device="cuda").item()
+    H, I = 144, 16  # noqa: E741
+    q_gu, q_dn, x = torch.zeros(1, 2 * I, H, device="cuda"), torch.zeros(1, H, I, device="cuda"), torch.zeros(1, H, device="cuda")
+    s_gu, s_dn = torch.ones(1, 2, 1, 2, device="cuda"), torch.ones(1, 2, 1, device="cuda")
+    x[0, 3], x[0, 130] = 64.0, v
+    q_gu[0, 2, 3], q_gu[0, I + 2, 130] = 1.0, 1.5  # gate 64, up 1.5 v, the intermediate 64 times that times the scale
+    q_dn[0, :, 2] = 1.0
+    run = lambda **c: moe.fp8_layer(x, None, q_gu.to(F8), c["s_gu"], q_dn.to(F8), c["s_dn"], 1, torch.empty(1, H, device="cuda"),  # noqa: E731
+                                    _workspace(moe, 1, H, I, 1, 1), logits_in=torch.zeros(1, 1, device="cuda"))
+    s_gu[0, 0], s_dn[:] = 2.0 ** -12, 2.0 ** 5  # gate 2^-6, whose silu is 2^-7 (1 + 2^-7 + ...)
+    silu = 2.0 ** -6 / (1 + torch.exp(torch.tensor(-(2.0 ** -6), dtype=D))).item()
+    y = run(s_gu=s_gu, s_dn=s_dn)
+    want = 1.5 * v * silu * 2.0 ** 5
+    # u three additions that may cut; exp, 1 +, the quotient and the product; the output three again
+    assert bool(((y.to(D) - want).abs() <= abs(want) * (6 + 8 + 6) * R32).all()), (y[0, :3].tolist(), want)
+    q_dn[0, :, 2], q_gu[0, I + 2, 130] = 1.5, 1.0
+    s_gu[0, 0], s_gu[0, 1] = 1.0, 2.0 ** -6
+    y = run(s_gu=s_gu, s_dn=torch.ones_like(s_dn))
+    assert bool(((y.to(D) - 1.5 * v).abs() <= 1.5 * v * 6 * R32).all()), (y[0, :3].tolist(), 1.5 * v)
+
+
 @pytest.mark.parametrize("T", [1, 11])
-@pytest.mark.parametrize("act,by", [("bf16", 110), ("f32", 110)])
+@pytest.mark.parametrize("act,by", [("bf16", 110), ("bf16", -110), ("f32", 110), ("f32", -105)])
 def test_sizes_between_activations_and_scales(moe, T, act, by):
     """Activations of 2^by times the size on scales of 2^-by times theirs, and an intermediate so on
     down's: the same bits, also where a block's sum of codes times activations alone leaves fp32's
