@@ -204,9 +204,10 @@ __device__ __forceinline__ void choose_of(const float* logits, int E, int k, int
     id = lane == j ? win : id;
   }
   const float v = logit_of(mine), top = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 0));
-  const float p = lane < k && v != -INFINITY ? expf(v - top) : 0.f;
+  const bool counts = lane < k && v != -INFINITY;
+  const float p = counts ? expf(v - top) : 0.f;
   const float sum = wave_sum(p);
-  w = sum == 0.f ? 0.f : p / sum;  // every logit -infinity: nothing
+  w = counts ? p / sum : 0.f;  // 0 also where the sum is NaN, for another logit's sake, or 0
   const uint64_t some = __ballot(w != 0.f);
   rank = 0;
   for (int j = 0; j < k; ++j) rank += (some >> j & 1) && __builtin_amdgcn_readlane(id, j) < id;

@@ -148,3 +148,38 @@ def test_scales_of_every_kind(moe):
         hit = torch.zeros(n, H, dtype=torch.bool, device="cuda")
         hit[2, B:] = True
         assert bool((~torch.isfinite(y[hit])).all()) and bool(torch.isfinite(y[~hit]).all())
+
+
+def test_masked_experts_of_tokens_that_are_not_finite(moe):
+    """A logit of -infinity gives weight 0, and its expert is not read, also where another logit of
+    the token is NaN or infinite."""
+    T, H, I, E, k = 6, 144, 32, 70, 4  # noqa: E741
+    s = _layer_inputs(T, H, I, E, k, "bf16", 71)
+    inf, nan = float("inf"), float("nan")
+    li = torch.full((T, E), -inf, device="cuda")
+    li[0, 33], li[1, 69], li[2, [5, 66]] = nan, inf, torch.tensor([inf, 2.0], device="cuda")
+    li[3, [7, 8, 9]] = torch.tensor([nan, 1.0, inf], device="cuda")
+    li[4, 0], li[5, 12] = 1.0, torch.finfo(torch.float32).min
+    for some in (list(range(T)), [0], [1], [2], [3], [4]):
+        n = len(some)
+        o, flat = _outputs(n, H, E, k, torch.bfloat16)
+        moe.fp8_layer(**{**s, "x": s["x"][some].contiguous()}, y=o["y"].m, x_out=o["x_out"].m, workspace=_workspace(moe, n, H, I, E, k),
+                      logits_in=li[some].contiguous(), **flat)
+        chosen = li[some].gather(1, flat["topk_ids"].long())
+        masked = chosen == -inf
+        assert bool((flat["topk_w"][masked] == 0).all()), flat["topk_w"]
+        for t, i in enumerate(some):
+            w = flat["topk_w"][t][~masked[t]]
+            if i in (0, 1, 3):
+                assert bool(torch.isnan(w).all())
+            if i in (0, 1, 2, 3):
+                assert bool(torch.isnan(o["y"].m[t]).all())
+            else:
+                assert w.tolist() == [1.0] and bool(torch.isfinite(o["y"].m[t]).all())
+    # what is masked may hold NaN codes
+    want = moe.fp8_layer(**s, y=torch.empty(T, H, device="cuda"), workspace=_workspace(moe, T, H, I, E, k), logits_in=li).clone()
+    for name in ("q_gu", "q_dn"):
+        s[name] = s[name].clone()
+        s[name].view(torch.uint8)[torch.isinf(li).logical_and(li < 0).all(0)] = 0x7F
+    y = moe.fp8_layer(**s, y=torch.empty(T, H, device="cuda"), workspace=_workspace(moe, T, H, I, E, k), logits_in=li)
+    assert torch.equal(y.nan_to_num(), want.nan_to_num())
