@@ -20,10 +20,11 @@
 namespace moe {
 namespace {
 
-// Tokens up to which this kernel runs: 8 on 4096 x 7168 9.3 us (tiles 11.0), on 2048 x 2048 5.0 (5.5), 4 on
-// 7168 x 7168 12.2 (12.4); where there are workgroups for more than one a CU, 8 go to tiles: 7168 x
-// 7168 13.1 (12.5), 14336 x 4096 17.0 (15.7).
-constexpr int kSkinnyRows = 8, kSkinnyRowsWide = 4, kWideGrid = 384;
+// Tokens up to which this kernel runs, on any weights, so that how exact a token's sums are turns on the
+// number of tokens alone: 8 on 4096 x 7168 9.0 us (fp32 tiles 11.1), on 7168 x 7168 12.9 (13.0), on 2048 x
+// 2048 5.3 (5.9), on 14336 x 4096 17.7 (16.4); bf16 tiles, whose products are cut, take 9.1, 12.4, 5.4 and
+// 14.9.
+constexpr int kSkinnyRows = 8;
 constexpr int kWaves = 8;  // of a workgroup, splitting K
 
 // A wave has kAhead blocks of K under way. A turn but the last loads as many, past the end the last
@@ -110,7 +111,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void k_fp8_skinny(Fp8Args a) {
 
 void launch_fp8_matmul(const Fp8Args& a, bool out_bf16, hipStream_t s) {
   const int grid = (a.N - 1) / 16 + 1;
-  if (a.T > (grid < kWideGrid ? kSkinnyRows : kSkinnyRowsWide)) return launch_fp8_gemm(a, out_bf16, s);
+  if (a.T > kSkinnyRows) return launch_fp8_gemm(a, out_bf16, s);
   const size_t lds = sizeof(float) * a.T * f8_blocks(a.K);
   if (out_bf16)
     hipLaunchKernelGGL((k_fp8_skinny<true>), dim3(grid), dim3(64 * kWaves), lds, s, a);

@@ -10,11 +10,12 @@
 //
 // bf16 outputs take v_mfma_f32_16x16x128_f8f6f4 on the codes themselves, 32 of a row a lane. It
 // adds eight neighbouring products at a time, each cut to 2^-13 of the binade of the largest
-// (measured with one large product beside small ones; 1.5e-5 of the sum on normal codes, 2^-13 of
-// the sum of sizes on codes of every size alike), and those sums in fp32. The output's own
-// rounding of 2^-8 covers it; the bf16 MFMA, on which the products are exact, has half of its
-// rate and its operands have to be converted first. fp32 outputs take that one, four steps of
-// 32 a block.
+// (measured with one large product beside small ones), and those sums in fp32: of normal codes the
+// outputs are off by 1.5e-5, of codes of every size alike by 2^-13 of the sum of the products' sizes,
+// and never by more than 7 x 2^-13 of it. That is under the outputs' own rounding of 2^-8 unless
+// they nearly cancel. It is taken for its rate: the bf16 MFMA, on which the products are exact, has
+// half of it and its operands have to be converted first (2048 x 7168 x 7168 250 us in fp32, 121 so; 256 x
+// 7168 43 and 31; 64 x 7168 20.1 and 19.5). fp32 outputs take that one, four steps of 32 a block.
 //
 // LDS holds rows of 128 bytes, whose 16-byte pieces stand at places piece ^ (row / 2 % 8), so that
 // the lanes that a read serves at once use every bank once; loads go from memory to LDS

@@ -590,11 +590,14 @@ moe_status moe_fp8_quantize(const moe_fp8_quantize_args* args, moe_stream stream
 /* Product of such codes:
  *   out[t][n] = act( sum_b s_x[t][b] s_w[n/128][b] sum_{k in block b} q_x[t][k] q_w[n][k]
  *                    + bias[n] + y_in[t][n] + res[t][n] )
- * summed in fp32, rounded once. For bf16 outputs of more than 4 tokens a block's inner sum may
- * come from the 8-bit matrix instruction, which cuts each of eight neighbouring products to
- * 2^-13 of the largest one's binade (1.5e-5 of the sum on normal codes, where the output's own
- * rounding is 2^-8); fp32 outputs, and up to 4 tokens, are summed from exact products. A block's
- * scales are multiplied with each other first. y_in, res and in-place outputs as in
+ * summed in fp32, rounded once. Up to 8 tokens, and fp32 outputs of any number, are summed from
+ * exact products. For bf16 outputs of more tokens a block's inner sum comes from the 8-bit matrix
+ * instruction, which adds eight neighbouring products at a time, each cut to 2^-13 of the largest
+ * one's binade: at most 7 x 2^-13 of the sum of the products' sizes (2^-13 of it on codes of every
+ * size alike, 1.5e-5 of the outputs on normal codes, where their own rounding is 2^-8). What is cut
+ * does not cancel where the products or the addends do: who needs such outputs asks for fp32 ones.
+ * A block's two scales are multiplied with each other first, in fp32 (which holds fewer bits
+ * under 2^-126, and no number past 2^128). y_in, res and in-place outputs as in
  * moe_int8_matmul. */
 typedef struct {
   int32_t T;              /* tokens, 0..2^20 */
