@@ -30,11 +30,11 @@
 #include "f8_dev.h"
 #include "fp8.h"
 #include "int8_out.h"
+#include "tiles.h"
 
 namespace moe {
 namespace {
 
-typedef __attribute__((address_space(3))) void lvoid;
 typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kBK = kF8Block;  // bytes of a row in a step
@@ -42,30 +42,6 @@ constexpr int kBK = kF8Block;  // bytes of a row in a step
 __device__ __forceinline__ int swizzle(int r) { return (r >> 1) & 7; }
 
 __device__ const f8i4 zero_codes = {0, 0, 0, 0};
-
-// Workgroups are dealt to the 8 XCDs round-robin; each XCD gets one contiguous range of
-// the tiles, so that the tiles of its L2 share rows and channels.
-__device__ __forceinline__ int xcd_order(int b, int nb) {
-  constexpr int kXcd = 8;
-  const int per = nb / kXcd, rem = nb % kXcd, x = b % kXcd, i = b / kXcd;
-  return x < rem ? x * (per + 1) + i : rem * (per + 1) + (x - rem) * per + i;
-}
-
-// All but the newest N of this wave's loads are in, every LDS read too, and so it is for every
-// wave of the workgroup. One block: what follows reads LDS that other waves' loads wrote.
-template <int N>
-__device__ __forceinline__ void meet_with_loads_but() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
-}
-
-// 16 (4) bytes from each lane's address to LDS at `to` + 16 (4) lane; the compiler adds no wait
-// for them, meet_with_loads_but counts them. (A write of M0 is followed by one wait state.)
-__device__ __forceinline__ void load_to_lds(const void* from, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory", "m0");
-}
-__device__ __forceinline__ void load_one_to_lds(const void* from, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(to), "v"(from) : "memory", "m0");
-}
 
 // A row's (column's) 32 codes of a lane, and as four operands of the bf16 MFMA.
 struct Codes {
@@ -400,27 +376,7 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_fp8_gemm(Fp8Args a, int mti
 // the next best tile that gives, at K = 7168 in a loop over one set of buffers: 2048 x 7168 138 us
 // (128 x 128: 182), 1024 x 7168 58 (128 x 128: 79), 512 x 7168 39 (64 x 128: 51), 256 x 7168 25.5 (64 x 64:
 // 30.6), 128 x 7168 16.7 (64 x 128: 24.1), 64 x 7168 14.0 (64 x 64: 16.1), 32 x 7168 11.9 (64 x 32: 12.5).
-struct Tile {
-  int tokens, channels;
-  float cost;
-};
-constexpr int kCus = 256;
 constexpr Tile kTiles[] = {{128, 256, 0.93f}, {128, 128, 0.66f}, {64, 128, 0.43f}, {64, 64, 0.29f}, {64, 32, 0.235f}, {32, 32, 0.18f}};
-constexpr int kTileCount = sizeof(kTiles) / sizeof(kTiles[0]);
-
-static int choose_tile(int64_t T, int64_t N, int first) {
-  int best = first;
-  float least = 0.f;
-  for (int i = first; i < kTileCount; ++i) {
-    const int64_t n = ((T - 1) / kTiles[i].tokens + 1) * ((N - 1) / kTiles[i].channels + 1);
-    const float cost = (float)((n - 1) / kCus + 1) * kTiles[i].cost;
-    if (i == first || cost < least) {
-      best = i;
-      least = cost;
-    }
-  }
-  return best;
-}
 
 template <bool BF16, int WM, int WN, int TM, int TN, int RING, int KG>
 static void gemm_tile(const Fp8Args& a, hipStream_t s) {
@@ -430,7 +386,7 @@ static void gemm_tile(const Fp8Args& a, hipStream_t s) {
 
 template <bool BF16>
 static void gemm(const Fp8Args& a, hipStream_t s) {
-  switch (choose_tile(a.T, a.N, BF16 ? 0 : 1)) {
+  switch (choose_tile(kTiles, a.T, a.N, BF16 ? 0 : 1)) {
     case 0:
       if constexpr (BF16) return gemm_tile<BF16, 2, 4, 2, 2, 3, 1>(a, s);
     case 1: return gemm_tile<BF16, 2, 4, 2, 1, 4, 1>(a, s);

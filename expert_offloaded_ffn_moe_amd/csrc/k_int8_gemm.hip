@@ -30,11 +30,10 @@
 #include <type_traits>
 
 #include "int8_out.h"
+#include "tiles.h"
 
 namespace moe {
 namespace {
-
-typedef __attribute__((address_space(3))) void lvoid;
 
 // Place of row r's piece p: p ^ swizzle(r). A 16-byte read serves sixteen lanes at once, lanes
 // 0-3, 12-15, 20-23 and 24-27 of each half wave and then the others: of 64-byte rows those
@@ -48,29 +47,6 @@ __device__ __forceinline__ int swizzle(int r) {
 
 // what pieces past K are read from
 __device__ const i32x4 zero_piece = {0, 0, 0, 0};
-
-// Workgroups are dealt to the 8 XCDs round-robin; each XCD gets one contiguous range of
-// the tiles, so that the tiles of its L2 share rows and channels.
-__device__ __forceinline__ int xcd_order(int b, int nb) {
-  constexpr int kXcd = 8;
-  const int per = nb / kXcd, rem = nb % kXcd, x = b % kXcd, i = b / kXcd;
-  return x < rem ? x * (per + 1) + i : rem * (per + 1) + (x - rem) * per + i;
-}
-
-// All but the newest N of this wave's loads are in, every LDS read too, and so it is for every
-// wave of the workgroup. One block: what follows reads LDS that other waves' loads wrote.
-template <int N>
-__device__ __forceinline__ void meet_with_loads_but() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
-}
-
-// 16 bytes from each lane's address to LDS at `to` + 16 lane. Written as one block, so that
-// the compiler, which cannot tell the ring's buffers apart, adds no wait for it before the
-// LDS reads of the others: meet_with_loads_but counts these loads instead. It has no output
-// register. (A write of M0 is followed by one wait state before its use.)
-__device__ __forceinline__ void load_to_lds(const int8_t* from, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory", "m0");
-}
 
 // PASSES rows, ROWS apart, of four channels each, from their sums in LDS. WHOLE: every row
 // and channel is one of the matrix's, and what the rows need is loaded for all of them
@@ -336,27 +312,8 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_int8_gemm(Int8Args a, int m
 // four groups of waves take the steps in turn (64 x 64 in one group: 18.3 us for 128 x 7168;
 // 64 x 32 11.3 and 64 x 64 13.2 us for 128 x 4096; 32 x 32 8.4, 64 x 32 9.1 and 64 x 64 11.1
 // us for 64 x 4096). 257 to 384 tokens run as 384 rows, on 160 to 168 CUs of the larger shapes.
-struct Tile {
-  int tokens, channels;
-  float cost;
-};
-constexpr int kCus = 256;
 constexpr Tile kTiles[] = {{256, 256, 1.65f}, {128, 256, 0.88f}, {128, 128, 0.53f}, {64, 128, 0.35f},
                           {64, 64, 0.25f},   {64, 32, 0.20f},   {32, 32, 0.16f}};
-
-static int choose_tile(int64_t T, int64_t channels) {
-  int best = 0;
-  float least = 0.f;
-  for (int i = 0; i < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++i) {
-    const int64_t n = ((T - 1) / kTiles[i].tokens + 1) * ((channels - 1) / kTiles[i].channels + 1);
-    const float cost = (float)((n - 1) / kCus + 1) * kTiles[i].cost;
-    if (i == 0 || cost < least) {
-      best = i;
-      least = cost;
-    }
-  }
-  return best;
-}
 
 template <bool GATED, bool BF16, int WM, int WN, int TM, int TN, int BK, int RING, int KG>
 static void gemm_tile(const Int8Args& a, hipStream_t s) {
@@ -366,7 +323,7 @@ static void gemm_tile(const Int8Args& a, hipStream_t s) {
 
 template <bool GATED, bool BF16>
 static void gemm(const Int8Args& a, hipStream_t s) {
-  switch (choose_tile(a.T, GATED ? 2 * (int64_t)a.N : a.N)) {
+  switch (choose_tile(kTiles, a.T, GATED ? 2 * (int64_t)a.N : a.N)) {
     case 0: return gemm_tile<GATED, BF16, 2, 4, 4, 2, 64, 4, 1>(a, s);
     case 1: return gemm_tile<GATED, BF16, 2, 4, 2, 2, 128, 3, 1>(a, s);
     case 2: return gemm_tile<GATED, BF16, 2, 4, 2, 1, 128, 4, 1>(a, s);
