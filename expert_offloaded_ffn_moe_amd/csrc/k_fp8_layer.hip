@@ -337,6 +337,7 @@ __device__ __forceinline__ void route(const Fp8LayerArgs& a, Route& r, bool writ
 
 constexpr int kWaves = 8;  // of a workgroup, taking blocks of 128 of K in turn
 constexpr int kRows = 8;   // of weights in an operand
+constexpr int kCus = 256;
 
 // Vectors: 8 tokens of one term, or 2 tokens of three (vector 3 c + k is token c's term k).
 template <int TERMS>
@@ -701,10 +702,11 @@ void layer(const Fp8LayerArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((k_f8_gate_up<kTerms, 2>), grid, dim3(64 * kWaves), 0, s, a);
   else
     hipLaunchKernelGGL((k_f8_gate_up<kTerms, 3>), grid, dim3(64 * kWaves), 0, s, a);
-  // Workgroups of 16 rows leave CUs idle while there are at most 256 of them; 8 rows and twice the waves then
-  // take 18.8 us for a token on 2048 / 768 (16 rows: 20.4), 72 for 16 tokens (80). Above, 16 rows read each
-  // vector half as often: a token on 7168 / 2048 61 us (8 rows: 80), 16 tokens 385 (461).
-  if (a.H / 16 <= 256)
+  // 8 rows and twice the waves a workgroup, which takes a CU to itself, while one round of the CUs holds them:
+  // H = 2048 17.5 us for a token and 66 for 16 (8 of 64 experts, I = 768; 16 rows: 18.2 and 74). Above, two
+  // workgroups of 16 rows a CU, which read each vector half as often: H = 2064 19.4 and 82 (8 rows: 21.9 and
+  // 94), 4096 27 and 97 (30 and 111), 7168 39 and 172 (47 and 198).
+  if (a.H / kRows <= kCus)
     down<ACT, 16, 1>(a, s);
   else
     down<ACT, 8, 2>(a, s);
