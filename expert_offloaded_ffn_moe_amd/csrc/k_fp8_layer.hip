@@ -674,11 +674,15 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_f8_down(Fp8LayerArgs a, DownS
 template <typename ACT, int WAVES, int OPS>
 void down(const Fp8LayerArgs& a, hipStream_t s) {
   const int IB = f8_blocks(a.I), n = a.T * a.k;
-  // as many parts of K as divide its blocks with little left over: the fewer tiles have to be at
-  // hand for every wave to have work
+  // K in two parts from 4 blocks on and in four from 16, where that leaves a wave at most an eighth of its steps
+  // without a block: fewer tiles then have to be at hand for every wave to have work, but the sums of more parts
+  // meet in LDS. A token (16 tokens) on H = 2048, in 1 / 2 / 4 / 8 parts, us: I = 256 13.8 / 14.5 / 15.1 / - (30.3 /
+  // 31.2 / 38.0), 512 13.0 / 12.8 / 13.6 / 14.1 (32.4 / 33.2 / 34.2 / 40.4), 768 17.8 / 17.3 / 18.7 / 19.9 (57.0 / 57.6 /
+  // 63.8 / 67.6), 2048 18.9 / 18.6 / 18.7 / 19.1 (76.7 / 77.2 / 78.2 / 78.9), 4096 20.2 / 18.5 / 18.2 / 18.3 (76.0 / 75.6 /
+  // 76.8 / 77.5); as many parts as waves 20.1 (81.4) on 2048.
   int ks = 1;
-  for (int p = 2; p <= WAVES && p <= IB; p *= 2)
-    if ((IB + p - 1) / p * p * 7 <= IB * 8) ks = p;
+  for (int p : {2, 4})
+    if (IB >= p * p && (IB + p - 1) / p * p * 7 <= IB * 8) ks = p;
   constexpr int kRoom = WAVES == 8 ? 48 << 10 : 96 << 10;  // LDS for the sums: two workgroups a CU, or one
   const int place = kRows * OPS * (int)sizeof(float), room = kRoom / (ks * place);
   DownShape d;
