@@ -370,12 +370,16 @@ __global__ __launch_bounds__(64 * WM* WN* KG) void k_fp8_gemm(Fp8Args a, int mti
 
 }  // namespace
 
-// The tiles, and what a block of K costs a CU in each (us), measured on products of 17 to 2048 tokens
+// The tiles, and what a block of K costs a CU in each (us), measured on bf16 products of 17 to 2048 tokens
 // with 1001 to 7168 channels and K = 2048 to 7168. A large tile reads the fewest bytes per product, but
 // too few of them leave CUs idle: the tile whose rounds over the 256 CUs cost least is taken. Against
-// the next best tile that gives, at K = 7168 in a loop over one set of buffers: 2048 x 7168 138 us
-// (128 x 128: 182), 1024 x 7168 58 (128 x 128: 79), 512 x 7168 39 (64 x 128: 51), 256 x 7168 25.5 (64 x 64:
-// 30.6), 128 x 7168 16.7 (64 x 128: 24.1), 64 x 7168 14.0 (64 x 64: 16.1), 32 x 7168 11.9 (64 x 32: 12.5).
+// the next best tile that gives, at K = 7168 in a loop over one set of buffers: 2048 x 7168 121 us
+// (128 x 128: 160), 1024 x 7168 60 (128 x 128: 80), 512 x 7168 38 (64 x 128: 51), 256 x 7168 25.5 (64 x 64:
+// 31), 128 x 7168 17.0 (64 x 128: 24.6), 64 x 7168 14.6 (64 x 64: 16.8), 16 x 7168 11.9 (64 x 32: 12.9).
+// fp32 products cost more a block, in the same proportions: 2048 x 7168 253 us (64 x 128: 284), 1024 x
+// 7168 127 (156), 512 x 7168 65 (64 x 128: 81), 256 x 7168 43 (64 x 64: 45), 128 x 7168 24 (64 x 32: 30), 64 x
+// 7168 16.6 (32 x 32: 22), 16 x 7168 12.8 (64 x 32: 16.3). Over these and 1001 x 2064, 2048 x 2048, 4096 x
+// 7168 and 5120 x 4096 channels x K, 16 to 2048 tokens, no tile beats the chosen one by 2% in either type.
 constexpr Tile kTiles[] = {{128, 256, 0.93f}, {128, 128, 0.66f}, {64, 128, 0.43f}, {64, 64, 0.29f}, {64, 32, 0.235f}, {32, 32, 0.18f}};
 
 template <bool BF16, int WM, int WN, int TM, int TN, int RING, int KG>

@@ -212,6 +212,9 @@ __device__ __forceinline__ void choose_of(const float* logits, int E, int k, int
   rank = 0;
   for (int j = 0; j < k; ++j) rank += (some >> j & 1) && __builtin_amdgcn_readlane(id, j) < id;
 }
+// A lane's experts are searched whether they are there or not, in every round: 128 experts in the form for 128
+// a token's layer of 2048 / 256 14.9 us (for 384: 15.7, for 1024: 17.7), 16 tokens' 38.3 (39.9, 44.2); 256 in that for
+// 384 16.5 and 41.9 (for 1024: 18.4, 46.1).
 __device__ __forceinline__ void choose(const float* logits, int E, int k, int& id, float& w, int& rank) {
   const int nv = (E + 63) / 64;
   if (nv <= 2)
@@ -698,8 +701,11 @@ void layer(const Fp8LayerArgs& a, hipStream_t s) {
   constexpr int kTerms = sizeof(ACT) == 2 ? 1 : 3;
   const int rows = a.logits_in ? 0 : a.E;
   hipLaunchKernelGGL((k_f8_router<ACT>), dim3(rows + a.T), dim3(kRouterThreads), 0, s, a, rows);
-  const int per = a.I / 16, most = a.T * a.k;  // blocks of rows; tiles
-  const dim3 grid(per, std::min(most, std::max(1, 512 / per)));
+  // blocks of rows; tiles, shared by as many workgroups as the CUs hold at two each: 16 tokens on 2048 / 768, 8 of
+  // 128 experts, 71.5 us (one each: 70.6, four: 75.6, half as many as CUs: 95.7), 64 tokens 183 (183, 197, 245), 16 on
+  // 7168 / 2048 341 (336, 339, 417), on 4096 / 256 55.7 (55.1, 61.1, 61.0), 40 on 1024 / 4096 185 (187, 194, 187)
+  const int per = a.I / 16, most = a.T * a.k;
+  const dim3 grid(per, std::min(most, std::max(1, 2 * kCus / per)));
   // Where no wave has more than two blocks of K, two under way: the third would be loaded for nothing (a token
   // on 2048 / 768 18.8 us, 19.8 with three; 7 tokens on 400 / 208 15.7, 16.1).
   if (f8_blocks(a.H) <= 2 * kWaves && (int)grid.y == most)
