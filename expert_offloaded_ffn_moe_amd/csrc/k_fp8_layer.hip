@@ -14,9 +14,11 @@
 // (2.5 us for one token), instead of a launch of its own; one leaves them for the second half.
 //
 // What bounds it: a token on 6 experts of 7168 / 2048 (264 MB) takes 61 us, of which gate and up
-// 31 (5.7 TB/s), down 18.7 (4.7), the router 6; a token on 8 of 2048 / 768 (38 MB) 18 us, of which
-// 3 + 9 + 6: there the starts of three short bursts count, not the bytes (7.5 us).
-// 16 tokens take 72 us on 2048 / 768 and 346 to 384 on 7168 / 2048 (4.2 to 5.2 TB/s).
+// 32 (5.6 TB/s), down 18 (4.9), the router 6; a token on 8 of 2048 / 768 (38 MB) 19 us, of which
+// 3 + 9 + 6: there the starts of three short bursts count, not the bytes (7.5 us). 16 tokens take 72 us on
+// 2048 / 768 (48 experts: gate and up 4.0 TB/s, down 2.6) and 382 on 7168 / 2048 (37: 5.5, 3.5). 64 tokens on one
+// expert of 2048 / 768 take 44: the router, with a workgroup for each expert, 18, down, which loads the weights
+// again for every two tokens, 13.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -409,9 +411,12 @@ __device__ __forceinline__ Fp8Tile uniform(const Fp8Tile* tile) {
 // its items are one sequence, of which it has kAhead under way. A turn but the last loads as
 // many, past the end the last tile's again: a load that a branch leaves out would make every
 // wait one for all loads.
-template <int TERMS, int kAhead>
+template <int TERMS>
 __global__ __launch_bounds__(64 * kWaves, 4) void k_f8_gate_up(Fp8LayerArgs a) {
   typedef Vectors<TERMS> Vec;
+  // With three, a token on 2048 / 768 takes 18.7 us (17.7), on 4096 / 768 27.8 (26.5), on 7168 / 2048 55.1 (54.2), 16 tokens
+  // 73.9 (72.8), 98.2 (96.9) and 355 (356); the most that a third wins is 3%, a token on 2560 / 2048 21.8 (22.5).
+  constexpr int kAhead = 2;
   __shared__ Route r;
   __shared__ float part[2][kWaves][4][2][64];  // [turn][wave][operand][row of the lane's two][lane]
   route<Vec::kTokens>(a, r, blockIdx.x + blockIdx.y == 0);
@@ -706,12 +711,7 @@ void layer(const Fp8LayerArgs& a, hipStream_t s) {
   // 7168 / 2048 341 (336, 339, 417), on 4096 / 256 55.7 (55.1, 61.1, 61.0), 40 on 1024 / 4096 185 (187, 194, 187)
   const int per = a.I / 16, most = a.T * a.k;
   const dim3 grid(per, std::min(most, std::max(1, 2 * kCus / per)));
-  // Where no wave has more than two blocks of K, two under way: the third would be loaded for nothing (a token
-  // on 2048 / 768 18.8 us, 19.8 with three; 7 tokens on 400 / 208 15.7, 16.1).
-  if (f8_blocks(a.H) <= 2 * kWaves && (int)grid.y == most)
-    hipLaunchKernelGGL((k_f8_gate_up<kTerms, 2>), grid, dim3(64 * kWaves), 0, s, a);
-  else
-    hipLaunchKernelGGL((k_f8_gate_up<kTerms, 3>), grid, dim3(64 * kWaves), 0, s, a);
+  hipLaunchKernelGGL((k_f8_gate_up<kTerms>), grid, dim3(64 * kWaves), 0, s, a);
   // 8 rows and twice the waves a workgroup, which takes a CU to itself, while one round of the CUs holds them:
   // H = 2048 17.5 us for a token and 66 for 16 (8 of 64 experts, I = 768; 16 rows: 18.2 and 74). Above, two
   // workgroups of 16 rows a CU, which read each vector half as often: H = 2064 19.4 and 82 (8 rows: 21.9 and
