@@ -8,7 +8,7 @@
 // the wave's with both scales, in fp32.
 //
 // Bound: the weights' bytes, which go from memory to registers with 16-byte loads: one token on 7168 x
-// 7168 10.9 us (4.7 TB/s) with all inputs from HBM, on 4096 x 7168 7.3. Scales are multiplied into LDS
+// 7168 11.0 us (4.7 TB/s) with all inputs from HBM, on 4096 x 7168 7.5. Scales are multiplied into LDS
 // first: loaded with each block, they took two of its five loads (12.7 us).
 #include <hip/hip_runtime.h>
 
@@ -21,9 +21,9 @@ namespace moe {
 namespace {
 
 // Tokens up to which this kernel runs, on any weights, so that how exact a token's sums are turns on the
-// number of tokens alone: 8 on 4096 x 7168 9.0 us (fp32 tiles 11.1), on 7168 x 7168 12.9 (13.0), on 2048 x
-// 2048 5.3 (5.9), on 14336 x 4096 17.7 (16.4); bf16 tiles, whose products are cut, take 9.1, 12.4, 5.4 and
-// 14.9.
+// number of tokens alone: 8 on 4096 x 7168 10.4 us (fp32 tiles 12.3), on 7168 x 7168 12.9 (13.0), on 2048 x
+// 2048 6.0 (6.6), on 14336 x 4096 17.8 (16.6); bf16 tiles, whose products are cut, take 11.4, 12.4, 6.1 and
+// 15.2.
 constexpr int kSkinnyRows = 8;
 constexpr int kWaves = 8;  // of a workgroup, splitting K
 

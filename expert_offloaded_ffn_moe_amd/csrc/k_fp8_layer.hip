@@ -14,10 +14,10 @@
 // (2.5 us for one token), instead of a launch of its own; one leaves them for the second half.
 //
 // What bounds it: a token on 6 experts of 7168 / 2048 (264 MB) takes 61 us, of which gate and up
-// 32 (5.6 TB/s), down 18 (4.9), the router 6; a token on 8 of 2048 / 768 (38 MB) 19 us, of which
-// 3 + 9 + 6: there the starts of three short bursts count, not the bytes (7.5 us). 16 tokens take 72 us on
-// 2048 / 768 (48 experts: gate and up 4.0 TB/s, down 2.6) and 382 on 7168 / 2048 (37: 5.5, 3.5). 64 tokens on one
-// expert of 2048 / 768 take 44: the router, with a workgroup for each expert, 18, down, which loads the weights
+// 31 (5.7 TB/s), down 18 (4.9), the router 6; a token on 8 of 2048 / 768 (38 MB) 19 us, of which
+// 3 + 9 + 6: there the starts of three short bursts count, not the bytes (7.5 us). 16 tokens take 71 us on
+// 2048 / 768 (48 experts: gate and up 4.2 TB/s, down 2.6) and 382 on 7168 / 2048 (37: 5.5, 3.5). 64 tokens on one
+// expert of 2048 / 768 take 42: the router, with a workgroup for each expert, 18, down, which loads the weights
 // again for every two tokens, 13.
 #include <hip/hip_runtime.h>
 
