@@ -633,8 +633,8 @@ moe_status moe_fp8_matmul(const moe_fp8_matmul_args* args, moe_stream stream);
  * with each weight its code times its block's scale, all sums in fp32 and the
  * intermediate kept in fp32. A logit of -infinity keeps its expert from counting: it has
  * weight 0 and is not computed, also where fewer than k others are left, and a token
- * whose logits are all -infinity has weights and y 0. Nothing of a token reaches another
- * token's outputs, which have the same bits in any batch. Experts that no token chose
+ * whose logits are all -infinity has weights and y 0. Nor is an expert computed whose weight
+ * underflows to 0. Nothing of a token reaches another token's outputs, which have the same bits in any batch. Experts that no token chose
  * are not read. The workspace holds what moe_fp8_layer_workspace says, 256-byte aligned;
  * its contents need not be kept or set, and calls that overlap in time need one each. */
 typedef struct {
